@@ -1,6 +1,7 @@
 /*
  * moe_mi355x.h -- C ABI of the routed mixture-of-experts expert-FFN hot path
- * for AMD Instinct MI355X (gfx950).
+ * and of the paged key-value cache and attention beside it, for AMD Instinct
+ * MI355X (gfx950).
  *
  * Pages cited by title and section:
  *   [GATE-PR]  "Enable and fuse the Inkling MoE gate epilogue on Intel XPU"
@@ -27,7 +28,7 @@
  *   - Host-detectable problems return a negative moe_status and enqueue
  *     nothing. Launch failures return MOE_ERR_HIP (moe_last_error() has the
  *     HIP message). Data-dependent problems found on the device (a routing
- *     id outside [0, num_experts_global)) OR a MOE_DEVERR_* bit into a
+ *     id outside [0, num_experts_global), a cache page that is not there) OR a MOE_DEVERR_* bit into a
  *     caller-owned int32 `err_word` (the caller zeroes it), skip the bad
  *     pair and leave every valid pair unaffected.
  *   - Row-major layouts; a "[G][N][K]" weight is G matrices of N output rows
@@ -389,6 +390,196 @@ int moe_forward_no_workspace(const moe_layer *layer, const void *x_bf16,
 /* Message of the calling thread's last moe_forward_no_workspace refusal
  * ("" if none). */
 const char *moe_scratch_error(void);
+
+/* ------------------------------------------------------- key-value cache -- */
+/* The other half of a decoder layer in serving: attention over a paged
+ * key-value cache, the writing of new keys and values into it and the upkeep
+ * of its pages. These follow from the formulas stated here (no page of the
+ * sources above covers them).
+ *
+ * One layer's cache is two arrays of pages, K and V, of n_pages pages of
+ * page_size tokens of n_heads key-value heads of head_dim values; value d of
+ * head h of token i of page p lies at element
+ *   p * stride_page + h * stride_head + i * stride_tok + d,
+ * so both [page][head][token][d] and [page][token][head][d] are expressed.
+ * Pages of several sequences are found through one moe_kv_table for all
+ * layers: token j of slot s is token j % page_size of page
+ * table[s * ld + j / page_size]; an entry outside [0, n_pages) (by
+ * convention -1) holds no page. len[s] is the number of tokens of slot s,
+ * the newest included. refs[p] counts the table entries that name page p;
+ * pages with refs 0 are free. */
+typedef enum {
+  MOE_KV_BF16 = 0,
+  MOE_KV_F16 = 1,
+  MOE_KV_E4M3 = 2      /* OCP e4m3fn codes; value = code * scale[head] */
+} moe_kv_fmt;
+
+typedef struct {
+  int fmt;             /* moe_kv_fmt */
+  int n_pages;         /* >= 1 */
+  int page_size;       /* a multiple of 16, 16..4096 */
+  int n_heads;         /* key-value heads, 1..1024 */
+  int head_dim;        /* 64, 128 or 256 */
+  long stride_page, stride_head, stride_tok;   /* elements; multiples of 16
+                          bytes, at least head_dim; stride_tok * 16 elements
+                          under 2^30 bytes */
+  void *k, *v;         /* 16-byte aligned */
+  const float *k_scale, *v_scale;   /* device fp32 [n_heads]; MOE_KV_E4M3
+                          only (NULL otherwise) */
+} moe_kv_cache;
+
+typedef struct {
+  int n_slots;         /* rows of table, entries of len */
+  int max_pages;       /* entries of a row; max_pages * page_size <= 2^28 */
+  long ld;             /* row stride of table, >= max_pages */
+  int n_pages;         /* as the cache's */
+  int page_size;       /* as the cache's */
+  int *table;          /* int32 [n_slots][ld] */
+  int *len;            /* int32 [n_slots], 0..max_pages * page_size (what
+                          lies outside is taken as the nearest bound) */
+  int *refs;           /* int32 [n_pages]; NULL for attention and append,
+                          which do not use it; never touched concurrently by
+                          two calls */
+} moe_kv_table;
+
+/* err_word bits of the calls below (the word is required; moe_read_device_error
+ * reads it) */
+#define MOE_DEVERR_CACHE_PAGE 0x8  /* a token that a call reads or writes has no
+                                      page, or a slot index is >= n_slots (that
+                                      token is taken as masked, or not written;
+                                      that slot as empty) */
+#define MOE_DEVERR_CACHE_FULL 0x10 /* grow or fork: not enough free pages or
+                                      table entries for a slot, left as it was */
+#define MOE_DEVERR_CACHE_BUSY 0x20 /* fork into a slot that holds tokens, left
+                                      as it was */
+
+/* Queries, outputs and mask of an attention call. Row r of q belongs to
+ * position p of its sequence (see the entry points), query head h to
+ * key-value head h / (n_heads / cache->n_heads). Key j is visible iff
+ *   j <= p and (window == 0 or p - j < window or j < n_first):
+ * causal, optionally within a sliding window of the last `window` keys, of
+ * which the first n_first keys of the sequence stay visible. With
+ * s_j = scale * sum_d q[d] K_j[d] over the visible keys,
+ *   out = sum_j exp(s_j - lse) V_j,  lse = log sum_j exp(s_j);
+ * a row that sees no key (or only scores of -infinity) gets out = 0 and
+ * lse = -infinity. What lies in masked places, infinities and NaN included,
+ * does not enter. Products accumulate in fp32, the softmax statistics are
+ * fp32; the probabilities enter the second product in the type of q. */
+typedef struct {
+  int fmt;             /* MOE_KV_BF16 or MOE_KV_F16: q and out; a cache that
+                          is not MOE_KV_E4M3 has the same fmt */
+  int n_heads;         /* a multiple of cache->n_heads, at most 64 times it */
+  const void *q;       /* [rows][n_heads][head_dim], 16-byte aligned */
+  long q_stride_row, q_stride_head;       /* elements, multiples of 8 */
+  void *out;           /* as q */
+  long out_stride_row, out_stride_head;
+  float *lse;          /* fp32 [rows][n_heads], dense, or NULL */
+  float scale;         /* finite */
+  int window;          /* >= 0; 0: no window */
+  int n_first;         /* >= 0; used with a window */
+} moe_attn;
+
+/* Attention of one new token per sequence: row i of q is the token at
+ * position len[s] - 1 of slot s = slots[i] (slots NULL: s = i). A negative
+ * slots[i] is a row without a sequence (out 0, lse -infinity), so a batch of
+ * fixed size can be captured once and run partly filled. The visible keys of
+ * all sequences and key-value heads are split evenly over the GPU, whatever
+ * the lengths, and the parts of one sequence joined in a fixed order (a
+ * second launch): results do not depend on timing. No length is read on the
+ * host. Limits: 0 <= n < 2^20. Workspace:
+ * moe_attn_decode_workspace_size(cache, n, n_heads) bytes (0 for invalid
+ * arguments). Errors: NULL, SHAPE, FORMAT (fmt), PARAM (alignment, scale,
+ * window, scales of a cache that takes none), WORKSPACE, HIP. */
+int moe_attn_decode(const moe_kv_cache *cache, const moe_kv_table *table,
+                    const int *slots, long n, const moe_attn *attn,
+                    int *err_word, void *ws, size_t ws_bytes, void *stream);
+size_t moe_attn_decode_workspace_size(const moe_kv_cache *cache, long n,
+                                      int n_heads);
+
+/* Attention of the newest tokens of n sequences: rows cu_q[i] ..
+ * cu_q[i + 1] - 1 of q (device int32 [n + 1], ascending from 0 to T) are the
+ * last m = cu_q[i + 1] - cu_q[i] tokens of slot s = slots[i] (NULL: s = i),
+ * row cu_q[i] + t at position len[s] - m + t. A whole prompt (m = len) or the
+ * next chunk of one; its keys and values are in the cache already
+ * (moe_cache_append). Rows with a negative slots[i] or position give 0 and
+ * -infinity. T = rows of q (< 2^31 / n_heads). Workspace:
+ * moe_attn_prefill_workspace_size(cache, n, T, n_heads) bytes. Errors
+ * as for moe_attn_decode. */
+int moe_attn_prefill(const moe_kv_cache *cache, const moe_kv_table *table,
+                     const int *slots, long n, const int *cu_q, long T,
+                     const moe_attn *attn, int *err_word, void *ws,
+                     size_t ws_bytes, void *stream);
+size_t moe_attn_prefill_workspace_size(const moe_kv_cache *cache, long n,
+                                       long T, int n_heads);
+
+/* Writes new keys and values: rows cu[i] .. cu[i + 1] - 1 of k and v (device
+ * int32 [n + 1]; NULL: one row each, T = n) go to positions start[i],
+ * start[i] + 1, ... of slot slots[i] (NULL: i). Nothing is written for a
+ * negative start[i] or slots[i]. k and v: [T][n_heads][head_dim] of type fmt
+ * (MOE_KV_BF16 or MOE_KV_F16; the cache's own unless that is MOE_KV_E4M3),
+ * 16-byte aligned, strides in elements, multiples of 8. Into a MOE_KV_E4M3
+ * cache: code = e4m3fn(round-to-nearest-even(x / scale[head])), the fp32
+ * quotient saturated to +-448 (NaN: 0x7F). Positions of different rows must
+ * differ. */
+int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
+                     const int *slots, const int *start, const int *cu, long n,
+                     long T, int fmt, const void *k, long k_stride_row,
+                     long k_stride_head, const void *v, long v_stride_row,
+                     long v_stride_head, int *err_word, void *stream);
+
+/* Upkeep of the pages. The slots of one call are distinct and valid. One
+ * call's table is not used by another stream meanwhile. Pages are taken
+ * lowest index first, in the order of the list: results do not depend on
+ * timing.
+ *
+ * moe_cache_grow makes room for n_new[i] >= 0 more tokens of slots[i] (NULL:
+ * i) and counts them in: start[i] = len, len += n_new[i], with new pages
+ * where page_size * (entries held) is short. A slot is left as it was, with
+ * start[i] = -1 and MOE_DEVERR_CACHE_FULL, if its table row is too short or
+ * if the slots up to it in the list whose rows suffice need more pages in all
+ * than are free.
+ *
+ * moe_cache_free gives the slots' pages back (refs - 1 each, entries -1,
+ * len 0). moe_cache_trim gives back the pages whose tokens j all have
+ * n_first <= j < len - window (no query from position len - 1 on sees them),
+ * entries -1, len unchanged.
+ *
+ * moe_cache_fork makes dst[i], an empty slot, a copy of src[i]: whole pages
+ * are shared (refs + 1), a partly filled last page is copied into a free
+ * page, in every layer, since both go on writing there. dst entries are
+ * distinct and none of them a src. If no page is free, dst[i] stays empty,
+ * with MOE_DEVERR_CACHE_FULL.
+ *
+ * moe_cache_compact moves pages, in every layer, so that the pages in use
+ * are the first ones: with U pages in use, the i-th of those at index >= U
+ * moves to the i-th free page below U; refs and every table entry follow.
+ * n_used[0] = U (device int32, NULL allowed).
+ *
+ * moe_cache_copy_pages copies page src[i] to page dst[i], in every layer;
+ * entries < 0 are skipped, entries >= n_pages too, with
+ * MOE_DEVERR_CACHE_PAGE. No dst occurs twice or is also a src.
+ *
+ * layers: host array of n_layers (1..1024) caches alike in all but their
+ * pointers and scales. Workspace: moe_cache_workspace_size(table, n) bytes
+ * serves grow, fork and compact for up to n slots. */
+int moe_cache_grow(const moe_kv_table *table, const int *slots,
+                   const int *n_new, long n, int *start, int *err_word,
+                   void *ws, size_t ws_bytes, void *stream);
+int moe_cache_free(const moe_kv_table *table, const int *slots, long n,
+                   int *err_word, void *stream);
+int moe_cache_trim(const moe_kv_table *table, const int *slots, long n,
+                   int window, int n_first, int *err_word, void *stream);
+int moe_cache_fork(const moe_kv_cache *layers, int n_layers,
+                   const moe_kv_table *table, const int *src, const int *dst,
+                   long n, int *err_word, void *ws, size_t ws_bytes,
+                   void *stream);
+int moe_cache_compact(const moe_kv_cache *layers, int n_layers,
+                      const moe_kv_table *table, int *n_used, int *err_word,
+                      void *ws, size_t ws_bytes, void *stream);
+int moe_cache_copy_pages(const moe_kv_cache *layers, int n_layers,
+                         const int *src, const int *dst, long n, int *err_word,
+                         void *stream);
+size_t moe_cache_workspace_size(const moe_kv_table *table, long n);
 
 /* --------------------------------------------------------------- misc -- */
 /* Synchronises `stream`, then copies *err_word (device) to *host_bits. */

@@ -1,11 +1,12 @@
 """Python binding of libmoe_mi355x.so: the routed MoE expert-FFN hot path
-on MI355X (gfx950).
+and the paged key-value cache and attention beside it, on MI355X (gfx950).
 
 Argument marshalling only. Every step of the path runs in the library's HIP
 kernels; torch supplies device memory (tensors) and the current stream. The
 functions carry the C names (moe_route, moe_permute, moe_quantize_act_fp8,
 moe_quantize_act_mxfp8,
-moe_grouped_gemm1_act, moe_grouped_gemm2_combine, moe_forward, ...), take
+moe_grouped_gemm1_act, moe_grouped_gemm2_combine, moe_forward,
+moe_attn_decode, moe_attn_prefill, moe_cache_append, ...), take
 torch tensors for the arrays, and raise MoeError on a negative status.
 There is no fallback: without the built library every call raises.
 """
@@ -29,6 +30,10 @@ _PACKED4 = (MOE_W_INT4_G32, MOE_W_NVFP4, MOE_W_MXFP4, MOE_W_MXFP4_A8)
 MOE_DEVERR_GLOBAL_ID_OOB = 0x1
 MOE_DEVERR_F16_RANGE = 0x2
 MOE_DEVERR_W4_SCALE = 0x4
+MOE_DEVERR_CACHE_PAGE = 0x8
+MOE_DEVERR_CACHE_FULL = 0x10
+MOE_DEVERR_CACHE_BUSY = 0x20
+MOE_KV_BF16, MOE_KV_F16, MOE_KV_E4M3 = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE",
           -3: "MOE_ERR_FORMAT", -4: "MOE_ERR_LOCAL_RANGE", -5: "MOE_ERR_PARAM",
           -6: "MOE_ERR_WORKSPACE", -8: "MOE_ERR_HIP", -9: "MOE_ERR_SCRATCH"}
@@ -64,6 +69,27 @@ class MoeLayer(ctypes.Structure):
                 ("shared_w", c_float), ("w13", MoeWeights), ("w2", MoeWeights),
                 ("act", MoeActParams), ("lora", POINTER(MoeLora)),
                 ("lora_down", POINTER(MoeLora))]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("fmt", c_int), ("n_pages", c_int), ("page_size", c_int),
+                ("n_heads", c_int), ("head_dim", c_int), ("stride_page", c_long),
+                ("stride_head", c_long), ("stride_tok", c_long), ("k", c_void_p),
+                ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class MoeKvTable(ctypes.Structure):
+    _fields_ = [("n_slots", c_int), ("max_pages", c_int), ("ld", c_long),
+                ("n_pages", c_int), ("page_size", c_int), ("table", c_void_p),
+                ("len", c_void_p), ("refs", c_void_p)]
+
+
+class MoeAttn(ctypes.Structure):
+    _fields_ = [("fmt", c_int), ("n_heads", c_int), ("q", c_void_p),
+                ("q_stride_row", c_long), ("q_stride_head", c_long),
+                ("out", c_void_p), ("out_stride_row", c_long),
+                ("out_stride_head", c_long), ("lse", c_void_p), ("scale", c_float),
+                ("window", c_int), ("n_first", c_int)]
 
 
 _lib = None
@@ -108,6 +134,31 @@ _SIGS = {
                                          c_long, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_void_p]),
     "moe_scratch_error": (ctypes.c_char_p, []),
+    "moe_attn_decode": (c_int, [POINTER(MoeKvCache), POINTER(MoeKvTable), c_void_p, c_long,
+                                POINTER(MoeAttn), c_void_p, c_void_p, c_size_t,
+                                c_void_p]),
+    "moe_attn_decode_workspace_size": (c_size_t, [POINTER(MoeKvCache), c_long, c_int]),
+    "moe_attn_prefill": (c_int, [POINTER(MoeKvCache), POINTER(MoeKvTable), c_void_p, c_long,
+                                 c_void_p, c_long, POINTER(MoeAttn), c_void_p, c_void_p,
+                                 c_size_t, c_void_p]),
+    "moe_attn_prefill_workspace_size": (c_size_t, [POINTER(MoeKvCache), c_long, c_long,
+                                                   c_int]),
+    "moe_cache_append": (c_int, [POINTER(MoeKvCache), POINTER(MoeKvTable), c_void_p,
+                                 c_void_p, c_void_p, c_long, c_long, c_int, c_void_p,
+                                 c_long, c_long, c_void_p, c_long, c_long, c_void_p,
+                                 c_void_p]),
+    "moe_cache_grow": (c_int, [POINTER(MoeKvTable), c_void_p, c_void_p, c_long, c_void_p,
+                               c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_cache_free": (c_int, [POINTER(MoeKvTable), c_void_p, c_long, c_void_p, c_void_p]),
+    "moe_cache_trim": (c_int, [POINTER(MoeKvTable), c_void_p, c_long, c_int, c_int,
+                               c_void_p, c_void_p]),
+    "moe_cache_fork": (c_int, [POINTER(MoeKvCache), c_int, POINTER(MoeKvTable), c_void_p,
+                               c_void_p, c_long, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_cache_compact": (c_int, [POINTER(MoeKvCache), c_int, POINTER(MoeKvTable), c_void_p,
+                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_cache_copy_pages": (c_int, [POINTER(MoeKvCache), c_int, c_void_p, c_void_p, c_long,
+                                     c_void_p, c_void_p]),
+    "moe_cache_workspace_size": (c_size_t, [POINTER(MoeKvTable), c_long]),
     "moe_read_device_error": (c_int, [c_void_p, POINTER(c_int), c_void_p]),
     "moe_status_string": (ctypes.c_char_p, [c_int]),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -320,6 +371,278 @@ def moe_read_device_error(err_word, stream=None) -> int:
     _check(lib().moe_read_device_error(_p(err_word), ctypes.byref(bits),
                                        _stream(stream)), "moe_read_device_error")
     return bits.value
+
+
+# ------------------------------------------------- key-value cache, attention
+
+_KV_FMT = {torch.bfloat16: MOE_KV_BF16, torch.float16: MOE_KV_F16,
+           torch.float8_e4m3fn: MOE_KV_E4M3}
+
+
+def _kv_fmt(t: torch.Tensor, where: str) -> int:
+    if t.dtype not in _KV_FMT:
+        raise MoeError(-3, where, f"dtype {t.dtype}")
+    return _KV_FMT[t.dtype]
+
+
+def _i32(t: Optional[torch.Tensor], n: int, where: str):
+    """Pointer of a contiguous int32 list of at least n entries (or None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise MoeError(-2, where, f"wants {n} contiguous int32, got {t.dtype} "
+                                  f"{tuple(t.shape)}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _bytes(ws: Optional[torch.Tensor]) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def kv_cache(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+             v_scale: Optional[torch.Tensor] = None) -> MoeKvCache:
+    """Descriptor of one layer's cache: k and v [pages][heads][page_size][head_dim]
+    of bfloat16, float16 or float8_e4m3fn (with scales [heads] fp32), of any
+    strides alike in both but with rows of head_dim contiguous; a cache laid
+    out [pages][page_size][heads][head_dim] is passed as its transpose(1, 2)."""
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
+        raise MoeError(-2, "kv_cache", "k and v differ in shape, strides or type")
+    if k.stride(3) != 1:
+        raise MoeError(-2, "kv_cache", "rows of head_dim are not contiguous")
+    for sc in (k_scale, v_scale):
+        if sc is not None and (sc.dtype != torch.float32 or sc.numel() != k.shape[1]
+                               or not sc.is_contiguous()):
+            raise MoeError(-2, "kv_cache", "scales are fp32 [heads]")
+    P, H, ps, D = k.shape
+    c = MoeKvCache(_kv_fmt(k, "kv_cache"), P, ps, H, D, k.stride(0), k.stride(1), k.stride(2),
+                   k.data_ptr(), v.data_ptr(),
+                   None if k_scale is None else k_scale.data_ptr(),
+                   None if v_scale is None else v_scale.data_ptr())
+    c._keep = (k, v, k_scale, v_scale)
+    return c
+
+
+def kv_table(table: torch.Tensor, lens: torch.Tensor, page_size: int, n_pages: int,
+             refs: Optional[torch.Tensor] = None) -> MoeKvTable:
+    """Descriptor of the page tables: table int32 [slots][max_pages], lens int32
+    [slots], refs int32 [n_pages] (for grow, free, trim, fork, compact)."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
+        raise MoeError(-2, "kv_table", "table is int32 [slots][max_pages], rows contiguous")
+    ld = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+    t = MoeKvTable(table.shape[0], table.shape[1], ld, n_pages, page_size, table.data_ptr(),
+                   _i32(lens, table.shape[0], "kv_table").value,
+                   None if refs is None else _i32(refs, n_pages, "kv_table").value)
+    t._keep = (table, lens, refs)
+    return t
+
+
+def _rows(t: torch.Tensor, where: str, rows: int, D: int):
+    """Strides (row, head) of a [rows][heads][head_dim] tensor. A dimension of
+    one entry has no stride of its own."""
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D or t.stride(2) != 1:
+        raise MoeError(-2, where, f"wants [{rows}][heads][{D}] with contiguous rows, got "
+                                  f"{tuple(t.shape)} strides {t.stride()}")
+    head = t.stride(1) if t.shape[1] > 1 else D
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * D), head
+
+
+def _attn(where, cache: MoeKvCache, q, out, scale, window, n_first, lse) -> MoeAttn:
+    T, Hq = q.shape[0], q.shape[1]
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise MoeError(-2, where, "out and q differ in shape or type")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq)
+                            or not lse.is_contiguous()):
+        raise MoeError(-2, where, "lse is fp32 [rows][heads], contiguous")
+    qs, os_ = (_rows(t, where, T, cache.head_dim) for t in (q, out))
+    a = MoeAttn(_kv_fmt(q, where), Hq, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0],
+                os_[1], None if lse is None else lse.data_ptr(), scale, window, n_first)
+    a._keep = (q, out, lse)
+    return a
+
+
+def moe_attn_decode_workspace_size(cache: MoeKvCache, n: int, n_heads: int) -> int:
+    return lib().moe_attn_decode_workspace_size(ctypes.byref(cache), n, n_heads)
+
+
+def moe_attn_decode(cache: MoeKvCache, table: MoeKvTable, q, out, scale, err_word, ws, *,
+                    window=0, n_first=0, slots=None, lse=None, stream=None):
+    """One new token per sequence: q and out [n][heads][head_dim], lse [n][heads]."""
+    where = "moe_attn_decode"
+    a = _attn(where, cache, q, out, scale, window, n_first, lse)
+    n = q.shape[0]
+    _check(lib().moe_attn_decode(ctypes.byref(cache), ctypes.byref(table),
+                                 _i32(slots, n, where), n, ctypes.byref(a), _p(err_word),
+                                 _p(ws), _bytes(ws), _stream(stream)), where)
+
+
+def moe_attn_prefill_workspace_size(cache: MoeKvCache, n: int, T: int, n_heads: int) -> int:
+    return lib().moe_attn_prefill_workspace_size(ctypes.byref(cache), n, T, n_heads)
+
+
+def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, err_word, ws,
+                     *, window=0, n_first=0, slots=None, lse=None, stream=None):
+    """The newest tokens of n = len(cu_q) - 1 sequences: q and out
+    [T][heads][head_dim], lse [T][heads]."""
+    where = "moe_attn_prefill"
+    a = _attn(where, cache, q, out, scale, window, n_first, lse)
+    n = cu_q.numel() - 1
+    _check(lib().moe_attn_prefill(ctypes.byref(cache), ctypes.byref(table),
+                                  _i32(slots, n, where), n, _i32(cu_q, 1, where), q.shape[0],
+                                  ctypes.byref(a), _p(err_word), _p(ws), _bytes(ws),
+                                  _stream(stream)), where)
+
+
+def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_word, *,
+                     slots=None, stream=None):
+    """k and v [T][heads][head_dim] to positions start[i].. of the slots; cu int32
+    [n + 1], or None for one token each."""
+    where = "moe_cache_append"
+    T = k.shape[0]
+    n = T if cu is None else cu.numel() - 1
+    if v.dtype != k.dtype or v.shape != k.shape or (T and k.shape[1] != cache.n_heads):
+        raise MoeError(-2, where, "k and v differ, or their heads from the cache's")
+    ks, vs = (_rows(t, where, T, cache.head_dim) for t in (k, v))
+    _check(lib().moe_cache_append(
+        ctypes.byref(cache), ctypes.byref(table), _i32(slots, n, where),
+        _i32(start, n, where), _i32(cu, 1, where), n, T, _kv_fmt(k, where), _p(k), ks[0],
+        ks[1], _p(v), vs[0], vs[1], _p(err_word), _stream(stream)), where)
+
+
+def moe_cache_workspace_size(table: MoeKvTable, n: int) -> int:
+    return lib().moe_cache_workspace_size(ctypes.byref(table), n)
+
+
+def moe_cache_grow(table: MoeKvTable, slots, n_new, start, err_word, ws, stream=None):
+    where = "moe_cache_grow"
+    n = n_new.numel()
+    _check(lib().moe_cache_grow(ctypes.byref(table), _i32(slots, n, where),
+                                _i32(n_new, n, where), n, _i32(start, n, where),
+                                _p(err_word), _p(ws), _bytes(ws), _stream(stream)), where)
+
+
+def moe_cache_free(table: MoeKvTable, slots, err_word, stream=None):
+    n = slots.numel()
+    _check(lib().moe_cache_free(ctypes.byref(table), _i32(slots, n, "moe_cache_free"), n,
+                                _p(err_word), _stream(stream)), "moe_cache_free")
+
+
+def moe_cache_trim(table: MoeKvTable, slots, window, n_first, err_word, stream=None):
+    n = slots.numel()
+    _check(lib().moe_cache_trim(ctypes.byref(table), _i32(slots, n, "moe_cache_trim"), n,
+                                window, n_first, _p(err_word), _stream(stream)),
+           "moe_cache_trim")
+
+
+def _layers(caches):
+    return (MoeKvCache * len(caches))(*caches)
+
+
+def moe_cache_fork(caches, table: MoeKvTable, src, dst, err_word, ws, stream=None):
+    """caches: the MoeKvCache of every layer."""
+    where = "moe_cache_fork"
+    n = src.numel()
+    _check(lib().moe_cache_fork(_layers(caches), len(caches), ctypes.byref(table),
+                                _i32(src, n, where), _i32(dst, n, where), n, _p(err_word),
+                                _p(ws), _bytes(ws), _stream(stream)), where)
+
+
+def moe_cache_compact(caches, table: MoeKvTable, n_used, err_word, ws, stream=None):
+    where = "moe_cache_compact"
+    _check(lib().moe_cache_compact(_layers(caches), len(caches), ctypes.byref(table),
+                                   _i32(n_used, 1, where), _p(err_word), _p(ws), _bytes(ws),
+                                   _stream(stream)), where)
+
+
+def moe_cache_copy_pages(caches, src, dst, err_word, stream=None):
+    where = "moe_cache_copy_pages"
+    n = src.numel()
+    _check(lib().moe_cache_copy_pages(_layers(caches), len(caches), _i32(src, n, where),
+                                      _i32(dst, n, where), n, _p(err_word),
+                                      _stream(stream)), where)
+
+
+class KvCache:
+    """A paged cache of several layers with its tables: device tensors, their
+    descriptors and one workspace. Slots are handed in as int32 device tensors.
+    Everything is enqueued on `stream` (the current one if None); calls on
+    different streams have to be ordered by the caller, as they share the
+    tables and the workspace. Problems found on the device are ORed into
+    err_word."""
+
+    def __init__(self, *, n_layers, n_pages, page_size, n_heads, head_dim, n_slots, max_pages,
+                 dtype=torch.bfloat16, k_scale=None, v_scale=None, device="cuda"):
+        shape = (n_layers, n_pages, n_heads, page_size, head_dim)
+        self.k = torch.empty(shape, dtype=dtype, device=device)
+        self.v = torch.empty(shape, dtype=dtype, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.full((n_slots, max_pages), -1, **i32)
+        self.lens = torch.zeros(n_slots, **i32)
+        self.refs = torch.zeros(n_pages, **i32)
+        self.err_word = torch.zeros(1, **i32)
+        # scales: [n_layers][n_heads], for float8_e4m3fn
+        self.layers = [kv_cache(self.k[i], self.v[i], None if k_scale is None else k_scale[i],
+                                None if v_scale is None else v_scale[i])
+                       for i in range(n_layers)]
+        self.desc = kv_table(self.table, self.lens, page_size, n_pages, self.refs)
+        self._ws = None
+
+    def _new(self, like, stream):
+        """An empty tensor like `like`, contiguous, of the stream it is used on."""
+        with torch.cuda.stream(stream):
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+    def workspace(self, need, stream=None):
+        if self._ws is None or self._ws.numel() < need:
+            with torch.cuda.stream(stream):
+                self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.k.device)
+        if stream is not None:
+            self._ws.record_stream(stream)
+        return self._ws
+
+    def grow(self, slots, n_new, stream=None):
+        """Room for n_new more tokens of each slot; returns their first positions
+        (-1 where there was none)."""
+        start = self._new(n_new, stream)
+        ws = self.workspace(moe_cache_workspace_size(self.desc, n_new.numel()), stream)
+        moe_cache_grow(self.desc, slots, n_new, start, self.err_word, ws, stream)
+        return start
+
+    def append(self, layer, slots, start, cu, k, v, stream=None):
+        moe_cache_append(self.layers[layer], self.desc, start, cu, k, v, self.err_word,
+                         slots=slots, stream=stream)
+
+    def decode(self, layer, slots, q, scale, out=None, window=0, n_first=0, lse=None,
+               stream=None):
+        out = self._new(q, stream) if out is None else out
+        c = self.layers[layer]
+        ws = self.workspace(moe_attn_decode_workspace_size(c, q.shape[0], q.shape[1]), stream)
+        moe_attn_decode(c, self.desc, q, out, scale, self.err_word, ws, window=window,
+                        n_first=n_first, slots=slots, lse=lse, stream=stream)
+        return out
+
+    def prefill(self, layer, slots, q, cu_q, scale, out=None, window=0, n_first=0, lse=None,
+                stream=None):
+        out = self._new(q, stream) if out is None else out
+        c = self.layers[layer]
+        ws = self.workspace(moe_attn_prefill_workspace_size(c, cu_q.numel() - 1, q.shape[0],
+                                                            q.shape[1]), stream)
+        moe_attn_prefill(c, self.desc, q, cu_q, out, scale, self.err_word, ws, window=window,
+                         n_first=n_first, slots=slots, lse=lse, stream=stream)
+        return out
+
+    def free(self, slots, stream=None):
+        moe_cache_free(self.desc, slots, self.err_word, stream)
+
+    def trim(self, slots, window, n_first=0, stream=None):
+        moe_cache_trim(self.desc, slots, window, n_first, self.err_word, stream)
+
+    def fork(self, src, dst, stream=None):
+        ws = self.workspace(moe_cache_workspace_size(self.desc, src.numel()), stream)
+        moe_cache_fork(self.layers, self.desc, src, dst, self.err_word, ws, stream)
+
+    def compact(self, n_used=None, stream=None):
+        ws = self.workspace(moe_cache_workspace_size(self.desc, 0), stream)
+        moe_cache_compact(self.layers, self.desc, n_used, self.err_word, ws, stream)
 
 
 # ------------------------------------------------------------ layer object

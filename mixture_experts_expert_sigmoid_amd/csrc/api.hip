@@ -21,12 +21,6 @@ namespace {
 
 thread_local char g_last_error[256] = "";
 
-int hip_fail(hipError_t e, const char* where) {
-  snprintf(g_last_error, sizeof g_last_error, "%s: %s", where,
-           hipGetErrorString(e));
-  return MOE_ERR_HIP;
-}
-
 inline size_t al(size_t b) { return (b + 255) & ~(size_t)255; }
 constexpr int kMaxAdapters = 1024;
 inline bool finite(float v) { return isfinite(v); }
@@ -81,6 +75,13 @@ bool batched(const moe_lora* l) { return l && l->n_adapters > 1; }
 long pcap_of(long T, int k, int shared) { return T * (long)k + (shared ? T : 0); }
 
 }  // namespace
+
+int moe::hip_fail(hipError_t e, const char* where) {
+  snprintf(g_last_error, sizeof g_last_error, "%s: %s", where,
+           hipGetErrorString(e));
+  return MOE_ERR_HIP;
+}
+using moe::hip_fail;
 
 extern "C" {
 

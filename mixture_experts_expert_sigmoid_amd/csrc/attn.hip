@@ -1,0 +1,73 @@
+// Launchers of the attention kernels: workspace layout, the split of large
+// batches into launches, the choice of the head_dim instantiation.
+#include "kv.h"
+
+namespace moe {
+
+hipError_t launch_decode_64(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_decode_128(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_decode_256(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_prefill_64(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_prefill_128(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
+
+namespace {
+inline size_t al16(size_t b) { return (b + 15) & ~(size_t)15; }
+size_t dec_part_bytes(int D) { return (size_t)kDecWgs * 2 * (32 + 16 * D) * 4; }
+}  // namespace
+
+size_t decode_ws_bytes(long n, int hq, int hkv, int D) {
+  const long m = n < kDecMaxSeqs ? n : kDecMaxSeqs;
+  const int ht = (hq / hkv + 15) / 16;
+  return dec_part_bytes(D) + al16((size_t)m * hkv * ht * 8);
+}
+
+hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
+  // a workgroup keeps the lengths of its launch's sequences in LDS
+  for (long b = 0; b < all.n; b += kDecMaxSeqs) {
+    AttnArgs a = all;
+    a.n = (int)(all.n - b < kDecMaxSeqs ? all.n - b : kDecMaxSeqs);
+    if (a.slots) {
+      a.slots += b;
+    } else {
+      a.t.table += b * a.t.ld;
+      a.t.len += b;
+      a.t.n_slots -= (int)b;
+    }
+    a.q += b * a.q_row;
+    a.out += b * a.o_row;
+    if (a.lse) a.lse += b * a.hq;
+    a.meta = (int*)((char*)a.part + dec_part_bytes(a.c.D));
+    hipError_t e = a.c.D == 64    ? launch_decode_64(a, fmt, s)
+                   : a.c.D == 128 ? launch_decode_128(a, fmt, s)
+                                  : launch_decode_256(a, fmt, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// Tiles of kPreRows rows that n sequences of T tokens can have, per
+// key-value head; parts per tile so that about 512 workgroups run.
+static long prefill_tiles(long n, long T, int g) { return T * g / kPreRows + n; }
+
+int prefill_splits(long n, long T, int hq, int hkv) {
+  const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
+  if (tiles >= 384) return 1;
+  const long s = (512 + tiles - 1) / tiles;
+  return (int)(s < 64 ? s : 64);
+}
+
+size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
+  const int s = prefill_splits(n, T, hq, hkv);
+  return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
+  AttnArgs a = all;
+  a.n_split = prefill_splits(a.n, a.T, a.hq, a.hq / a.g);
+  return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
+         : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
+                        : launch_prefill_256(a, fmt, s);
+}
+
+}  // namespace moe

@@ -7,6 +7,9 @@
 
 namespace moe {
 
+// keeps the message for moe_last_error() and returns MOE_ERR_HIP (api.hip)
+int hip_fail(hipError_t e, const char* where);
+
 // bias: NULL (rank on the raw logit) or [n_routed] (rank on fp32
 // sigmoid(x) + bias); packed: NULL or [T][k] (id << 16 | bf16 weight)
 hipError_t launch_route(const float* logits, long T, long ld, int n_routed,
