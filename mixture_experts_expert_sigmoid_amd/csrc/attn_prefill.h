@@ -7,8 +7,8 @@
 // key-value head, token-major, so the heads that share keys share the tile:
 // a tile spans few positions, and a short chunk still fills it.
 //
-// Layout. Four waves of 32 rows, v_mfma_*_32x32x16. A wave's row lies in a
-// lane's column of S^T (lane l: row l % 32, 16 of 32 keys), so the softmax
+// Layout. Four waves of two 32-row blocks (one for head_dim 256),
+// v_mfma_*_32x32x16. A row lies in a lane's column of S^T (lane l: row l % 32, 16 of 32 keys), so the softmax
 // is a loop in the lane and one exchange with lane l ^ 32, and P is the B
 // operand of the second product as it stands when each lane half's 8-key
 // slice of a 16-key step is taken as keys 4h..4h+3 and 8+4h..8+4h+3 of it.
@@ -35,10 +35,19 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// keys of a tile, 32-row blocks of a wave, rows of a workgroup's tile
+template <int D>
+struct PreShape {
+  static constexpr int BN = D == 256 ? 32 : 64;
+  static constexpr int RB = D == 64 ? 2 : 1;
+  static constexpr int ROWS = prefill_rows(D);
+  static_assert(ROWS == 128 * RB, "four waves");
+};
+
 // what a workgroup works on
 struct PreTile {
   int seq, slot, L, m, q0;     // sequence; its slot, length, new tokens, first row of q
-  int tile, rows;              // tile of kPreRows rows, rows of the sequence
+  int tile, rows;              // tile of PreShape::ROWS rows, rows of the sequence
   int p_min, p_max;            // positions of its first and last row
   int lo_min, lo_max;          // first key of the window at those
   int nb1, b2, nb;             // key tiles: 0..nb1-1, then b2 .. b2 + nb - nb1 - 1
@@ -49,17 +58,18 @@ __device__ __forceinline__ int pre_cu(const AttnArgs& a, int i) {
   return c < 0 ? 0 : (c > a.T ? (int)a.T : c);
 }
 
-template <int BN>
+template <int D>
 __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
+  constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   const int g = a.g;
   t.q0 = pre_cu(a, t.seq);
   t.m = max(0, pre_cu(a, t.seq + 1) - t.q0);
   t.rows = t.m * g;
-  if (t.tile * kPreRows >= t.rows) return false;
+  if (t.tile * ROWS >= t.rows) return false;
   t.slot = kv_slot(a.slots, t.seq, a.t.n_slots, a.err);
   t.L = kv_len(a.t, t.slot);
-  const int r1 = min(t.rows, (t.tile + 1) * kPreRows) - 1;
-  t.p_min = t.L - t.m + t.tile * kPreRows / g;
+  const int r1 = min(t.rows, (t.tile + 1) * ROWS) - 1;
+  t.p_min = t.L - t.m + t.tile * ROWS / g;
   t.p_max = t.L - t.m + r1 / g;
   t.lo_min = a.window ? max(0, t.p_min - a.window + 1) : 0;
   t.lo_max = a.window ? max(0, t.p_max - a.window + 1) : 0;
@@ -77,29 +87,32 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
 
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(AttnArgs a) {
-  constexpr int BN = D == 256 ? 32 : 64;         // keys of a tile
+  constexpr int BN = PreShape<D>::BN, RB = PreShape<D>::RB, ROWS = PreShape<D>::ROWS;
   constexpr int NA = BN / 32;                    // 32-key score tiles
   constexpr int NC = D / 16;                     // steps of the first product
   constexpr int ND = D / 32;                     // 32-row tiles of O^T
   constexpr int UPR = D / 8;                     // 16-byte units of a row in LDS
-  constexpr int GPR = F8 ? D / 16 : D / 8;       // 16-byte units of a row in memory
-  constexpr int RPI = 256 / GPR;                 // rows of one load of the workgroup
-  constexpr int NL = BN / RPI;                   // loads per thread and array
-  static_assert(NL >= 1 && BN % RPI == 0, "tile");
+  constexpr int WR = BN / 4;                     // rows of a tile that a wave brings
+  constexpr int GPR = F8 ? D / 16 : UPR;         // 16-byte units of a row in memory
+  constexpr int NL = WR * GPR / 64;              // loads per lane and array
+  constexpr int TB = BN * D * 2;                 // bytes of a tile in LDS
+  static_assert(NL >= 1, "tile");
 
-  __shared__ __align__(16) char s_k[BN * D * 2];
-  __shared__ __align__(16) char s_v[BN * D * 2];
-  __shared__ int s_bad;                          // tile whose V holds values not finite
+  __shared__ __align__(16) char s_k[2][TB];
+  __shared__ __align__(16) char s_v[2][TB];
+  __shared__ int s_ok[2][4];                     // page there, by bringing wave
+  __shared__ int s_bad;                          // values of V not finite were taken out
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l31 = lane & 31;
 
   PreTile t;
   const int kvh = blockIdx.x % a.c.hkv;
   {
-    // longest tiles first; sequence i's tiles start at cu[i] g / kPreRows + i
+    // longest tiles first; sequence i's tiles start at cu[i] g / ROWS + i
     const int tt = (int)(gridDim.x / a.c.hkv) - 1 - (int)(blockIdx.x / a.c.hkv);
-    auto base = [&](int i) { return (int)((long)pre_cu(a, i) * a.g / kPreRows) + i; };
+    auto base = [&](int i) { return (int)((long)pre_cu(a, i) * a.g / ROWS) + i; };
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -107,98 +120,144 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     }
     t.seq = lo;
     t.tile = tt - base(lo);
-    if (!pre_span<BN>(a, t)) return;
+    if (!pre_span<D>(a, t)) return;
   }
   const int parts = pre_parts(a, t.nb);
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
   const int x1 = (int)((long)(blockIdx.y + 1) * t.nb / parts);
-  if (tid == 0) s_bad = -1;
+  if (tid == 0) s_bad = 0;
 
-  // this lane's row
-  const int r = t.tile * kPreRows + 32 * w + l31;
-  const bool have = r < t.rows;
-  const int tok = have ? r / a.g : 0;
-  const int head = kvh * a.g + (have ? r - tok * a.g : 0);
-  const int pos = have ? t.L - t.m + tok : -1;
-  const int lo = a.window ? pos - a.window + 1 : 0;
+  // the wave's rows and what they see
+  const int r0 = t.tile * ROWS + w * (32 * RB);
+  const bool idle = r0 >= t.rows;
+  const int wp_min = t.L - t.m + min(r0, t.rows - 1) / a.g;
+  const int wp_max = t.L - t.m + (min(r0 + 32 * RB, t.rows) - 1) / a.g;
+  const int wlo_min = a.window ? max(0, wp_min - a.window + 1) : 0;
+  const int wlo_max = a.window ? max(0, wp_max - a.window + 1) : 0;
 
-  u32x4 q[NC];
-  {
-    const char* p = a.q + (long)(t.q0 + tok) * a.q_row + head * a.q_head + 16 * half;
+  // scores are compared unscaled: the sign of the scale goes into q
+  float sc = F8 ? a.scale * a.c.ks[kvh] : a.scale;
+  const uint32_t flip = sc < 0.0f ? 0x80008000u : 0u;
+  const bool flat = sc == 0.0f;
+  sc = flat ? 1.0f : fabsf(sc);
+  const float thr = fminf(8.0f / sc, 1e30f);
+
+  // this lane's rows
+  bool have[RB];
+  int head[RB], pos[RB], lo[RB];
+  long qrow[RB];
+  u32x4 q[RB][NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) q[c] = *(const u32x4*)(p + 32 * c);
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = r0 + 32 * rb + l31;
+    have[rb] = r < t.rows;
+    const int tok = have[rb] ? r / a.g : 0;
+    head[rb] = kvh * a.g + (have[rb] ? r - tok * a.g : 0);
+    pos[rb] = have[rb] ? t.L - t.m + tok : -1;
+    lo[rb] = a.window ? pos[rb] - a.window + 1 : 0;
+    qrow[rb] = t.q0 + tok;
+    const char* p = a.q + qrow[rb] * a.q_row + head[rb] * a.q_head + 16 * half;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const u32x4 y = *(const u32x4*)(p + 32 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[rb][c][e] = flat ? 0u : y[e] ^ flip;
+    }
   }
-  const float sc = F8 ? a.scale * a.c.ks[kvh] : a.scale;
 
-  f32x16 o[ND];
+  f32x16 o[RB][ND];
+  float m[RB], l[RB];
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+  for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = kNegInf, l = 0.0f;
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[rb][d][i] = 0.0f;
+    m[rb] = kNegInf;
+    l[rb] = 0.0f;
+  }
 
   const int* row = a.t.table + (long)max(0, t.slot) * a.t.ld;
   const char* kb = a.c.k + kvh * a.c.sh;
   const char* vb = a.c.v + kvh * a.c.sh;
-  const int srow = tid / GPR, scol = tid % GPR;  // this thread's unit of a load
+  const int grp = w * WR / 16;                   // 16-key group that this wave brings from
 
   auto key_of = [&](int x) { return BN * (x < t.nb1 ? x : t.b2 + x - t.nb1); };
-  // page of a 16-key group, -1 where it is missing or holds no visible key
-  auto page_of = [&](int key) {
-    if (key > t.p_max || !(key + 16 > t.lo_min || key < a.first)) return -1;
-    const int p = row[kv_entry(a.t, key)];
-    if (p >= 0 && p < a.t.n_pages) return p;
-    atomicOr(a.err, kErrPage);
-    return -1;
+  auto group_seen = [&](int key) {
+    return key <= t.p_max && (key + 16 > t.lo_min || key < a.first);
   };
-
-  u32x4 rk[NL], rv[NL];
-  auto load = [&](int x) {
-    const int key = key_of(x);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int kr = key + i * RPI + srow;
-      const int k16 = __builtin_amdgcn_readfirstlane(kr & ~15);
-      const int p = page_of(k16);
-      rk[i] = rv[i] = u32x4{0, 0, 0, 0};
-      if (p >= 0) {
-        const int in = k16 - kv_entry(a.t, k16) * a.t.ps;
-        const long off = p * a.c.sp + (long)(in + (kr & 15)) * a.c.st + 16 * scol;
-        rk[i] = *(const u32x4*)(kb + off);
-        rv[i] = *(const u32x4*)(vb + off);
-      }
-    }
+  // table entry of the wave's group of tile x; -2: nothing of it is visible
+  auto fetch = [&](int x) {
+    const int key = key_of(x) + 16 * grp;
+    return x < x1 && group_seen(key) ? row[kv_entry(a.t, key)] : -2;
   };
   auto whole_of = [&](int key) {
     return key + BN - 1 <= t.p_min && (key >= t.lo_max || key + BN <= a.first);
   };
-  // 16-byte unit u of key kr in LDS
-  auto k_unit = [&](char* b, int kr, int u) {
-    return b + kr * (2 * D) + 16 * (u ^ (kr & (UPR < 16 ? UPR - 1 : 15)));
-  };
-  auto v_swz = [&](int kr) {
-    return UPR == 8 ? ((kr >> 1) & 3) << 1 : (kr & 7) << 1;
-  };
-  auto bad16 = [&](uint32_t x) {       // either half infinite or NaN
-    const uint32_t e = BF ? 0x7F80u : 0x7C00u;
-    return (x & e) == e || ((x >> 16) & e) == e;
+  // swizzle of 16-byte units by row (of the tile)
+  auto k_swz = [&](int kr) { return kr & (UPR < 16 ? UPR - 1 : 15); };
+  auto v_swz = [&](int kr) { return UPR == 8 ? ((kr >> 1) & 3) << 1 : (kr & 7) << 1; };
+  const uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
+  auto bad16 = [&](uint32_t x) {                 // either half infinite or NaN
+    return (x & kExp) == kExp || ((x >> 16) & kExp) == kExp;
   };
   auto clean16 = [&](uint32_t x) {
-    const uint32_t e = BF ? 0x7F80u : 0x7C00u;
-    if ((x & e) == e) x &= 0xFFFF0000u;
-    if (((x >> 16) & e) == e) x &= 0x0000FFFFu;
+    if ((x & kExp) == kExp) x &= 0xFFFF0000u;
+    if (((x >> 16) & kExp) == kExp) x &= 0x0000FFFFu;
     return x;
   };
-  auto stage = [&](int x) {
-    const int key = key_of(x);
-    const bool whole = whole_of(key);
+  // a unit of V of a tile that is not whole, as it is to be staged
+  auto clean = [&](u32x4 v, int key, int kr) {
+    const int j = key + kr;
+    if (j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
+    if (bad16(v[0]) || bad16(v[1]) || bad16(v[2]) || bad16(v[3])) {
+      s_bad = 1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = clean16(v[e]);
+    }
+    return v;
+  };
+
+  u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];        // e4m3: raw units on their way
+  // starts the loads of this wave's rows of tile x: 16-bit straight into LDS
+  auto issue = [&](int x, int e, int buf) {
+    const int key = key_of(x) + 16 * grp;
+    const bool ok = e >= 0 && e < a.t.n_pages;
+    if (!ok && e != -2 && lane == 0) atomicOr(a.err, kErrPage);
+    if (lane == 0) s_ok[buf][w] = ok;
+    const int in = ok ? key - kv_entry(a.t, key) * a.t.ps : 0;
+    // a uniform base, and an offset of the lane below 2^31 (16 stride_tok < 2^30)
+    const long off = (ok ? e : 0) * a.c.sp + in * a.c.st;
+    const char* kp = kb + off;
+    const char* vp = vb + off;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int lr = i * RPI + srow, kr = key + lr;
-      const bool dead = kr > t.p_max || !(kr >= t.lo_min || kr < a.first);
-      u32x4 kk[2], vv[2];
+      const int up = i * 64 + lane, kr = w * WR + up / GPR, u = up % GPR;
+      const uint32_t ro = (uint32_t)(kr & 15) * (uint32_t)a.c.st;
       if constexpr (F8) {
+        rk[i] = *(const u32x4*)(kp + (ro + 16 * u));
+        rv[i] = *(const u32x4*)(vp + (ro + 16 * u));
+      } else {
+        const int at = (w * WR * UPR + i * 64) * 16;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(kp + (ro + 16 * (u ^ k_swz(kr)))),
+            (__attribute__((address_space(3))) void*)(s_k[buf] + at), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(vp + (ro + 16 * (u ^ v_swz(kr)))),
+            (__attribute__((address_space(3))) void*)(s_v[buf] + at), 16, 0, 0);
+      }
+    }
+  };
+  // completes them: waits, expands e4m3, takes masked values out of V
+  auto finish = [&](int x, int buf) {
+    const int key = key_of(x);
+    const bool whole = whole_of(key);
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int up = i * 64 + lane, kr = w * WR + up / GPR, u = up % GPR;
+        u32x4 kk[2], vv[2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           kk[e >> 1][2 * (e & 1)] = from_e4m3<BF, false>(rk[i][e]);
@@ -206,129 +265,123 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
           vv[e >> 1][2 * (e & 1)] = from_e4m3<BF, false>(rv[i][e]);
           vv[e >> 1][2 * (e & 1) + 1] = from_e4m3<BF, true>(rv[i][e]);
         }
-      } else {
-        kk[0] = rk[i];
-        vv[0] = rv[i];
-      }
-      constexpr int H = F8 ? 2 : 1;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        if (!whole) {
-          if (dead) vv[h] = u32x4{0, 0, 0, 0};
-          if (bad16(vv[h][0]) || bad16(vv[h][1]) || bad16(vv[h][2]) || bad16(vv[h][3])) {
-            s_bad = x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vv[h][e] = clean16(vv[h][e]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          if (!whole) vv[h] = clean(vv[h], key, kr);
+          *(u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ k_swz(kr))) = kk[h];
+          *(u32x4*)(s_v[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = vv[h];
         }
-        const int u = H * scol + h;
-        *(u32x4*)k_unit(s_k, lr, u) = kk[h];
-        *(u32x4*)(s_v + lr * (2 * D) + 16 * (u ^ v_swz(lr))) = vv[h];
+      }
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int up = i * 64 + lane, kr = w * WR + up / GPR;
+          u32x4* p = (u32x4*)(s_v[buf] + (w * WR * UPR + up) * 16);
+          *p = clean(*p, key, kr);
+        }
       }
     }
   };
 
-  if (x0 < x1) load(x0);
+  int e_next = 0;
+  if (x0 < x1) {
+    issue(x0, fetch(x0), 0);
+    e_next = fetch(x0 + 1);
+  }
   for (int x = x0; x < x1; ++x) {
-    const int key = key_of(x);
-    __syncthreads();                   // the tile before is done with
-    stage(x);
+    const int key = key_of(x), buf = (x - x0) & 1;
+    finish(x, buf);
     __syncthreads();
-    uint32_t gone = 0;                 // 16-key groups without a page
-    bool whole = whole_of(key);
+    // the other buffer's tile is done with: every wave has passed the barrier
+    if (x + 1 < x1) {
+      issue(x + 1, e_next, buf ^ 1);
+      e_next = fetch(x + 2);
+    }
+    if (idle || key > wp_max || (key + BN <= wlo_min && key >= a.first)) continue;
+    uint32_t gone = 0;                           // 16-key groups without a page
 #pragma unroll
-    for (int gi = 0; gi < BN / 16; ++gi)
-      if (page_of(key + 16 * gi) < 0) gone |= 1u << gi;
-    if (gone) whole = false;
-    if (x + 1 < x1) load(x + 1);
+    for (int i = 0; i < 4; ++i)
+      if (!s_ok[buf][i]) gone |= 1u << (i * WR / 16);
+    const bool whole = !gone && key + BN - 1 <= wp_min && (key >= wlo_max || key + BN <= a.first);
 
-    f32x16 s[NA];
+    f32x16 s[RB][NA];
 #pragma unroll
     for (int aa = 0; aa < NA; ++aa) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[aa][i] = 0.0f;
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[rb][aa][i] = 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const u32x4 ka = *(const u32x4*)k_unit(s_k, 32 * aa + l31, 2 * c + half);
-        s[aa] = mfma32<BF>(ka, q[c], s[aa]);
+        const int kr = 32 * aa + l31;
+        const u32x4 ka =
+            *(const u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * c + half) ^ k_swz(kr)));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) s[rb][aa] = mfma32<BF>(ka, q[rb][c], s[rb][aa]);
       }
     }
-    float bm = kNegInf;
+    if (!whole) {
 #pragma unroll
-    for (int aa = 0; aa < NA; ++aa)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[aa][i] *= sc;
-        if (!whole) {
-          const int kk = 32 * aa + 8 * (i >> 2) + 4 * half + (i & 3), j = key + kk;
-          const bool ok = j <= pos && (j >= lo || j < a.first) && !((gone >> (kk >> 4)) & 1);
-          if (!ok) s[aa][i] = kNegInf;
-        }
-        bm = fmaxf(bm, s[aa][i]);
-      }
-    bm = xor32_reduce(bm, OpMax{});
-    if (__any(bm > m + 8.0f)) {
-      const float mn = fmaxf(m, bm);
-      const float f = exp2_fast(m - (mn == kNegInf ? 0.0f : mn));
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= f;
-    }
-    const float mu = m == kNegInf ? 0.0f : m;
-#pragma unroll
-    for (int aa = 0; aa < NA; ++aa)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[aa][i] = exp2_fast(s[aa][i] - mu);
-        l += s[aa][i];
-      }
-
-    if (!whole && s_bad == x) {
-      // values of V that are not finite, for the rows that see their key
-      for (int k = 0; k < BN; ++k) {
-        const int kp = page_of((key + k) & ~15);
-        if (kp < 0) continue;
-        float pv = 0.0f;
+      for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int aa = 0; aa < NA; ++aa)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k == 32 * aa + 8 * (i >> 2) + 4 * ((k >> 2) & 1) + (i & 3)) pv = s[aa][i];
-        pv = __shfl(pv, l31 + 32 * ((k >> 2) & 1));
-        const int j = key + k;
-        const bool sees = j <= pos && (j >= lo || j < a.first);
-        const int in = j - kv_entry(a.t, j) * a.t.ps;
-        const char* vr = vb + kp * a.c.sp + (long)in * a.c.st;
+          for (int i = 0; i < 16; ++i) {
+            const int kk = 32 * aa + 8 * (i >> 2) + (i & 3), at = key + 4 * half;
+            const bool ok = kk <= pos[rb] - at && (kk >= lo[rb] - at || kk < a.first - at) &&
+                            !((gone >> (kk >> 4)) & 1);
+            if (!ok) s[rb][aa][i] = kNegInf;
+          }
+    }
+    float bm[RB];
+    bool grown = false;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      bm[rb] = s[rb][0][0];
+#pragma unroll
+      for (int aa = 0; aa < NA; ++aa)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bm[rb] = fmaxf(bm[rb], s[rb][aa][i]);
+      bm[rb] = xor32_reduce(bm[rb], OpMax{});
+      grown |= bm[rb] > m[rb] + thr;
+    }
+    if (__any(grown)) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        const float mn = fmaxf(m[rb], bm[rb]);
+        const float f = exp2_fast((m[rb] - (mn == kNegInf ? 0.0f : mn)) * sc);
+        m[rb] = mn;
+        l[rb] *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int dd = 32 * d + 8 * (i >> 2) + 4 * half + (i & 3);
-            uint32_t x16;
-            if constexpr (F8)
-              x16 = from_e4m3<BF, false>(*(const uint8_t*)(vr + dd)) & 0xFFFF;
-            else
-              x16 = *(const uint16_t*)(vr + 2 * dd);
-            if (bad16(x16) && sees) {
-              const float vf = BF ? bf16_bits_to_f32(x16)
-                                  : (float)__builtin_bit_cast(_Float16, (uint16_t)x16);
-              o[d][i] += pv * vf;
-            }
-          }
+          for (int i = 0; i < 16; ++i) o[rb][d][i] *= f;
       }
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const float neg = m[rb] == kNegInf ? 0.0f : -m[rb] * sc;
+#pragma unroll
+      for (int aa = 0; aa < NA; ++aa)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[rb][aa][i] = exp2_fast(__builtin_fmaf(s[rb][aa][i], sc, neg));
+          l[rb] += s[rb][aa][i];
+        }
     }
 
 #pragma unroll
     for (int aa = 0; aa < NA; ++aa)
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        u32x4 pb;
+        u32x4 pb[RB];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          pb[j] = pack16<BF>(s[aa][8 * st + 2 * j], s[aa][8 * st + 2 * j + 1]);
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            pb[rb][j] = pack16<BF>(s[rb][aa][8 * st + 2 * j], s[rb][aa][8 * st + 2 * j + 1]);
         // keys 4 half + 0..3 of the 16-key step, then the same + 8; lane i of
         // 16 reads row i / 4, 4 values from 4 (i % 4), and gets column i
         const int k0 = 32 * aa + 16 * st + 4 * half + ((lane & 15) >> 2);
@@ -340,47 +393,106 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
           for (int h = 0; h < 2; ++h) {
             const int kr = k0 + 8 * h;
             const int b = 2 * (32 * d + dc);      // byte in the row
-            char* p = s_v + kr * (2 * D) + (16 * ((b >> 4) ^ v_swz(kr)) + (b & 15));
+            char* p = s_v[buf] + kr * (2 * D) + (16 * ((b >> 4) ^ v_swz(kr)) + (b & 15));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4*)p);
             const u32x2 z = __builtin_bit_cast(u32x2, y);
             va[2 * h] = z[0];
             va[2 * h + 1] = z[1];
           }
-          o[d] = mfma32<BF>(va, pb, o[d]);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) o[rb][d] = mfma32<BF>(va, pb[rb], o[rb][d]);
         }
       }
   }
 
-  l = xor32_reduce(l, OpSum{});
-  if (!have) return;
-  if (parts == 1) {
-    float inv = l == 0.0f ? 0.0f : 1.0f / l;       // no visible key: 0
-    if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
-    char* dst = a.out + (long)(t.q0 + tok) * a.o_row + head * a.o_head;
+  // values of V that are not finite and were staged as zeros: their products,
+  // for the rows that see their key
+  __syncthreads();
+  if (s_bad && !idle) {
+    for (int x = x0; x < x1; ++x) {
+      const int key = key_of(x);
+      if (whole_of(key)) continue;
+      for (int j = key; j < key + BN; ++j) {
+        if (j > t.p_max || !(j >= t.lo_min || j < a.first)) continue;
+        const int e = kv_entry(a.t, j), p = row[e];
+        if (p < 0 || p >= a.t.n_pages) continue;
+        const long off = p * a.c.sp + (long)(j - e * a.t.ps) * a.c.st;
+        auto value = [&](const char* base, int dd) {
+          uint32_t x16;
+          if constexpr (F8)
+            x16 = from_e4m3<BF, false>(*(const uint8_t*)(base + off + dd)) & 0xFFFF;
+          else
+            x16 = *(const uint16_t*)(base + off + 2 * dd);
+          return BF ? bf16_bits_to_f32(x16)
+                    : (float)__builtin_bit_cast(_Float16, (uint16_t)x16);
+        };
+        auto finite = [](float f) { return fabsf(f) < __builtin_huge_valf(); };
+        bool any = false;
+#pragma unroll 1
+        for (int dd = lane; dd < D; dd += 64) any |= !finite(value(vb, dd));
+        if (!__any(any)) continue;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+        for (int rb = 0; rb < RB; ++rb) {
+          float dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const u32x2 y = {pack16<BF>(o[d][i] * inv, o[d][i + 1] * inv),
-                         pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t q16 = (q[rb][c][i >> 1] >> (16 * (i & 1))) & 0xFFFF;
+              dot += value(kb, 16 * c + 8 * half + i) *
+                     (BF ? bf16_bits_to_f32(q16)
+                         : (float)__builtin_bit_cast(_Float16, (uint16_t)q16));
+            }
+          dot = xor32_reduce(dot, OpSum{});
+          const bool sees = j <= pos[rb] && (j >= lo[rb] || j < a.first);
+          const float pv = exp2_fast(
+              __builtin_fmaf(dot, sc, m[rb] == kNegInf ? 0.0f : -m[rb] * sc));
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = value(vb, 32 * d + 8 * (i >> 2) + 4 * half + (i & 3));
+              if (sees && !finite(f)) o[rb][d][i] += pv * f;
+              if (i == 15) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
       }
-    if (a.lse && half == 0)
-      a.lse[(long)(t.q0 + tok) * a.hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
-  } else {
-    const long rows = a.T * a.hq, ri = (long)(t.q0 + tok) * a.hq + head;
-    float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
+    }
+  }
+
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+  for (int rb = 0; rb < RB; ++rb) {
+    l[rb] = xor32_reduce(l[rb], OpSum{});
+    if (!have[rb]) continue;
+    if (parts == 1) {
+      float inv = l[rb] == 0.0f ? 0.0f : 1.0f / l[rb];      // no visible key: 0
+      if (F8 && l[rb] != 0.0f) inv *= a.c.vs[kvh];
+      char* dst = a.out + qrow[rb] * a.o_row + head[rb] * a.o_head;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *(f32x4*)(dst + 32 * d + 2 * i + 4 * half) =
-            f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-    if (half == 0) {
-      float* ml = a.part + (long)a.n_split * rows * D + ((long)blockIdx.y * rows + ri) * 2;
-      ml[0] = m;
-      ml[1] = l;
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const u32x2 y = {pack16<BF>(o[rb][d][i] * inv, o[rb][d][i + 1] * inv),
+                           pack16<BF>(o[rb][d][i + 2] * inv, o[rb][d][i + 3] * inv)};
+          *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
+        }
+      if (a.lse && half == 0)
+        a.lse[qrow[rb] * a.hq + head[rb]] = (m[rb] * sc + __builtin_amdgcn_logf(l[rb])) * kLn2;
+    } else {
+      const long rows = a.T * a.hq, ri = qrow[rb] * a.hq + head[rb];
+      float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *(f32x4*)(dst + 32 * d + 2 * i + 4 * half) =
+              f32x4{o[rb][d][i], o[rb][d][i + 1], o[rb][d][i + 2], o[rb][d][i + 3]};
+      if (half == 0) {
+        float* ml = a.part + (long)a.n_split * rows * D + ((long)blockIdx.y * rows + ri) * 2;
+        ml[0] = m[rb] * sc;
+        ml[1] = l[rb];
+      }
     }
   }
 }
@@ -388,7 +500,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
 // Joins the parts of split tiles: one wave per (token, query head).
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
-  constexpr int BN = D == 256 ? 32 : 64;
+  constexpr int ROWS = PreShape<D>::ROWS;
   constexpr int E = D / 64;
   const long rows = a.T * a.hq;
   const long ri = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -402,8 +514,8 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
       if (pre_cu(a, mid) <= tok) lo = mid; else hi = mid - 1;
     }
     t.seq = lo;
-    t.tile = ((tok - pre_cu(a, lo)) * a.g + head % a.g) / kPreRows;
-    if (!pre_span<BN>(a, t)) return;
+    t.tile = ((tok - pre_cu(a, lo)) * a.g + head % a.g) / ROWS;
+    if (!pre_span<D>(a, t)) return;
   }
   const int parts = pre_parts(a, t.nb);
   if (parts == 1) return;
@@ -439,7 +551,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
 
 template <bool BF, bool F8, int D>
 hipError_t run_prefill(const AttnArgs& a, hipStream_t s) {
-  const long tiles = a.T * a.g / kPreRows + a.n;
+  const long tiles = prefill_tiles(a.n, a.T, a.g, D);
   attn_prefill_kernel<BF, F8, D>
       <<<dim3((unsigned)(tiles * a.c.hkv), a.n_split), 256, 0, s>>>(a);
   if (a.n_split > 1)
