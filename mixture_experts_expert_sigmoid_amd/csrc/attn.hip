@@ -47,21 +47,21 @@ hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
 }
 
 // parts per tile so that about 512 workgroups run
-int prefill_splits(long n, long T, int hq, int hkv, int D) {
-  const long tiles = prefill_tiles(n, T, hq / hkv, D) * hkv;
+int prefill_splits(long n, long T, int hq, int hkv) {
+  const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
   if (tiles >= 384) return 1;
   const long s = (512 + tiles - 1) / tiles;
   return (int)(s < 64 ? s : 64);
 }
 
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
-  const int s = prefill_splits(n, T, hq, hkv, D);
+  const int s = prefill_splits(n, T, hq, hkv);
   return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
   AttnArgs a = all;
-  a.n_split = prefill_splits(a.n, a.T, a.hq, a.hq / a.g, a.c.D);
+  a.n_split = prefill_splits(a.n, a.T, a.hq, a.hq / a.g);
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);

@@ -7,8 +7,8 @@
 // key-value head, token-major, so the heads that share keys share the tile:
 // a tile spans few positions, and a short chunk still fills it.
 //
-// Layout. Four waves of two 32-row blocks (one for head_dim 256),
-// v_mfma_*_32x32x16. A row lies in a lane's column of S^T (lane l: row l % 32, 16 of 32 keys), so the softmax
+// Layout. Four waves of 32 rows, v_mfma_*_32x32x16. A row lies in a lane's
+// column of S^T (lane l: row l % 32, 16 of 32 keys), so the softmax
 // is a loop in the lane and one exchange with lane l ^ 32, and P is the B
 // operand of the second product as it stands when each lane half's 8-key
 // slice of a 16-key step is taken as keys 4h..4h+3 and 8+4h..8+4h+3 of it.
@@ -35,13 +35,11 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// keys of a tile, 32-row blocks of a wave, rows of a workgroup's tile
+// keys of a tile, rows of a workgroup's tile
 template <int D>
 struct PreShape {
   static constexpr int BN = D == 256 ? 32 : 64;
-  static constexpr int RB = D == 64 ? 2 : 1;
-  static constexpr int ROWS = prefill_rows(D);
-  static_assert(ROWS == 128 * RB, "four waves");
+  static constexpr int ROWS = kPreRows;
 };
 
 // what a workgroup works on
@@ -87,7 +85,7 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
 
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(AttnArgs a) {
-  constexpr int BN = PreShape<D>::BN, RB = PreShape<D>::RB, ROWS = PreShape<D>::ROWS;
+  constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   constexpr int NA = BN / 32;                    // 32-key score tiles
   constexpr int NC = D / 16;                     // steps of the first product
   constexpr int ND = D / 32;                     // 32-row tiles of O^T
@@ -129,11 +127,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   if (tid == 0) s_bad = 0;
 
   // the wave's rows and what they see
-  const int r0 = t.tile * ROWS + w * (32 * RB);
-  const bool idle = r0 >= t.rows;
+  const int r0 = t.tile * ROWS + w * 32;
   const int wp_min = t.L - t.m + min(r0, t.rows - 1) / a.g;
-  const int wp_max = t.L - t.m + (min(r0 + 32 * RB, t.rows) - 1) / a.g;
-  const int wlo_min = a.window ? max(0, wp_min - a.window + 1) : 0;
+  const int wp_max = t.L - t.m + (min(r0 + 32, t.rows) - 1) / a.g;
   const int wlo_max = a.window ? max(0, wp_max - a.window + 1) : 0;
 
   // scores are compared unscaled: the sign of the scale goes into q
@@ -143,61 +139,64 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   sc = flat ? 1.0f : fabsf(sc);
   const float thr = fminf(8.0f / sc, 1e30f);
 
-  // this lane's rows
-  bool have[RB];
-  int head[RB], pos[RB], lo[RB];
-  long qrow[RB];
-  u32x4 q[RB][NC];
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const int r = r0 + 32 * rb + l31;
-    have[rb] = r < t.rows;
-    const int tok = have[rb] ? r / a.g : 0;
-    head[rb] = kvh * a.g + (have[rb] ? r - tok * a.g : 0);
-    pos[rb] = have[rb] ? t.L - t.m + tok : -1;
-    lo[rb] = a.window ? pos[rb] - a.window + 1 : 0;
-    qrow[rb] = t.q0 + tok;
-    const char* p = a.q + qrow[rb] * a.q_row + head[rb] * a.q_head + 16 * half;
+  // this lane's row
+  const int r = r0 + l31;
+  const bool have = r < t.rows;
+  const int tok = have ? r / a.g : 0;
+  const int head = kvh * a.g + (have ? r - tok * a.g : 0);
+  const int pos = have ? t.L - t.m + tok : -1;
+  const int lo = a.window ? pos - a.window + 1 : 0;
+  const long qrow = t.q0 + tok;
+  u32x4 q[NC];
+  {
+    const char* p = a.q + qrow * a.q_row + head * a.q_head + 16 * half;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const u32x4 y = *(const u32x4*)(p + 32 * c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[rb][c][e] = flat ? 0u : y[e] ^ flip;
+      for (int e = 0; e < 4; ++e) q[c][e] = flat ? 0u : y[e] ^ flip;
     }
   }
 
-  f32x16 o[RB][ND];
-  float m[RB], l[RB];
+  f32x16 o[ND];
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
+  for (int d = 0; d < ND; ++d)
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[rb][d][i] = 0.0f;
-    m[rb] = kNegInf;
-    l[rb] = 0.0f;
-  }
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = kNegInf, l = 0.0f;
 
-  const int* row = a.t.table + (long)max(0, t.slot) * a.t.ld;
+  // the sequence's table row; no kernel that runs beside this one writes it,
+  // so its entries come by scalar loads, which do not wait for the tiles'
+  typedef const __attribute__((address_space(4))) int* ConstInts;
+  const ConstInts row =
+      (ConstInts)(uintptr_t)(a.t.table + (long)max(0, t.slot) * a.t.ld);
   const char* kb = a.c.k + kvh * a.c.sh;
   const char* vb = a.c.v + kvh * a.c.sh;
   const int grp = w * WR / 16;                   // 16-key group that this wave brings from
 
   auto key_of = [&](int x) { return BN * (x < t.nb1 ? x : t.b2 + x - t.nb1); };
-  auto group_seen = [&](int key) {
-    return key <= t.p_max && (key + 16 > t.lo_min || key < a.first);
-  };
   // table entry of the wave's group of tile x; -2: nothing of it is visible
   auto fetch = [&](int x) {
     const int key = key_of(x) + 16 * grp;
-    return x < x1 && group_seen(key) ? row[kv_entry(a.t, key)] : -2;
+    const bool seen = x < x1 && key <= t.p_max && (key + 16 > t.lo_min || key < a.first);
+    return seen ? row[kv_entry(a.t, key)] : -2;
   };
+  auto there = [&](int e) { return e >= 0 && e < a.t.n_pages; };
+  // every row of the tile sees every key of tile x
   auto whole_of = [&](int key) {
     return key + BN - 1 <= t.p_min && (key >= t.lo_max || key + BN <= a.first);
   };
   // swizzle of 16-byte units by row (of the tile)
-  auto k_swz = [&](int kr) { return kr & (UPR < 16 ? UPR - 1 : 15); };
-  auto v_swz = [&](int kr) { return UPR == 8 ? ((kr >> 1) & 3) << 1 : (kr & 7) << 1; };
+  auto k_swz = [](int kr) { return kr & (UPR < 16 ? UPR - 1 : 15); };
+  auto v_swz = [](int kr) { return UPR == 8 ? ((kr >> 1) & 3) << 1 : (kr & 7) << 1; };
+  // This lane's places in a tile. Rows are a multiple of 128 bytes and the
+  // swizzle is the same for rows 16 (K: 32) apart, so units 2 c + half of K
+  // are at k_at ^ 32 c, values 32 d.. of V at v_at ^ 64 d, and the row blocks
+  // at constant distances: one address register each, turned by an exclusive
+  // or where it is used.
+  int k_at = l31 * (2 * D) + 16 * (half ^ k_swz(l31));
+  const int v_row = 4 * half + ((lane & 15) >> 2), v_d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  int v_at = v_row * (2 * D) + (16 * ((v_d >> 3) ^ v_swz(v_row)) + 2 * (v_d & 7));
   const uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
   auto bad16 = [&](uint32_t x) {                 // either half infinite or NaN
     return (x & kExp) == kExp || ((x >> 16) & kExp) == kExp;
@@ -208,9 +207,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     return x;
   };
   // a unit of V of a tile that is not whole, as it is to be staged
-  auto clean = [&](u32x4 v, int key, int kr) {
+  auto clean = [&](u32x4 v, int key, int kr, bool ok) {
     const int j = key + kr;
-    if (j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
+    if (!ok || j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
     if (bad16(v[0]) || bad16(v[1]) || bad16(v[2]) || bad16(v[3])) {
       s_bad = 1;
 #pragma unroll
@@ -219,204 +218,247 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     return v;
   };
 
-  u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];        // e4m3: raw units on their way
-  // starts the loads of this wave's rows of tile x: 16-bit straight into LDS
-  auto issue = [&](int x, int e, int buf) {
+  // The wave's rows of a tile: load i takes RPL of them, row i RPL + lane /
+  // GPR of the wave. 16-bit caches load straight into LDS, so the swizzle is
+  // applied to the units read: by an exclusive or, as row numbers are put
+  // together from disjoint bits. e4m3 ones go through registers, expanded on
+  // arrival. A lane's offset stays below 2^31 (16 stride_tok < 2^30).
+  constexpr int RPL = 64 / GPR;
+  const int l_row = lane / GPR, w_row = (w * WR) & 15;
+  const uint32_t l_st = (uint32_t)l_row * (uint32_t)a.c.st;
+  uint32_t k_from = 16 * (lane % GPR ^ (F8 ? 0 : k_swz(l_row)));
+  uint32_t v_from = 16 * (lane % GPR ^ (F8 ? 0 : v_swz(l_row)));
+  u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];
+  auto place = [&](int x, int e) {
     const int key = key_of(x) + 16 * grp;
-    const bool ok = e >= 0 && e < a.t.n_pages;
-    if (!ok && e != -2 && lane == 0) atomicOr(a.err, kErrPage);
-    if (lane == 0) s_ok[buf][w] = ok;
-    const int in = ok ? key - kv_entry(a.t, key) * a.t.ps : 0;
-    // a uniform base, and an offset of the lane below 2^31 (16 stride_tok < 2^30)
-    const long off = (ok ? e : 0) * a.c.sp + in * a.c.st;
-    const char* kp = kb + off;
-    const char* vp = vb + off;
+    const long in = there(e) ? e * a.c.sp + (key - kv_entry(a.t, key) * a.t.ps) * a.c.st : 0L;
+    return in + w_row * a.c.st;
+  };
+  auto issue = [&](const char* p, uint32_t from, char* to, u32x4* raw, auto swz) {
+    asm volatile("" : "+v"(from));               // offsets turned here, not kept
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int up = i * 64 + lane, kr = w * WR + up / GPR, u = up % GPR;
-      const uint32_t ro = (uint32_t)(kr & 15) * (uint32_t)a.c.st;
-      if constexpr (F8) {
-        rk[i] = *(const u32x4*)(kp + (ro + 16 * u));
-        rv[i] = *(const u32x4*)(vp + (ro + 16 * u));
-      } else {
-        const int at = (w * WR * UPR + i * 64) * 16;
+      const char* pi = p + i * RPL * a.c.st;
+      if constexpr (F8)
+        raw[i] = *(const u32x4*)(pi + (l_st + from));
+      else
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(kp + (ro + 16 * (u ^ k_swz(kr)))),
-            (__attribute__((address_space(3))) void*)(s_k[buf] + at), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(vp + (ro + 16 * (u ^ v_swz(kr)))),
-            (__attribute__((address_space(3))) void*)(s_v[buf] + at), 16, 0, 0);
-      }
+            (const __attribute__((address_space(1))) void*)(
+                pi + (l_st + (from ^ (uint32_t)(16 * swz(w_row + i * RPL))))),
+            (__attribute__((address_space(3))) void*)(to + (w * WR * UPR + i * 64) * 16), 16, 0,
+            0);
     }
   };
-  // completes them: waits, expands e4m3, takes masked values out of V
-  auto finish = [&](int x, int buf) {
-    const int key = key_of(x);
-    const bool whole = whole_of(key);
+  auto issue_k = [&](int x, int e, int buf) {
+    if (!there(e) && e != -2 && lane == 0) atomicOr(a.err, kErrPage);
+    if (lane == 0) s_ok[buf][w] = there(e);
+    issue(kb + place(x, e), k_from, s_k[buf], rk, k_swz);
+  };
+  auto issue_v = [&](int x, int e, int buf) {
+    issue(vb + place(x, e), v_from, s_v[buf], rv, v_swz);
+  };
+  auto expand = [&](const u32x4& raw, u32x4 (&y)[2]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e >> 1][2 * (e & 1)] = from_e4m3<BF, false>(raw[e]);
+      y[e >> 1][2 * (e & 1) + 1] = from_e4m3<BF, true>(raw[e]);
+    }
+  };
+  auto arrived = [&] {
+    if constexpr (!F8) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  auto finish_k = [&](int buf) {
     if constexpr (F8) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int up = i * 64 + lane, kr = w * WR + up / GPR, u = up % GPR;
-        u32x4 kk[2], vv[2];
+        u32x4 y[2];
+        expand(rk[i], y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kk[e >> 1][2 * (e & 1)] = from_e4m3<BF, false>(rk[i][e]);
-          kk[e >> 1][2 * (e & 1) + 1] = from_e4m3<BF, true>(rk[i][e]);
-          vv[e >> 1][2 * (e & 1)] = from_e4m3<BF, false>(rv[i][e]);
-          vv[e >> 1][2 * (e & 1) + 1] = from_e4m3<BF, true>(rv[i][e]);
-        }
+        for (int h = 0; h < 2; ++h)
+          *(u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ k_swz(kr))) = y[h];
+      }
+    }
+  };
+  // takes masked values out of V
+  auto finish_v = [&](int x, int e, int buf) {
+    const int key = key_of(x);
+    const bool ok = there(e), whole = whole_of(key) && ok;
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int up = i * 64 + lane, kr = w * WR + up / GPR, u = up % GPR;
+        u32x4 y[2];
+        expand(rv[i], y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!whole) vv[h] = clean(vv[h], key, kr);
-          *(u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ k_swz(kr))) = kk[h];
-          *(u32x4*)(s_v[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = vv[h];
+          if (!whole) y[h] = clean(y[h], key, kr, ok);
+          *(u32x4*)(s_v[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = y[h];
         }
       }
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      if (!whole) {
+    } else if (!whole) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          const int up = i * 64 + lane, kr = w * WR + up / GPR;
-          u32x4* p = (u32x4*)(s_v[buf] + (w * WR * UPR + up) * 16);
-          *p = clean(*p, key, kr);
-        }
+      for (int i = 0; i < NL; ++i) {
+        const int up = i * 64 + lane, kr = w * WR + up / GPR;
+        u32x4* p = (u32x4*)(s_v[buf] + (w * WR * UPR + up) * 16);
+        *p = clean(*p, key, kr, ok);
       }
     }
   };
 
-  int e_next = 0;
-  if (x0 < x1) {
-    issue(x0, fetch(x0), 0);
-    e_next = fetch(x0 + 1);
-  }
-  for (int x = x0; x < x1; ++x) {
-    const int key = key_of(x), buf = (x - x0) & 1;
-    finish(x, buf);
-    __syncthreads();
-    // the other buffer's tile is done with: every wave has passed the barrier
-    if (x + 1 < x1) {
-      issue(x + 1, e_next, buf ^ 1);
-      e_next = fetch(x + 2);
-    }
-    if (idle || key > wp_max || (key + BN <= wlo_min && key >= a.first)) continue;
+  // S^T of a tile, unscaled
+  auto scores = [&](f32x16 (&s)[NA], int buf) {
+    asm volatile("" : "+v"(k_at));               // not 2 x NC addresses kept in registers
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int aa = 0; aa < NA; ++aa) {
+        const u32x4 ka = *(const u32x4*)(s_k[buf] + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
+        const f32x16 zero = {};
+        s[aa] = mfma32<BF>(ka, q[c], c == 0 ? zero : s[aa]);
+      }
+  };
+  // masks them, and lets m, l and O follow the maximum
+  auto settle = [&](f32x16 (&s)[NA], int x, int buf) {
+    const int key = key_of(x);
     uint32_t gone = 0;                           // 16-key groups without a page
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (!s_ok[buf][i]) gone |= 1u << (i * WR / 16);
-    const bool whole = !gone && key + BN - 1 <= wp_min && (key >= wlo_max || key + BN <= a.first);
-
-    f32x16 s[RB][NA];
-#pragma unroll
-    for (int aa = 0; aa < NA; ++aa) {
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[rb][aa][i] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int kr = 32 * aa + l31;
-        const u32x4 ka =
-            *(const u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * c + half) ^ k_swz(kr)));
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) s[rb][aa] = mfma32<BF>(ka, q[rb][c], s[rb][aa]);
-      }
-    }
-    if (!whole) {
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int aa = 0; aa < NA; ++aa)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int kk = 32 * aa + 8 * (i >> 2) + (i & 3), at = key + 4 * half;
-            const bool ok = kk <= pos[rb] - at && (kk >= lo[rb] - at || kk < a.first - at) &&
-                            !((gone >> (kk >> 4)) & 1);
-            if (!ok) s[rb][aa][i] = kNegInf;
-          }
-    }
-    float bm[RB];
-    bool grown = false;
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      bm[rb] = s[rb][0][0];
-#pragma unroll
-      for (int aa = 0; aa < NA; ++aa)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) bm[rb] = fmaxf(bm[rb], s[rb][aa][i]);
-      bm[rb] = xor32_reduce(bm[rb], OpMax{});
-      grown |= bm[rb] > m[rb] + thr;
-    }
-    if (__any(grown)) {
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        const float mn = fmaxf(m[rb], bm[rb]);
-        const float f = exp2_fast((m[rb] - (mn == kNegInf ? 0.0f : mn)) * sc);
-        m[rb] = mn;
-        l[rb] *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[rb][d][i] *= f;
-      }
-    }
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const float neg = m[rb] == kNegInf ? 0.0f : -m[rb] * sc;
+    gone = __builtin_amdgcn_readfirstlane(gone);
+    if (gone || key + BN - 1 > wp_min || !(key >= wlo_max || key + BN <= a.first)) {
+      // selects, no branches: a branch per element would copy the tile
+      const int at = key + 4 * half, hi = pos - at, below = lo - at, kept = a.first - at;
 #pragma unroll
       for (int aa = 0; aa < NA; ++aa)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[rb][aa][i] = exp2_fast(__builtin_fmaf(s[rb][aa][i], sc, neg));
-          l[rb] += s[rb][aa][i];
+          const int kk = 32 * aa + 8 * (i >> 2) + (i & 3);
+          const bool ok = (kk <= hi) & ((kk >= below) | (kk < kept)) &
+                          !((gone >> (2 * aa + (i >> 3))) & 1);
+          s[aa][i] = ok ? s[aa][i] : kNegInf;
         }
     }
-
+    float bm = s[0][0];
+#pragma unroll
+    for (int aa = 0; aa < NA; ++aa)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) bm = fmaxf(bm, s[aa][i]);
+    bm = xor32_reduce(bm, OpMax{});
+    if (__any(bm > m + thr)) {
+      const float mn = fmaxf(m, bm);
+      const float f = exp2_fast((m - (mn == kNegInf ? 0.0f : mn)) * sc);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+  };
+  // P of a tile, its sum, and its product with V
+  auto accumulate = [&](f32x16 (&s)[NA], int buf) {
+    asm volatile("" : "+v"(v_at));
+    const float neg = m == kNegInf ? 0.0f : -m * sc;
 #pragma unroll
     for (int aa = 0; aa < NA; ++aa)
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        u32x4 pb[RB];
+        u32x4 pb;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            pb[rb][j] = pack16<BF>(s[rb][aa][8 * st + 2 * j], s[rb][aa][8 * st + 2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          const float p0 = exp2_fast(__builtin_fmaf(s[aa][8 * st + 2 * j], sc, neg));
+          const float p1 = exp2_fast(__builtin_fmaf(s[aa][8 * st + 2 * j + 1], sc, neg));
+          l += p0;
+          l += p1;
+          pb[j] = pack16<BF>(p0, p1);
+        }
         // keys 4 half + 0..3 of the 16-key step, then the same + 8; lane i of
         // 16 reads row i / 4, 4 values from 4 (i % 4), and gets column i
-        const int k0 = 32 * aa + 16 * st + 4 * half + ((lane & 15) >> 2);
-        const int dc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
           u32x4 va;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int kr = k0 + 8 * h;
-            const int b = 2 * (32 * d + dc);      // byte in the row
-            char* p = s_v[buf] + kr * (2 * D) + (16 * ((b >> 4) ^ v_swz(kr)) + (b & 15));
+            char* p = s_v[buf] + (32 * aa + 16 * st + 8 * h) * (2 * D) + (v_at ^ (64 * d));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4*)p);
             const u32x2 z = __builtin_bit_cast(u32x2, y);
             va[2 * h] = z[0];
             va[2 * h + 1] = z[1];
           }
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) o[rb][d] = mfma32<BF>(va, pb[rb], o[rb][d]);
+          o[d] = mfma32<BF>(va, pb, o[d]);
         }
       }
+  };
+
+  // Tile x's second product runs with tile x + 1's first, so that one's
+  // exponentials fill the other's matrix instructions. Iteration x waits for
+  // K of x + 1 and V of x and starts the loads of K of x + 2 and V of x + 1,
+  // into the buffers that iteration x - 1 read last.
+  f32x16 sa[NA], sb[NA];
+  int e0 = -2, e1 = -2, e2 = -2;                 // table entries of x, x + 1, x + 2
+  int x = x0;
+  auto step = [&](f32x16 (&s)[NA], f32x16 (&sn)[NA], int buf) {
+    arrived();
+    finish_k(buf ^ 1);
+    if (x > x0) finish_v(x, e0, buf);
+    __syncthreads();
+    if (x + 2 < x1) issue_k(x + 2, e2, buf);
+    issue_v(x + 1, e1, buf ^ 1);
+    e0 = e1;
+    e1 = e2;
+    e2 = fetch(x + 3);
+    scores(sn, buf ^ 1);
+    accumulate(s, buf);
+    settle(sn, x + 1, buf ^ 1);
+    ++x;
+  };
+  auto last = [&](f32x16 (&s)[NA], int buf) {
+    if (x > x0) {
+      arrived();
+      finish_v(x, e0, buf);
+      __syncthreads();
+    }
+    accumulate(s, buf);
+  };
+  if (x0 < x1) {
+    e0 = fetch(x0);
+    e1 = fetch(x0 + 1);
+    issue_k(x0, e0, 0);
+    issue_v(x0, e0, 0);
+    arrived();
+    finish_k(0);
+    finish_v(x0, e0, 0);
+    __syncthreads();
+    if (x0 + 1 < x1) issue_k(x0 + 1, e1, 1);
+    e2 = fetch(x0 + 2);
+    scores(sa, 0);
+    settle(sa, x0, 0);
+    while (x + 2 < x1) {
+      step(sa, sb, 0);
+      step(sb, sa, 1);
+    }
+    if (x + 1 < x1) {
+      step(sa, sb, 0);
+      last(sb, 1);
+    } else {
+      last(sa, 0);
+    }
   }
 
   // values of V that are not finite and were staged as zeros: their products,
   // for the rows that see their key
   __syncthreads();
-  if (s_bad && !idle) {
-    for (int x = x0; x < x1; ++x) {
-      const int key = key_of(x);
-      if (whole_of(key)) continue;
+  if (s_bad) {
+    for (int xx = x0; xx < x1; ++xx) {
+      const int key = key_of(xx);
       for (int j = key; j < key + BN; ++j) {
         if (j > t.p_max || !(j >= t.lo_min || j < a.first)) continue;
         const int e = kv_entry(a.t, j), p = row[e];
-        if (p < 0 || p >= a.t.n_pages) continue;
+        // in a whole tile only the groups of a wave that missed its page were
+        // staged anew, all zeros
+        if (!there(p) || whole_of(key)) continue;
         const long off = p * a.c.sp + (long)(j - e * a.t.ps) * a.c.st;
         auto value = [&](const char* base, int dd) {
           uint32_t x16;
@@ -432,67 +474,59 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
 #pragma unroll 1
         for (int dd = lane; dd < D; dd += 64) any |= !finite(value(vb, dd));
         if (!__any(any)) continue;
+        float dot = 0.0f;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          float dot = 0.0f;
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t q16 = (q[c][i >> 1] >> (16 * (i & 1))) & 0xFFFF;
+            dot += value(kb, 16 * c + 8 * half + i) *
+                   (BF ? bf16_bits_to_f32(q16)
+                       : (float)__builtin_bit_cast(_Float16, (uint16_t)q16));
+          }
+        dot = xor32_reduce(dot, OpSum{});
+        const bool sees = j <= pos && (j >= lo || j < a.first);
+        const float pv = exp2_fast(__builtin_fmaf(dot, sc, m == kNegInf ? 0.0f : -m * sc));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t q16 = (q[rb][c][i >> 1] >> (16 * (i & 1))) & 0xFFFF;
-              dot += value(kb, 16 * c + 8 * half + i) *
-                     (BF ? bf16_bits_to_f32(q16)
-                         : (float)__builtin_bit_cast(_Float16, (uint16_t)q16));
-            }
-          dot = xor32_reduce(dot, OpSum{});
-          const bool sees = j <= pos[rb] && (j >= lo[rb] || j < a.first);
-          const float pv = exp2_fast(
-              __builtin_fmaf(dot, sc, m[rb] == kNegInf ? 0.0f : -m[rb] * sc));
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float f = value(vb, 32 * d + 8 * (i >> 2) + 4 * half + (i & 3));
-              if (sees && !finite(f)) o[rb][d][i] += pv * f;
-              if (i == 15) __builtin_amdgcn_sched_barrier(0);
-            }
-        }
+          for (int i = 0; i < 16; ++i) {
+            const float f = value(vb, 32 * d + 8 * (i >> 2) + 4 * half + (i & 3));
+            if (sees && !finite(f)) o[d][i] += pv * f;
+            if (i == 15) __builtin_amdgcn_sched_barrier(0);
+          }
       }
     }
   }
 
+  l = xor32_reduce(l, OpSum{});
+  if (!have) return;
+  if (parts == 1) {
+    float inv = l == 0.0f ? 0.0f : 1.0f / l;     // no visible key: 0
+    if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
+    char* dst = a.out + qrow * a.o_row + head * a.o_head;
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    l[rb] = xor32_reduce(l[rb], OpSum{});
-    if (!have[rb]) continue;
-    if (parts == 1) {
-      float inv = l[rb] == 0.0f ? 0.0f : 1.0f / l[rb];      // no visible key: 0
-      if (F8 && l[rb] != 0.0f) inv *= a.c.vs[kvh];
-      char* dst = a.out + qrow[rb] * a.o_row + head[rb] * a.o_head;
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const u32x2 y = {pack16<BF>(o[rb][d][i] * inv, o[rb][d][i + 1] * inv),
-                           pack16<BF>(o[rb][d][i + 2] * inv, o[rb][d][i + 3] * inv)};
-          *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
-        }
-      if (a.lse && half == 0)
-        a.lse[qrow[rb] * a.hq + head[rb]] = (m[rb] * sc + __builtin_amdgcn_logf(l[rb])) * kLn2;
-    } else {
-      const long rows = a.T * a.hq, ri = qrow[rb] * a.hq + head[rb];
-      float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *(f32x4*)(dst + 32 * d + 2 * i + 4 * half) =
-              f32x4{o[rb][d][i], o[rb][d][i + 1], o[rb][d][i + 2], o[rb][d][i + 3]};
-      if (half == 0) {
-        float* ml = a.part + (long)a.n_split * rows * D + ((long)blockIdx.y * rows + ri) * 2;
-        ml[0] = m[rb] * sc;
-        ml[1] = l[rb];
+      for (int i = 0; i < 16; i += 4) {
+        const u32x2 y = {pack16<BF>(o[d][i] * inv, o[d][i + 1] * inv),
+                         pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
       }
+    if (a.lse && half == 0) a.lse[qrow * a.hq + head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
+  } else {
+    const long rows = a.T * a.hq, ri = qrow * a.hq + head;
+    float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *(f32x4*)(dst + 32 * d + 2 * i + 4 * half) =
+            f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+    if (half == 0) {
+      float* ml = a.part + (long)a.n_split * rows * D + ((long)blockIdx.y * rows + ri) * 2;
+      ml[0] = m * sc;
+      ml[1] = l;
     }
   }
 }
@@ -551,7 +585,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
 
 template <bool BF, bool F8, int D>
 hipError_t run_prefill(const AttnArgs& a, hipStream_t s) {
-  const long tiles = prefill_tiles(a.n, a.T, a.g, D);
+  const long tiles = prefill_tiles(a.n, a.T, a.g);
   attn_prefill_kernel<BF, F8, D>
       <<<dim3((unsigned)(tiles * a.c.hkv), a.n_split), 256, 0, s>>>(a);
   if (a.n_split > 1)

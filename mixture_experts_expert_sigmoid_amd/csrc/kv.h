@@ -64,14 +64,14 @@ constexpr int kDecKeys = 32;            // keys of one wave's step
 size_t decode_ws_bytes(long n, int hq, int hkv, int D);
 hipError_t launch_attn_decode(const AttnArgs& a, int fmt, hipStream_t s);
 
-// Prefill: tiles of prefill_rows(D) rows, a row being a (token, query head)
-// pair of one key-value head; when the tiles cannot fill the GPU the keys of
-// each are split over up to prefill_splits workgroups, whose partial results
-// (fp32 rows, maxima, sums) the join kernel adds in order.
-constexpr int prefill_rows(int D) { return D == 64 ? 256 : 128; }
+// Prefill: tiles of kPreRows rows, a row being a (token, query head) pair of
+// one key-value head; when the tiles cannot fill the GPU the keys of each are
+// split over up to prefill_splits workgroups, whose partial results (fp32
+// rows, maxima, sums) the join kernel adds in order.
+constexpr int kPreRows = 128;
 // tiles that n sequences of T tokens can have, per key-value head
-inline long prefill_tiles(long n, long T, int g, int D) { return T * g / prefill_rows(D) + n; }
-int prefill_splits(long n, long T, int hq, int hkv, int D);
+inline long prefill_tiles(long n, long T, int g) { return T * g / kPreRows + n; }
+int prefill_splits(long n, long T, int hq, int hkv);
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 
