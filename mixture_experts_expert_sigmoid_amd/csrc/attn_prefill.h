@@ -96,8 +96,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   constexpr int TB = BN * D * 2;                 // bytes of a tile in LDS
   static_assert(NL >= 1, "tile");
 
-  __shared__ __align__(16) char s_k[2][TB];
-  __shared__ __align__(16) char s_v[2][TB];
+  __shared__ __align__(16) char s_k0[TB], s_k1[TB], s_v0[TB], s_v1[TB];
   __shared__ int s_ok[2][4];                     // page there, by bringing wave
   __shared__ int s_bad;                          // values of V not finite were taken out
 
@@ -249,13 +248,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
             0);
     }
   };
-  auto issue_k = [&](int x, int e, int buf) {
+  auto issue_k = [&](int x, int e, char* to, int* ok) {
     if (!there(e) && e != -2 && lane == 0) atomicOr(a.err, kErrPage);
-    if (lane == 0) s_ok[buf][w] = there(e);
-    issue(kb + place(x, e), k_from, s_k[buf], rk, k_swz);
+    if (lane == 0) ok[w] = there(e);
+    issue(kb + place(x, e), k_from, to, rk, k_swz);
   };
-  auto issue_v = [&](int x, int e, int buf) {
-    issue(vb + place(x, e), v_from, s_v[buf], rv, v_swz);
+  auto issue_v = [&](int x, int e, char* to) {
+    issue(vb + place(x, e), v_from, to, rv, v_swz);
   };
   auto expand = [&](const u32x4& raw, u32x4 (&y)[2]) {
 #pragma unroll
@@ -267,7 +266,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   auto arrived = [&] {
     if constexpr (!F8) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
-  auto finish_k = [&](int buf) {
+  auto finish_k = [&](char* to) {
     if constexpr (F8) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -276,12 +275,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
         expand(rk[i], y);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *(u32x4*)(s_k[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ k_swz(kr))) = y[h];
+          *(u32x4*)(to + kr * (2 * D) + 16 * ((2 * u + h) ^ k_swz(kr))) = y[h];
       }
     }
   };
   // takes masked values out of V
-  auto finish_v = [&](int x, int e, int buf) {
+  auto finish_v = [&](int x, int e, char* to) {
     const int key = key_of(x);
     const bool ok = there(e), whole = whole_of(key) && ok;
     if constexpr (F8) {
@@ -293,38 +292,38 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!whole) y[h] = clean(y[h], key, kr, ok);
-          *(u32x4*)(s_v[buf] + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = y[h];
+          *(u32x4*)(to + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = y[h];
         }
       }
     } else if (!whole) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int up = i * 64 + lane, kr = w * WR + up / GPR;
-        u32x4* p = (u32x4*)(s_v[buf] + (w * WR * UPR + up) * 16);
+        u32x4* p = (u32x4*)(to + (w * WR * UPR + up) * 16);
         *p = clean(*p, key, kr, ok);
       }
     }
   };
 
   // S^T of a tile, unscaled
-  auto scores = [&](f32x16 (&s)[NA], int buf) {
+  auto scores = [&](f32x16 (&s)[NA], const char* from) {
     asm volatile("" : "+v"(k_at));               // not 2 x NC addresses kept in registers
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int aa = 0; aa < NA; ++aa) {
-        const u32x4 ka = *(const u32x4*)(s_k[buf] + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
+        const u32x4 ka = *(const u32x4*)(from + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
         const f32x16 zero = {};
         s[aa] = mfma32<BF>(ka, q[c], c == 0 ? zero : s[aa]);
       }
   };
   // masks them, and lets m, l and O follow the maximum
-  auto settle = [&](f32x16 (&s)[NA], int x, int buf) {
+  auto settle = [&](f32x16 (&s)[NA], int x, const int* there_w) {
     const int key = key_of(x);
     uint32_t gone = 0;                           // 16-key groups without a page
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (!s_ok[buf][i]) gone |= 1u << (i * WR / 16);
+      if (!there_w[i]) gone |= 1u << (i * WR / 16);
     gone = __builtin_amdgcn_readfirstlane(gone);
     if (gone || key + BN - 1 > wp_min || !(key >= wlo_max || key + BN <= a.first)) {
       // selects, no branches: a branch per element would copy the tile
@@ -357,7 +356,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     }
   };
   // P of a tile, its sum, and its product with V
-  auto accumulate = [&](f32x16 (&s)[NA], int buf) {
+  auto accumulate = [&](f32x16 (&s)[NA], const char* from) {
     asm volatile("" : "+v"(v_at));
     const float neg = m == kNegInf ? 0.0f : -m * sc;
 #pragma unroll
@@ -380,9 +379,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
           u32x4 va;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            char* p = s_v[buf] + (32 * aa + 16 * st + 8 * h) * (2 * D) + (v_at ^ (64 * d));
+            const char* p = from + (32 * aa + 16 * st + 8 * h) * (2 * D) + (v_at ^ (64 * d));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)p);
+                (__attribute__((address_space(3))) s16x4*)const_cast<char*>(p));
             const u32x2 z = __builtin_bit_cast(u32x2, y);
             va[2 * h] = z[0];
             va[2 * h + 1] = z[1];
@@ -399,51 +398,54 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   f32x16 sa[NA], sb[NA];
   int e0 = -2, e1 = -2, e2 = -2;                 // table entries of x, x + 1, x + 2
   int x = x0;
-  auto step = [&](f32x16 (&s)[NA], f32x16 (&sn)[NA], int buf) {
+  // kx, vx: tile x's K and V; kn, vn: tile x + 1's. Distinct buffers, told so
+  // that reads do not wait for the loads in flight into the others.
+  auto step = [&](f32x16 (&s)[NA], f32x16 (&sn)[NA], char* __restrict kx, char* __restrict kn,
+                  char* __restrict vx, char* __restrict vn, int* okx, int* okn) {
     arrived();
-    finish_k(buf ^ 1);
-    if (x > x0) finish_v(x, e0, buf);
+    finish_k(kn);
+    if (x > x0) finish_v(x, e0, vx);
     __syncthreads();
-    if (x + 2 < x1) issue_k(x + 2, e2, buf);
-    issue_v(x + 1, e1, buf ^ 1);
+    if (x + 2 < x1) issue_k(x + 2, e2, kx, okx);
+    issue_v(x + 1, e1, vn);
     e0 = e1;
     e1 = e2;
     e2 = fetch(x + 3);
-    scores(sn, buf ^ 1);
-    accumulate(s, buf);
-    settle(sn, x + 1, buf ^ 1);
+    scores(sn, kn);
+    accumulate(s, vx);
+    settle(sn, x + 1, okn);
     ++x;
   };
-  auto last = [&](f32x16 (&s)[NA], int buf) {
+  auto last = [&](f32x16 (&s)[NA], char* vx) {
     if (x > x0) {
       arrived();
-      finish_v(x, e0, buf);
+      finish_v(x, e0, vx);
       __syncthreads();
     }
-    accumulate(s, buf);
+    accumulate(s, vx);
   };
   if (x0 < x1) {
     e0 = fetch(x0);
     e1 = fetch(x0 + 1);
-    issue_k(x0, e0, 0);
-    issue_v(x0, e0, 0);
+    issue_k(x0, e0, s_k0, s_ok[0]);
+    issue_v(x0, e0, s_v0);
     arrived();
-    finish_k(0);
-    finish_v(x0, e0, 0);
+    finish_k(s_k0);
+    finish_v(x0, e0, s_v0);
     __syncthreads();
-    if (x0 + 1 < x1) issue_k(x0 + 1, e1, 1);
+    if (x0 + 1 < x1) issue_k(x0 + 1, e1, s_k1, s_ok[1]);
     e2 = fetch(x0 + 2);
-    scores(sa, 0);
-    settle(sa, x0, 0);
+    scores(sa, s_k0);
+    settle(sa, x0, s_ok[0]);
     while (x + 2 < x1) {
-      step(sa, sb, 0);
-      step(sb, sa, 1);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_ok[0], s_ok[1]);
+      step(sb, sa, s_k1, s_k0, s_v1, s_v0, s_ok[1], s_ok[0]);
     }
     if (x + 1 < x1) {
-      step(sa, sb, 0);
-      last(sb, 1);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_ok[0], s_ok[1]);
+      last(sb, s_v1);
     } else {
-      last(sa, 0);
+      last(sa, s_v0);
     }
   }
 
