@@ -28,6 +28,8 @@
 // short ones. Few tiles: the keys of each are split over workgroups and the
 // parts joined in order.
 #pragma once
+#include <type_traits>
+
 #include "attn_dev.h"
 
 namespace moe {
@@ -97,7 +99,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   static_assert(NL >= 1, "tile");
 
   __shared__ __align__(16) char s_k0[TB], s_k1[TB], s_v0[TB], s_v1[TB];
-  __shared__ int s_ok[2][4];                     // page there, by bringing wave
+  __shared__ int s_gone;                         // last tile with a group that has no page
+  __shared__ int s_miss[2][4];                   // the same for each wave's group, by buffer
   __shared__ int s_bad;                          // values of V not finite were taken out
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -123,13 +126,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
   const int x1 = (int)((long)(blockIdx.y + 1) * t.nb / parts);
-  if (tid == 0) s_bad = 0;
+  if (tid < 8) s_miss[tid >> 2][tid & 3] = -1;
+  if (tid == 0) {
+    s_gone = -1;
+    s_bad = 0;
+  }
 
-  // the wave's rows and what they see
-  const int r0 = t.tile * ROWS + w * 32;
-  const int wp_min = t.L - t.m + min(r0, t.rows - 1) / a.g;
-  const int wp_max = t.L - t.m + (min(r0 + 32, t.rows) - 1) / a.g;
-  const int wlo_max = a.window ? max(0, wp_max - a.window + 1) : 0;
 
   // scores are compared unscaled: the sign of the scale goes into q
   float sc = F8 ? a.scale * a.c.ks[kvh] : a.scale;
@@ -139,7 +141,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   const float thr = fminf(8.0f / sc, 1e30f);
 
   // this lane's row
-  const int r = r0 + l31;
+  const int r = t.tile * ROWS + w * 32 + l31;
   const bool have = r < t.rows;
   const int tok = have ? r / a.g : 0;
   const int head = kvh * a.g + (have ? r - tok * a.g : 0);
@@ -164,26 +166,42 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = kNegInf, l = 0.0f;
 
-  // the sequence's table row; no kernel that runs beside this one writes it,
-  // so its entries come by scalar loads, which do not wait for the tiles'
-  typedef const __attribute__((address_space(4))) int* ConstInts;
-  const ConstInts row =
-      (ConstInts)(uintptr_t)(a.t.table + (long)max(0, t.slot) * a.t.ld);
+  const int* row = a.t.table + (long)max(0, t.slot) * a.t.ld;
   const char* kb = a.c.k + kvh * a.c.sh;
   const char* vb = a.c.v + kvh * a.c.sh;
   const int grp = w * WR / 16;                   // 16-key group that this wave brings from
 
   auto key_of = [&](int x) { return BN * (x < t.nb1 ? x : t.b2 + x - t.nb1); };
-  // table entry of the wave's group of tile x; -2: nothing of it is visible
-  auto fetch = [&](int x) {
-    const int key = key_of(x) + 16 * grp;
-    const bool seen = x < x1 && key <= t.p_max && (key + 16 > t.lo_min || key < a.first);
-    return seen ? row[kv_entry(a.t, key)] : -2;
+  // tiles of which every row sees every key (some of the first keys' tiles
+  // may be such too, and are treated as if not)
+  const int whole0 = t.nb1 - t.b2 + (t.lo_max + BN - 1) / BN;
+  const int whole1 = t.nb1 - t.b2 + (t.p_min + 1) / BN;
+  auto whole = [&](int x) { return x >= t.nb1 && x >= whole0 && x < whole1; };
+
+  // Byte offset in the cache of the wave's group of the next 64 tiles, a tile
+  // a lane; kMissing: no page, kUnseen: nothing of it is visible. One lookup a
+  // tile is then two lane reads.
+  constexpr long kMissing = -(1L << 32), kUnseen = -(2L << 32);
+  struct Group {
+    long off;                                    // 0 without a page
+    int state;                                   // < 0 without one: high word of the above
   };
-  auto there = [&](int e) { return e >= 0 && e < a.t.n_pages; };
-  // every row of the tile sees every key of tile x
-  auto whole_of = [&](int key) {
-    return key + BN - 1 <= t.p_min && (key >= t.lo_max || key + BN <= a.first);
+  int at0 = x0;
+  auto lookup = [&](int x) {
+    const int key = key_of(x) + 16 * grp;
+    if (x >= x1 || key > t.p_max || !(key + 16 > t.lo_min || key < a.first)) return kUnseen;
+    const int i = kv_entry(a.t, key), e = row[i];
+    return e >= 0 && e < a.t.n_pages ? e * a.c.sp + (key - i * a.t.ps) * a.c.st : kMissing;
+  };
+  long offs = lookup(x0 + lane);
+  auto group_of = [&](int x) {                   // x one after another
+    if (x - at0 == 64) {
+      at0 = x;
+      offs = lookup(x + lane);
+    }
+    const uint32_t lo32 = __builtin_amdgcn_readlane((int)offs, x - at0);
+    const int hi32 = __builtin_amdgcn_readlane((int)(offs >> 32), x - at0);
+    return Group{(long)(((uint64_t)(uint32_t)max(hi32, 0) << 32) | lo32), hi32};
   };
   // swizzle of 16-byte units by row (of the tile)
   auto k_swz = [](int kr) { return kr & (UPR < 16 ? UPR - 1 : 15); };
@@ -219,43 +237,41 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
 
   // The wave's rows of a tile: load i takes RPL of them, row i RPL + lane /
   // GPR of the wave. 16-bit caches load straight into LDS, so the swizzle is
-  // applied to the units read: by an exclusive or, as row numbers are put
-  // together from disjoint bits. e4m3 ones go through registers, expanded on
+  // applied to the units read. e4m3 ones go through registers, expanded on
   // arrival. A lane's offset stays below 2^31 (16 stride_tok < 2^30).
   constexpr int RPL = 64 / GPR;
   const int l_row = lane / GPR, w_row = (w * WR) & 15;
-  const uint32_t l_st = (uint32_t)l_row * (uint32_t)a.c.st;
-  uint32_t k_from = 16 * (lane % GPR ^ (F8 ? 0 : k_swz(l_row)));
-  uint32_t v_from = 16 * (lane % GPR ^ (F8 ? 0 : v_swz(l_row)));
+  uint32_t k_from[NL], v_from[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int rr = w_row + i * RPL + l_row;
+    k_from[i] = (uint32_t)rr * (uint32_t)a.c.st + 16 * (lane % GPR ^ (F8 ? 0 : k_swz(rr)));
+    v_from[i] = (uint32_t)rr * (uint32_t)a.c.st + 16 * (lane % GPR ^ (F8 ? 0 : v_swz(rr)));
+  }
   u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];
-  auto place = [&](int x, int e) {
-    const int key = key_of(x) + 16 * grp;
-    const long in = there(e) ? e * a.c.sp + (key - kv_entry(a.t, key) * a.t.ps) * a.c.st : 0L;
-    return in + w_row * a.c.st;
-  };
-  auto issue = [&](const char* p, uint32_t from, char* to, u32x4* raw, auto swz) {
-    asm volatile("" : "+v"(from));               // offsets turned here, not kept
+  auto issue = [&](const char* p, const uint32_t (&from)[NL], char* to, u32x4* raw) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const char* pi = p + i * RPL * a.c.st;
+      uint32_t f = from[i];
+      asm volatile("" : "+v"(f));                // added by the load, not ahead of it
       if constexpr (F8)
-        raw[i] = *(const u32x4*)(pi + (l_st + from));
+        raw[i] = *(const u32x4*)(p + f);
       else
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(
-                pi + (l_st + (from ^ (uint32_t)(16 * swz(w_row + i * RPL))))),
+            (const __attribute__((address_space(1))) void*)(p + f),
             (__attribute__((address_space(3))) void*)(to + (w * WR * UPR + i * 64) * 16), 16, 0,
             0);
     }
   };
-  auto issue_k = [&](int x, int e, char* to, int* ok) {
-    if (!there(e) && e != -2 && lane == 0) atomicOr(a.err, kErrPage);
-    if (lane == 0) ok[w] = there(e);
-    issue(kb + place(x, e), k_from, to, rk, k_swz);
+  auto issue_k = [&](int x, const Group& gr, char* to, int* miss) {
+    if (gr.state == (int)(kMissing >> 32) && lane == 0) {
+      atomicOr(a.err, kErrPage);
+      s_gone = x;
+      miss[w] = x;
+    }
+    issue(kb + gr.off, k_from, to, rk);
   };
-  auto issue_v = [&](int x, int e, char* to) {
-    issue(vb + place(x, e), v_from, to, rv, v_swz);
-  };
+  auto issue_v = [&](const Group& gr, char* to) { issue(vb + gr.off, v_from, to, rv); };
   auto expand = [&](const u32x4& raw, u32x4 (&y)[2]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -280,9 +296,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
     }
   };
   // takes masked values out of V
-  auto finish_v = [&](int x, int e, char* to) {
+  auto finish_v = [&](int x, const Group& gr, char* to) {
     const int key = key_of(x);
-    const bool ok = there(e), whole = whole_of(key) && ok;
+    const bool as_is = whole(x) && gr.state >= 0;
     if constexpr (F8) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -291,43 +307,63 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
         expand(rv[i], y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!whole) y[h] = clean(y[h], key, kr, ok);
+          if (!as_is) y[h] = clean(y[h], key, kr, gr.state >= 0);
           *(u32x4*)(to + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = y[h];
         }
       }
-    } else if (!whole) {
+    } else if (!as_is) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int up = i * 64 + lane, kr = w * WR + up / GPR;
         u32x4* p = (u32x4*)(to + (w * WR * UPR + up) * 16);
-        *p = clean(*p, key, kr, ok);
+        *p = clean(*p, key, kr, gr.state >= 0);
       }
     }
   };
 
+  // Operand c, aa of the first product: 8 values of D of 32 keys
+  auto read_k = [&](const char* from, int c, int aa) {
+    return *(const u32x4*)(from + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
+  };
+  // Operand of the second product: keys 4 half + 0..3 of the gth 16-key step,
+  // then the same + 8; lane i of 16 reads row i / 4, 4 values from 4 (i % 4),
+  // and gets column i
+  auto read_v = [&](const char* from, int g, int d) {
+    u32x4 va;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const char* p = from + (16 * g + 8 * h) * (2 * D) + (v_at ^ (64 * d));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)const_cast<char*>(p));
+      const u32x2 z = __builtin_bit_cast(u32x2, y);
+      va[2 * h] = z[0];
+      va[2 * h + 1] = z[1];
+    }
+    return va;
+  };
   // S^T of a tile, unscaled
   auto scores = [&](f32x16 (&s)[NA], const char* from) {
-    asm volatile("" : "+v"(k_at));               // not 2 x NC addresses kept in registers
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int aa = 0; aa < NA; ++aa) {
-        const u32x4 ka = *(const u32x4*)(from + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
         const f32x16 zero = {};
-        s[aa] = mfma32<BF>(ka, q[c], c == 0 ? zero : s[aa]);
+        s[aa] = mfma32<BF>(read_k(from, c, aa), q[c], c == 0 ? zero : s[aa]);
       }
   };
   // masks them, and lets m, l and O follow the maximum
-  auto settle = [&](f32x16 (&s)[NA], int x, const int* there_w) {
-    const int key = key_of(x);
-    uint32_t gone = 0;                           // 16-key groups without a page
+  auto settle = [&](f32x16 (&s)[NA], int x, int gone_tile, const int* miss) {
+    const bool miss_any = __builtin_amdgcn_readfirstlane(gone_tile) >= x;
+    if (miss_any || !whole(x)) {
+      uint32_t gone = 0;                         // 16-key groups without a page
+      if (miss_any) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!there_w[i]) gone |= 1u << (i * WR / 16);
-    gone = __builtin_amdgcn_readfirstlane(gone);
-    if (gone || key + BN - 1 > wp_min || !(key >= wlo_max || key + BN <= a.first)) {
+        for (int i = 0; i < 4; ++i)
+          if (miss[i] == x) gone |= 1u << (i * WR / 16);
+        gone = __builtin_amdgcn_readfirstlane(gone);
+      }
       // selects, no branches: a branch per element would copy the tile
-      const int at = key + 4 * half, hi = pos - at, below = lo - at, kept = a.first - at;
+      const int at = key_of(x) + 4 * half, hi = pos - at, below = lo - at, kept = a.first - at;
 #pragma unroll
       for (int aa = 0; aa < NA; ++aa)
 #pragma unroll
@@ -355,40 +391,55 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
   };
-  // P of a tile, its sum, and its product with V
-  auto accumulate = [&](f32x16 (&s)[NA], const char* from) {
-    asm volatile("" : "+v"(v_at));
+  // P of a tile (s), its sum and its product with V (vx), and beside them, if
+  // NEXT, S^T of the next tile (sn) from its K (kn). One matrix instruction
+  // after another, each with the read of the operand that is due kAhead of
+  // them later and a share of the exponentials behind it: the order is kept
+  // as written, since the reads' latency (some 130 cycles) and the vector
+  // work both have to go under matrix instructions of 32 cycles.
+  constexpr int kAhead = 4;
+  auto products = [&](auto next, f32x16 (&s)[NA], f32x16 (&sn)[NA], const char* kn,
+                      const char* vx) {
+    constexpr bool NEXT = decltype(next)::value;
+    constexpr int MQ = NEXT ? NA * NC : 0, MV = 2 * NA * ND, NE = 16 * NA;
+    asm volatile("" : "+v"(k_at), "+v"(v_at));   // not 2 x NC addresses kept in registers
     const float neg = m == kNegInf ? 0.0f : -m * sc;
+    u32x4 op[MQ + MV], pb[2 * NA];
+    float p0 = 0.0f;
+    auto read = [&](int i) {
+      op[i] = i < MQ ? read_k(kn, i / NA, i % NA) : read_v(vx, (i - MQ) / ND, (i - MQ) % ND);
+    };
+    // probabilities come before the step that needs them: 8 for each ND of MV
+    auto element = [&](int e) {
+      const float pe = exp2_fast(__builtin_fmaf(s[e >> 4][e & 15], sc, neg));
+      l += pe;
+      if (e & 1) pb[e >> 3][(e & 7) >> 1] = pack16<BF>(p0, pe);
+      p0 = pe;
+    };
+    if (!NEXT) {
 #pragma unroll
-    for (int aa = 0; aa < NA; ++aa)
+      for (int e = 0; e < 8; ++e) element(e);
+    }
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        u32x4 pb;
+    for (int i = 0; i < kAhead; ++i) read(i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p0 = exp2_fast(__builtin_fmaf(s[aa][8 * st + 2 * j], sc, neg));
-          const float p1 = exp2_fast(__builtin_fmaf(s[aa][8 * st + 2 * j + 1], sc, neg));
-          l += p0;
-          l += p1;
-          pb[j] = pack16<BF>(p0, p1);
-        }
-        // keys 4 half + 0..3 of the 16-key step, then the same + 8; lane i of
-        // 16 reads row i / 4, 4 values from 4 (i % 4), and gets column i
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          u32x4 va;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const char* p = from + (32 * aa + 16 * st + 8 * h) * (2 * D) + (v_at ^ (64 * d));
-            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)const_cast<char*>(p));
-            const u32x2 z = __builtin_bit_cast(u32x2, y);
-            va[2 * h] = z[0];
-            va[2 * h + 1] = z[1];
-          }
-          o[d] = mfma32<BF>(va, pb, o[d]);
-        }
+    for (int i = 0; i < MQ + MV; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + kAhead < MQ + MV) read(i + kAhead);
+      if (i < MQ) {
+        const f32x16 zero = {};
+        sn[i % NA] = mfma32<BF>(op[i], q[i / NA], i < NA ? zero : sn[i % NA]);
+      } else {
+        const int j = i - MQ;
+        o[j % ND] = mfma32<BF>(op[i], pb[j / ND], o[j % ND]);
       }
+#pragma unroll
+      for (int e = NEXT ? 0 : 8; e < NE; ++e) {
+        const int at = NEXT ? e * (MQ + MV - ND) / NE : (e - 8) * (MV - ND) / (NE - 8);
+        if (at == i) element(e);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   // Tile x's second product runs with tile x + 1's first, so that one's
@@ -396,53 +447,55 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   // K of x + 1 and V of x and starts the loads of K of x + 2 and V of x + 1,
   // into the buffers that iteration x - 1 read last.
   f32x16 sa[NA], sb[NA];
-  int e0 = -2, e1 = -2, e2 = -2;                 // table entries of x, x + 1, x + 2
+  Group g0{0, -2}, g1{0, -2};                    // of tiles x and x + 1
   int x = x0;
   // kx, vx: tile x's K and V; kn, vn: tile x + 1's. Distinct buffers, told so
   // that reads do not wait for the loads in flight into the others.
   auto step = [&](f32x16 (&s)[NA], f32x16 (&sn)[NA], char* __restrict kx, char* __restrict kn,
-                  char* __restrict vx, char* __restrict vn, int* okx, int* okn) {
+                  char* __restrict vx, char* __restrict vn, int* missx, int* missn) {
     arrived();
     finish_k(kn);
-    if (x > x0) finish_v(x, e0, vx);
+    if (x > x0) finish_v(x, g0, vx);
     __syncthreads();
-    if (x + 2 < x1) issue_k(x + 2, e2, kx, okx);
-    issue_v(x + 1, e1, vn);
-    e0 = e1;
-    e1 = e2;
-    e2 = fetch(x + 3);
-    scores(sn, kn);
-    accumulate(s, vx);
-    settle(sn, x + 1, okn);
+    const int gone_tile = s_gone;
+    g0 = g1;
+    if (x + 2 < x1) {
+      g1 = group_of(x + 2);
+      issue_k(x + 2, g1, kx, missx);
+    }
+    issue_v(g0, vn);
+    products(std::true_type{}, s, sn, kn, vx);
+    settle(sn, x + 1, gone_tile, missn);
     ++x;
   };
   auto last = [&](f32x16 (&s)[NA], char* vx) {
     if (x > x0) {
       arrived();
-      finish_v(x, e0, vx);
+      finish_v(x, g0, vx);
       __syncthreads();
     }
-    accumulate(s, vx);
+    products(std::false_type{}, s, s, nullptr, vx);
   };
   if (x0 < x1) {
-    e0 = fetch(x0);
-    e1 = fetch(x0 + 1);
-    issue_k(x0, e0, s_k0, s_ok[0]);
-    issue_v(x0, e0, s_v0);
+    g0 = group_of(x0);
+    __syncthreads();                             // s_gone and s_miss are set
+    issue_k(x0, g0, s_k0, s_miss[0]);
+    issue_v(g0, s_v0);
+    if (x0 + 1 < x1) g1 = group_of(x0 + 1);
     arrived();
     finish_k(s_k0);
-    finish_v(x0, e0, s_v0);
+    finish_v(x0, g0, s_v0);
     __syncthreads();
-    if (x0 + 1 < x1) issue_k(x0 + 1, e1, s_k1, s_ok[1]);
-    e2 = fetch(x0 + 2);
+    const int gone_tile = s_gone;
+    if (x0 + 1 < x1) issue_k(x0 + 1, g1, s_k1, s_miss[1]);
     scores(sa, s_k0);
-    settle(sa, x0, s_ok[0]);
+    settle(sa, x0, gone_tile, s_miss[0]);
     while (x + 2 < x1) {
-      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_ok[0], s_ok[1]);
-      step(sb, sa, s_k1, s_k0, s_v1, s_v0, s_ok[1], s_ok[0]);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_miss[0], s_miss[1]);
+      step(sb, sa, s_k1, s_k0, s_v1, s_v0, s_miss[1], s_miss[0]);
     }
     if (x + 1 < x1) {
-      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_ok[0], s_ok[1]);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_miss[0], s_miss[1]);
       last(sb, s_v1);
     } else {
       last(sa, s_v0);
@@ -454,13 +507,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   __syncthreads();
   if (s_bad) {
     for (int xx = x0; xx < x1; ++xx) {
+      if (whole(xx)) continue;
       const int key = key_of(xx);
       for (int j = key; j < key + BN; ++j) {
         if (j > t.p_max || !(j >= t.lo_min || j < a.first)) continue;
         const int e = kv_entry(a.t, j), p = row[e];
-        // in a whole tile only the groups of a wave that missed its page were
-        // staged anew, all zeros
-        if (!there(p) || whole_of(key)) continue;
+        if (p < 0 || p >= a.t.n_pages) continue;
         const long off = p * a.c.sp + (long)(j - e * a.t.ps) * a.c.st;
         auto value = [&](const char* base, int dd) {
           uint32_t x16;
