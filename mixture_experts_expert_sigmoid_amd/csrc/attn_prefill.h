@@ -58,6 +58,22 @@ __device__ __forceinline__ int pre_cu(const AttnArgs& a, int i) {
   return c < 0 ? 0 : (c > a.T ? (int)a.T : c);
 }
 
+// The last sequence i whose ok(i, cu[i]) holds (ok holds up to some i >= 0 and
+// not after): a search with 64 candidates a step, one to a lane.
+template <typename Ok>
+__device__ __forceinline__ int pre_last(const AttnArgs& a, Ok ok) {
+  const int lane = lane_id();
+  int lo = 0, n = a.n;
+  while (true) {
+    const int step = (n + 63) / 64, i = lo + lane * step;
+    const bool yes = lane * step < n && ok(i, pre_cu(a, i));
+    const int last = 63 - __builtin_clzll(__ballot(yes) | 1);
+    lo += last * step;
+    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+    n = min(step, n - last * step);
+  }
+}
+
 template <int D>
 __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
@@ -86,7 +102,7 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
 }
 
 template <bool BF, bool F8, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_prefill_kernel(AttnArgs a) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   constexpr int NA = BN / 32;                    // 32-key score tiles
   constexpr int NC = D / 16;                     // steps of the first product
@@ -109,19 +125,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
 
   PreTile t;
   const int kvh = blockIdx.x % a.c.hkv;
-  {
-    // longest tiles first; sequence i's tiles start at cu[i] g / ROWS + i
-    const int tt = (int)(gridDim.x / a.c.hkv) - 1 - (int)(blockIdx.x / a.c.hkv);
-    auto base = [&](int i) { return (int)((long)pre_cu(a, i) * a.g / ROWS) + i; };
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (base(mid) <= tt) lo = mid; else hi = mid - 1;
-    }
-    t.seq = lo;
-    t.tile = tt - base(lo);
-    if (!pre_span<D>(a, t)) return;
-  }
+  // longest tiles first; sequence i's tiles start at cu[i] g / ROWS + i
+  const int tt = (int)(gridDim.x / a.c.hkv) - 1 - (int)(blockIdx.x / a.c.hkv);
+  t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
+  t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
+  if (!pre_span<D>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
@@ -215,9 +223,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   const int v_row = 4 * half + ((lane & 15) >> 2), v_d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   int v_at = v_row * (2 * D) + (16 * ((v_d >> 3) ^ v_swz(v_row)) + 2 * (v_d & 7));
   const uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
-  auto bad16 = [&](uint32_t x) {                 // either half infinite or NaN
-    return (x & kExp) == kExp || ((x >> 16) & kExp) == kExp;
-  };
+  // either value of a pair infinite or NaN: the exponent's carry
+  auto carry = [&](uint32_t x) { return (x & 0x7FFF7FFFu) + (BF ? 0x00800080u : 0x04000400u); };
   auto clean16 = [&](uint32_t x) {
     if ((x & kExp) == kExp) x &= 0xFFFF0000u;
     if (((x >> 16) & kExp) == kExp) x &= 0x0000FFFFu;
@@ -227,7 +234,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
   auto clean = [&](u32x4 v, int key, int kr, bool ok) {
     const int j = key + kr;
     if (!ok || j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
-    if (bad16(v[0]) || bad16(v[1]) || bad16(v[2]) || bad16(v[3])) {
+    if ((carry(v[0]) | carry(v[1]) | carry(v[2]) | carry(v[3])) & 0x80008000u) {
       s_bad = 1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = clean16(v[e]);
@@ -362,17 +369,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prefill_kernel(Att
           if (miss[i] == x) gone |= 1u << (i * WR / 16);
         gone = __builtin_amdgcn_readfirstlane(gone);
       }
-      // selects, no branches: a branch per element would copy the tile
-      const int at = key_of(x) + 4 * half, hi = pos - at, below = lo - at, kept = a.first - at;
+      // Bit n of `see`: element n of the lane, key 8 (n / 4) + n % 4 of those
+      // from `at` on. Elements ascend by key, so each bound is a run of ones.
+      // (Selects without branches: a branch per element would copy the tile.)
+      auto below = [&](int c) {                  // elements of keys < c
+        const int k = min(max(c, 0), 64), cnt = 4 * (k >> 3) + min(k & 7, 4);
+        return (uint32_t)((1ull << cnt) - 1);
+      };
+      const int at = key_of(x) + 4 * half;
+      uint32_t see = below(pos + 1 - at) & (~below(lo - at) | below(a.first - at));
 #pragma unroll
-      for (int aa = 0; aa < NA; ++aa)
+      for (int i = 0; i < 4; ++i) see &= (gone >> i) & 1 ? ~(0xFFu << (8 * i)) : ~0u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int kk = 32 * aa + 8 * (i >> 2) + (i & 3);
-          const bool ok = (kk <= hi) & ((kk >= below) | (kk < kept)) &
-                          !((gone >> (2 * aa + (i >> 3))) & 1);
-          s[aa][i] = ok ? s[aa][i] : kNegInf;
-        }
+      for (int n = 0; n < 16 * NA; ++n) {
+        const uint32_t keep = (uint32_t)((int)(see << (31 - n)) >> 31);
+        const uint32_t v = __float_as_uint(s[n >> 4][n & 15]);
+        s[n >> 4][n & 15] = __uint_as_float((v & keep) | (0xFF800000u & ~keep));
+      }
     }
     float bm = s[0][0];
 #pragma unroll
@@ -595,16 +608,9 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   if (ri >= rows) return;
   const int tok = (int)(ri / a.hq), head = (int)(ri - (long)tok * a.hq);
   PreTile t;
-  {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre_cu(a, mid) <= tok) lo = mid; else hi = mid - 1;
-    }
-    t.seq = lo;
-    t.tile = ((tok - pre_cu(a, lo)) * a.g + head % a.g) / ROWS;
-    if (!pre_span<D>(a, t)) return;
-  }
+  t.seq = pre_last(a, [&](int, int cu) { return cu <= tok; });
+  t.tile = ((tok - pre_cu(a, t.seq)) * a.g + head % a.g) / ROWS;
+  if (!pre_span<D>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if (parts == 1) return;
   const int lane = lane_id();
