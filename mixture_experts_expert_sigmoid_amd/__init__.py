@@ -183,13 +183,16 @@ def lib():
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """The hipStream_t to enqueue on: the current device's current stream if
+    None (asked of torch directly; building a Stream object for it costs more
+    than a kernel launch)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -380,19 +383,20 @@ _KV_FMT = {torch.bfloat16: MOE_KV_BF16, torch.float16: MOE_KV_F16,
 
 
 def _kv_fmt(t: torch.Tensor, where: str) -> int:
-    if t.dtype not in _KV_FMT:
+    fmt = _KV_FMT.get(t.dtype)
+    if fmt is None:
         raise MoeError(-3, where, f"dtype {t.dtype}")
-    return _KV_FMT[t.dtype]
+    return fmt
 
 
 def _i32(t: Optional[torch.Tensor], n: int, where: str):
     """Pointer of a contiguous int32 list of at least n entries (or None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
         raise MoeError(-2, where, f"wants {n} contiguous int32, got {t.dtype} "
                                   f"{tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _bytes(ws: Optional[torch.Tensor]) -> int:
@@ -430,34 +434,34 @@ def kv_table(table: torch.Tensor, lens: torch.Tensor, page_size: int, n_pages: i
         raise MoeError(-2, "kv_table", "table is int32 [slots][max_pages], rows contiguous")
     ld = table.stride(0) if table.shape[0] > 1 else table.shape[1]
     t = MoeKvTable(table.shape[0], table.shape[1], ld, n_pages, page_size, table.data_ptr(),
-                   _i32(lens, table.shape[0], "kv_table").value,
-                   None if refs is None else _i32(refs, n_pages, "kv_table").value)
+                   _i32(lens, table.shape[0], "kv_table"),
+                   None if refs is None else _i32(refs, n_pages, "kv_table"))
     t._keep = (table, lens, refs)
     return t
 
 
-def _rows(t: torch.Tensor, where: str, rows: int, D: int):
+def _rows(t: torch.Tensor, where: str, shape, D: int):
     """Strides (row, head) of a [rows][heads][head_dim] tensor. A dimension of
     one entry has no stride of its own."""
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D or t.stride(2) != 1:
-        raise MoeError(-2, where, f"wants [{rows}][heads][{D}] with contiguous rows, got "
-                                  f"{tuple(t.shape)} strides {t.stride()}")
-    head = t.stride(1) if t.shape[1] > 1 else D
-    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * D), head
+    st = t.stride()
+    if t.shape != shape or len(st) != 3 or shape[2] != D or st[2] != 1:
+        raise MoeError(-2, where, f"wants {tuple(shape)} of [rows][heads][{D}] with contiguous "
+                                  f"rows, got {tuple(t.shape)} strides {st}")
+    rows, heads, _ = shape
+    return (st[0] if rows > 1 else heads * D), (st[1] if heads > 1 else D)
 
 
 def _attn(where, cache: MoeKvCache, q, out, scale, window, n_first, lse) -> MoeAttn:
-    T, Hq = q.shape[0], q.shape[1]
-    if out.dtype != q.dtype or out.shape != q.shape:
-        raise MoeError(-2, where, "out and q differ in shape or type")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq)
+    shape, D = q.shape, cache.head_dim
+    if out.dtype is not q.dtype:
+        raise MoeError(-2, where, "out and q differ in type")
+    qr, qh = _rows(q, where, shape, D)
+    orow, ohead = _rows(out, where, shape, D)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
                             or not lse.is_contiguous()):
         raise MoeError(-2, where, "lse is fp32 [rows][heads], contiguous")
-    qs, os_ = (_rows(t, where, T, cache.head_dim) for t in (q, out))
-    a = MoeAttn(_kv_fmt(q, where), Hq, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0],
-                os_[1], None if lse is None else lse.data_ptr(), scale, window, n_first)
-    a._keep = (q, out, lse)
-    return a
+    return MoeAttn(_kv_fmt(q, where), shape[1], q.data_ptr(), qr, qh, out.data_ptr(), orow,
+                   ohead, None if lse is None else lse.data_ptr(), scale, window, n_first)
 
 
 def moe_attn_decode_workspace_size(cache: MoeKvCache, n: int, n_heads: int) -> int:
@@ -499,9 +503,10 @@ def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_
     where = "moe_cache_append"
     T = k.shape[0]
     n = T if cu is None else cu.numel() - 1
-    if v.dtype != k.dtype or v.shape != k.shape or (T and k.shape[1] != cache.n_heads):
-        raise MoeError(-2, where, "k and v differ, or their heads from the cache's")
-    ks, vs = (_rows(t, where, T, cache.head_dim) for t in (k, v))
+    shape, D = k.shape, cache.head_dim
+    if v.dtype is not k.dtype or (T and shape[1] != cache.n_heads):
+        raise MoeError(-2, where, "k and v differ in type, or their heads from the cache's")
+    ks, vs = _rows(k, where, shape, D), _rows(v, where, shape, D)
     _check(lib().moe_cache_append(
         ctypes.byref(cache), ctypes.byref(table), _i32(slots, n, where),
         _i32(start, n, where), _i32(cu, 1, where), n, T, _kv_fmt(k, where), _p(k), ks[0],

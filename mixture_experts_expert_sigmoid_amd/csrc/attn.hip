@@ -13,13 +13,15 @@ hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
 
 namespace {
 inline size_t al16(size_t b) { return (b + 15) & ~(size_t)15; }
-size_t dec_part_bytes(int D) { return (size_t)kDecWgs * 2 * (32 + 16 * D) * 4; }
+size_t dec_part_bytes(int D, bool f8) {
+  return (size_t)dec_wgs(D, f8) * 2 * (32 + 16 * D) * 4;
+}
 }  // namespace
 
-size_t decode_ws_bytes(long n, int hq, int hkv, int D) {
+size_t decode_ws_bytes(long n, int hq, int hkv, int D, bool f8) {
   const long m = n < kDecMaxSeqs ? n : kDecMaxSeqs;
   const int ht = (hq / hkv + 15) / 16;
-  return dec_part_bytes(D) + al16((size_t)m * hkv * ht * 8);
+  return dec_part_bytes(D, f8) + al16((size_t)m * hkv * ht * 8);
 }
 
 hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
@@ -37,7 +39,7 @@ hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
     a.q += b * a.q_row;
     a.out += b * a.o_row;
     if (a.lse) a.lse += b * a.hq;
-    a.meta = (int*)((char*)a.part + dec_part_bytes(a.c.D));
+    a.meta = (int*)((char*)a.part + dec_part_bytes(a.c.D, a.c.fmt == KV_E4M3));
     hipError_t e = a.c.D == 64    ? launch_decode_64(a, fmt, s)
                    : a.c.D == 128 ? launch_decode_128(a, fmt, s)
                                   : launch_decode_256(a, fmt, s);

@@ -78,7 +78,7 @@ struct DecRaw {
 };
 
 template <bool BF, bool F8, int D>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(AttnArgs a) {
   constexpr int NC = D / 32;             // 32-deep steps of the first product
   constexpr int VE = D / 16;             // d values of a lane (rows of V^T it feeds)
   constexpr int VH = F8 ? 1 : (VE > 8 ? 2 : 1);    // 16-byte halves of them
@@ -413,9 +413,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_decode_kernel(AttnA
   }
 }
 
-// Joins the parts of the pairs that more than one workgroup had. One
-// workgroup per (pair, head): the waves take every fourth part, a lane D / 64
-// values, eight parts' loads in flight.
+// Joins the parts of the pairs that more than one workgroup had, in their
+// order, eight parts' loads in flight: up to eight parts by one wave a head (a
+// lane has D / 64 values), more by four waves, each every fourth part.
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
   constexpr int E = D / 64;
@@ -429,77 +429,89 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
   const int heads = min(16, a.g - hbase);
   const int lane = lane_id(), w = threadIdx.x >> 6;
   const size_t sf = dec_slot_floats(D);
-  auto part_of = [&](int i) {
-    return a.part + (2 * (size_t)(wg0 + i) + (i == 0)) * sf;
+
+  struct State {
+    float m, l, o[E];
   };
+  // adds parts first, first + stride, ... (at most eight) of head hh
+  auto add = [&](State& s, int hh, int first, int stride) {
+    float pm[8], pl[8], po[8][E];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = first + stride * k, ii = i < cnt ? i : first;
+      const float* p = a.part + (2 * (size_t)(wg0 + ii) + (ii == 0)) * sf;
+      pm[k] = i < cnt ? p[hh] : kNegInf;
+      pl[k] = p[16 + hh];
+#pragma unroll
+      for (int e = 0; e < E; ++e) po[k][e] = p[kDecPartRow + hh * D + lane * E + e];
+    }
+    float mn = s.m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, pm[k]);
+    const float mu = mn == kNegInf ? 0.0f : mn;
+    const float f0 = exp2_fast(s.m - mu);
+    s.l *= f0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s.o[e] *= f0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (first + stride * k < cnt) {
+        const float f = exp2_fast(pm[k] - mu);
+        s.l += f * pl[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.o[e] += f * po[k][e];
+      }
+    }
+    s.m = mn;
+  };
+  auto write = [&](const State& s, int hh) {
+    float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+    if (F8 && s.l != 0.0f) inv *= a.c.vs[kvh];
+    const int head = kvh * a.g + hbase + hh;
+    char* dst = a.out + seq * a.o_row + head * a.o_head;
+    if constexpr (E == 1) {
+      *(uint16_t*)(dst + 2 * lane) = (uint16_t)pack16<BF>(s.o[0] * inv, 0.0f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *(uint32_t*)(dst + 2 * (lane * E + e)) = pack16<BF>(s.o[e] * inv, s.o[e + 1] * inv);
+    }
+    if (a.lse && lane == 0)
+      a.lse[(long)seq * a.hq + head] = (s.m + __builtin_amdgcn_logf(s.l)) * kLn2;
+  };
+  const State none{kNegInf, 0.0f, {}};
+
+  if (cnt <= 8) {
+    for (int hh = 4 * blockIdx.y + w; hh < heads; hh += 4 * gridDim.y) {
+      State s = none;
+      add(s, hh, 0, 1);
+      write(s, hh);
+    }
+    return;
+  }
   for (int hh = blockIdx.y; hh < heads; hh += gridDim.y) {
-    float m = kNegInf, l = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int i0 = w; i0 < cnt; i0 += 32) {
-      float pm[8], pl[8], po[8][E];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + 4 * k;
-        const float* p = part_of(i < cnt ? i : i0);
-        pm[k] = i < cnt ? p[hh] : kNegInf;
-        pl[k] = p[16 + hh];
-#pragma unroll
-        for (int e = 0; e < E; ++e) po[k][e] = p[kDecPartRow + hh * D + lane * E + e];
-      }
-      float mn = m;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mn = fmaxf(mn, pm[k]);
-      const float mu = mn == kNegInf ? 0.0f : mn;
-      const float f0 = exp2_fast(m - mu);
-      l *= f0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (i0 + 4 * k < cnt) {
-          const float f = exp2_fast(pm[k] - mu);
-          l += f * pl[k];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += f * po[k][e];
-        }
-      }
-      m = mn;
-    }
+    State s = none;
+    for (int first = w; first < cnt; first += 32) add(s, hh, first, 4);
     if (lane == 0) {
-      s_ml[w][0] = m;
-      s_ml[w][1] = l;
+      s_ml[w][0] = s.m;
+      s_ml[w][1] = s.l;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = acc[e];
+    for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = s.o[e];
     __syncthreads();
     if (w == 0) {
-      float mm = kNegInf, ll = 0.0f;
+      State t = none;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mm = fmaxf(mm, s_ml[i][0]);
-      const float mu = mm == kNegInf ? 0.0f : mm;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+      for (int i = 0; i < 4; ++i) t.m = fmaxf(t.m, s_ml[i][0]);
+      const float mu = t.m == kNegInf ? 0.0f : t.m;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float f = exp2_fast(s_ml[i][0] - mu);
-        ll += f * s_ml[i][1];
+        t.l += f * s_ml[i][1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * s_o[i][lane * E + e];
+        for (int e = 0; e < E; ++e) t.o[e] += f * s_o[i][lane * E + e];
       }
-      float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-      if (F8 && ll != 0.0f) inv *= a.c.vs[kvh];
-      const int head = kvh * a.g + hbase + hh;
-      char* dst = a.out + seq * a.o_row + head * a.o_head;
-      if constexpr (E == 1) {
-        *(uint16_t*)(dst + 2 * lane) = (uint16_t)pack16<BF>(acc[0] * inv, 0.0f);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-          *(uint32_t*)(dst + 2 * (lane * E + e)) = pack16<BF>(acc[e] * inv, acc[e + 1] * inv);
-      }
-      if (a.lse && lane == 0)
-        a.lse[(long)seq * a.hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+      write(t, hh);
     }
     __syncthreads();
   }
@@ -512,7 +524,7 @@ hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   const long seen = a.window ? (long)a.window + a.first + 2 * kDecKeys : cap;
   const long units = ((seen < cap ? seen : cap) + kDecUnit - 1) / kDecUnit + 1;
   const long bound = (long)a.n * HT * units;
-  const int grid = (int)(bound < kDecWgs ? bound : kDecWgs);
+  const int wgs = dec_wgs(D, F8), grid = (int)(bound < wgs ? bound : wgs);
   attn_decode_kernel<BF, F8, D><<<grid, 256, 0, s>>>(a);
   const long pairs = (long)a.n * HT;
   const dim3 jg((unsigned)pairs, pairs >= 256 ? 1 : (a.g < 16 ? a.g : 16));

@@ -54,14 +54,16 @@ struct AttnArgs {
   int* meta;
 };
 
-// Decode: at most kDecWgs workgroups; partial-result slots, two a workgroup
-// (the sequence it continues, the one it leaves open), of 16 rows of D
-// floats + 16 maxima + 16 sums; and one (first workgroup, count) pair per
-// (sequence, key-value head, 16 query heads).
-constexpr int kDecWgs = 1024;           // workgroups of a launch
+// Decode: dec_wgs workgroups, as many as are resident at once on 256 CUs, so
+// that an even share of the keys for each is one even pass; partial-result
+// slots, two a workgroup (the sequence it continues, the one it leaves open),
+// of 16 rows of D floats + 16 maxima + 16 sums; and one (first workgroup,
+// count) pair per (sequence, key-value head, 16 query heads).
+constexpr int dec_waves(int D, bool f8) { return D == 64 ? 4 : D == 128 && f8 ? 3 : 2; }
+constexpr int dec_wgs(int D, bool f8) { return 256 * dec_waves(D, f8); }
 constexpr int kDecMaxSeqs = 512;        // sequences per launch
 constexpr int kDecKeys = 32;            // keys of one wave's step
-size_t decode_ws_bytes(long n, int hq, int hkv, int D);
+size_t decode_ws_bytes(long n, int hq, int hkv, int D, bool f8);
 hipError_t launch_attn_decode(const AttnArgs& a, int fmt, hipStream_t s);
 
 // Prefill: tiles of kPreRows rows, a row being a (token, query head) pair of

@@ -177,7 +177,8 @@ extern "C" {
 
 size_t moe_attn_decode_workspace_size(const moe_kv_cache* cache, long n, int n_heads) {
   if (!ws_shape_ok(cache, n_heads) || n < 0 || n >= (1L << 20)) return 0;
-  return moe::decode_ws_bytes(n, n_heads, cache->n_heads, cache->head_dim);
+  return moe::decode_ws_bytes(n, n_heads, cache->n_heads, cache->head_dim,
+                              cache->fmt == MOE_KV_E4M3);
 }
 
 int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_table* table, const int* slots,
@@ -188,7 +189,7 @@ int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_table* table, const 
   if (st) return st;
   if (!slots && n > table->n_slots) return MOE_ERR_SHAPE;
   if (n == 0) return MOE_OK;
-  const size_t need = moe::decode_ws_bytes(n, a.hq, a.c.hkv, a.c.D);
+  const size_t need = moe::decode_ws_bytes(n, a.hq, a.c.hkv, a.c.D, a.c.fmt == moe::KV_E4M3);
   if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return MOE_ERR_WORKSPACE;
   a.part = (float*)ws;
   return done(moe::launch_attn_decode(a, attn->fmt, (hipStream_t)stream), "moe_attn_decode");
