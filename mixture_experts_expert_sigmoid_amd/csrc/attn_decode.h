@@ -5,15 +5,16 @@
 // maximum m and sum l of a softmax, O^T = V^T P^T, rescaled when m grows.
 // One pass over the keys and values, everything else in registers.
 //
-// Layout. A wave takes 32 keys at a time with v_mfma_*_16x16x32. K rows go
-// from memory straight to the A operand (lane l: key l % 16, 8 values of D).
-// The result has a query head in each lane's column (l % 16) and 4 keys in
-// its rows, so a lane holds P of 8 keys of one head -- the B operand of the
-// second product as it stands, if its 8-key slice of lane group l / 16 is
-// taken as keys 4 (l / 16) + 0..3 of both 16-key tiles. V is loaded in that
-// order, 8 keys of D / 16 consecutive d a lane, and the 16-bit pairs turned
-// round in the lane (one v_perm per pair of values), so row m of output tile
-// td is d = (D / 16) m + td. Nothing of K, V, S or P passes through LDS.
+// Layout. A wave takes 32 keys at a time with v_mfma_*_16x16x32. Its K and V
+// go straight into its own part of LDS, in loads of whole cache lines (loads
+// into the operand registers would take 64 bytes of 16 keys each, half a line,
+// and the second half stalled on the first), and no wave waits for another
+// while it streams. S^T = K Q^T has a query head in each lane's column (l %
+// 16) and 4 keys in its rows, so a lane holds P of 8 keys of one head -- the B
+// operand of the second product as it stands, if its 8-key slice of lane group
+// l / 16 is taken as keys 4 (l / 16) + 0..3 of both 16-key tiles. V is read
+// transposed (ds_read_b64_tr_b16) in that key order; e4m3 values are expanded
+// and turned round in the lane.
 //
 // Split. The keys that each sequence sees are cut into units of 128 (32 per
 // wave); the units of all (sequence, key-value head) pairs, laid end to end,
@@ -24,6 +25,8 @@
 // Bound: HBM reads of K and V; short contexts by latency (length -> table ->
 // keys -> join).
 #pragma once
+#include <type_traits>
+
 #include "attn_dev.h"
 
 namespace moe {
@@ -55,43 +58,68 @@ __device__ __forceinline__ int dec_units(const DecSpan& s) {
   return u > 0 ? u : 1;               // a sequence without keys still gets its row written
 }
 
-// Q operand of one lane: head l % 16 of the tile, D values in the order of
-// the K loads
-template <bool F8, int D>
-__device__ __forceinline__ void dec_load_q(u32x4 (&q)[D / 32], const char* row, bool have) {
-  const int lg = lane_id() >> 4;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    const int d = F8 ? 64 * (c >> 1) + 16 * lg + 8 * (c & 1) : 32 * c + 8 * lg;
-    u32x4 z = {0, 0, 0, 0};
-    q[c] = have ? *(const u32x4*)(row + 2 * d) : z;
-  }
+// Waits until at most N of the wave's vector memory operations are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// raw bytes of one wave's block: K per 16-key tile, V per key
-template <bool F8, int D>
-struct DecRaw {
-  static constexpr int KL = F8 ? D / 64 : D / 32;          // 16-byte loads per lane and tile
-  static constexpr int VB = F8 ? D / 16 : D / 8;           // bytes per lane and key
-  u32x4 k[2][KL];
-  uint32_t v[8][VB / 4];
-};
+// Reads of LDS by byte address with their wait in the same statement, ordered
+// among the loads into LDS as written (volatile, memory).
+template <int T>
+__device__ __forceinline__ void lds_read_b128x2(u32x4& a, u32x4& b, uint32_t at) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(a), "=&v"(b)
+               : "v"(at), "n"(T)
+               : "memory");
+}
+template <int T>
+__device__ __forceinline__ void lds_read_tr16x4(u32x2& a0, u32x2& a1, u32x2& b0, u32x2& b1,
+                                                uint32_t a, uint32_t b) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+      "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a0), "=&v"(a1), "=&v"(b0), "=&v"(b1)
+      : "v"(a), "v"(b), "n"(T)
+      : "memory");
+}
+template <int VW> struct Dwords { typedef uint32_t type __attribute__((ext_vector_type(VW))); };
+template <> struct Dwords<1> { typedef uint32_t type; };
+// VW dwords from each of at, at + S, at + 2 S, at + 3 S
+template <int VW, int S, typename Words>
+__device__ __forceinline__ void lds_read_x4(Words& a, Words& b, Words& c, Words& d, uint32_t at) {
+#define MOE_READ4(OP)                                                                       \
+  asm volatile(OP " %0, %4\n\t" OP " %1, %4 offset:%5\n\t" OP " %2, %4 offset:%6\n\t" OP  \
+                  " %3, %4 offset:%7\n\ts_waitcnt lgkmcnt(0)"                               \
+               : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)                                     \
+               : "v"(at), "n"(S), "n"(2 * S), "n"(3 * S)                                    \
+               : "memory")
+  if constexpr (VW == 1) MOE_READ4("ds_read_b32");
+  else if constexpr (VW == 2) MOE_READ4("ds_read_b64");
+  else MOE_READ4("ds_read_b128");
+#undef MOE_READ4
+}
 
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(AttnArgs a) {
   constexpr int NC = D / 32;             // 32-deep steps of the first product
-  constexpr int VE = D / 16;             // d values of a lane (rows of V^T it feeds)
-  constexpr int VH = F8 ? 1 : (VE > 8 ? 2 : 1);    // 16-byte halves of them
-  constexpr int VW = VE / VH;            // d values of one half
-  using Raw = DecRaw<F8, D>;
+  constexpr int ND = D / 16;             // 16-row tiles of O^T
+  constexpr int ROW = F8 ? D : 2 * D;    // bytes of a key
+  constexpr int UPR = ROW / 16;          // 16-byte units of a key
+  constexpr int KI = 16 * UPR / 64;      // loads of a 16-key tile
+  constexpr int KB = kDecKeys * ROW;     // bytes of a wave's block of K, and of V
+  // a wave's LDS: its blocks of K and V, afterwards its result for the join
+  constexpr int OB = 16 * (D + 4) * 4, RB = 2 * KB > OB ? 2 * KB : OB;
 
   __shared__ int s_pref[kDecMaxSeqs + 1];
   __shared__ int s_len[kDecMaxSeqs];
   __shared__ int s_scan[4];
   __shared__ float s_ml[4][2][16];
-  __shared__ float s_o[4][16][D + 4];
+  __shared__ __align__(16) char s_wave[4][RB];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lg = lane >> 4, lc = lane & 15;
   const int n = a.n, ht = (a.g + 15) >> 4;       // 16-head tiles per key-value head
   const int HT = a.c.hkv * ht;
@@ -136,9 +164,28 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
       if ((long)s_pref[mid] * HT <= u) seq = mid; else hi = mid - 1;
     }
   }
+  seq = __builtin_amdgcn_readfirstlane(seq);
 
-  const long koff = (long)lc * a.c.st + 16 * lg;            // K: key lc, 16 bytes of D
-  const long voff = (long)(4 * lg) * a.c.st + lc * (F8 ? VE : 2 * VW);
+  // K and V go to LDS 64 units a load, whole cache lines at a time. Unit u of
+  // row r lies at u ^ swz(r): a read of the first product takes one unit of 16
+  // rows, a transposed one of the second 32 bytes of 16 rows.
+  auto k_swz = [](int r) { return r & (UPR < 16 ? UPR - 1 : 15); };
+  auto v_swz = [](int r) { return F8 ? 0 : UPR == 8 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; };
+  uint32_t k_from[KI], v_from[KI];
+#pragma unroll
+  for (int i = 0; i < KI; ++i) {
+    const int r = i * (64 / UPR) + lane / UPR;
+    k_from[i] = (uint32_t)r * (uint32_t)a.c.st + 16 * (lane % UPR ^ k_swz(r));
+    v_from[i] = (uint32_t)r * (uint32_t)a.c.st + 16 * (lane % UPR ^ v_swz(r));
+  }
+  const uint32_t k_at = lc * ROW + 16 * (lg ^ k_swz(lc));      // turned by 64 bytes a step
+  // V: key row v_row of a tile. 16 bits: lane i of 16 reads row i / 4, 4
+  // values from 4 (i % 4), and gets column i; e4m3: D / 16 values of row 4 lg
+  const int v_row = 4 * lg + (F8 ? 0 : lc >> 2);
+  const uint32_t v_at =
+      v_row * ROW + (F8 ? lc * (D / 16) : 16 * ((lc & 3) >> 1 ^ v_swz(v_row)) + 8 * (lc & 1));
+  char* const my = s_wave[w];
+  const uint32_t my_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)my;
 
   while (u < u_end) {
     const int pre = s_pref[seq], ns = s_pref[seq + 1] - pre;
@@ -151,184 +198,221 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
     const int slot = a.slots ? a.slots[seq] : seq;
     const int* row = a.t.table + (long)(slot < 0 || slot >= a.t.n_slots ? 0 : slot) * a.t.ld;
 
+    // blocks 4 x + w of units x = b0 .. b1 - 1 are this wave's
+    const int x_end = __builtin_amdgcn_readfirstlane(min(b1, (sp.nb - w + 3) >> 2));
+    auto key_of = [&](int x) {
+      const int bi = 4 * x + w;
+      return kDecKeys * (bi < sp.nb1 ? bi : sp.b2 + bi - sp.nb1);
+    };
+    // Byte offset in the cache of the two 16-key tiles of the next 64 blocks,
+    // a block a lane; negative where a tile has no page or no visible key
+    int at0 = b0;
+    auto lookup = [&](int x, int t) {
+      const int kt = key_of(x) + 16 * t;
+      if (x >= x_end || kt >= sp.L || !(kt + 16 > sp.lo || kt < sp.nf)) return -1L;
+      const int i = kv_entry(a.t, kt), p = row[i];
+      if (p >= 0 && p < a.t.n_pages) return p * a.c.sp + (kt - i * a.t.ps) * a.c.st;
+      atomicOr(a.err, kErrPage);
+      return -1L;
+    };
+    long offs[2] = {lookup(b0 + lane, 0), lookup(b0 + lane, 1)};
+    struct Place {
+      long off[2];                       // 0 without one
+      bool there[2];
+    };
+    auto place_of = [&](int x) {         // x one after another
+      if (x - at0 == 64) {
+        at0 = x;
+        offs[0] = lookup(x + lane, 0);
+        offs[1] = lookup(x + lane, 1);
+      }
+      Place p;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t lo = __builtin_amdgcn_readlane((int)offs[t], x - at0);
+        const int hi = __builtin_amdgcn_readlane((int)(offs[t] >> 32), x - at0);
+        p.there[t] = hi >= 0;
+        p.off[t] = hi >= 0 ? (long)(((uint64_t)(uint32_t)hi << 32) | lo) : 0L;
+      }
+      return p;
+    };
+
+    // head lc of the tile, D values in the order of the K reads
     u32x4 q[NC];
-    dec_load_q<F8, D>(q, a.q + seq * a.q_row + (long)(kvh * a.g + hbase + lc) * a.q_head,
-                      lc < heads);
+    {
+      const char* src = a.q + seq * a.q_row + (long)(kvh * a.g + hbase + lc) * a.q_head;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int d = F8 ? 64 * (c >> 1) + 16 * lg + 8 * (c & 1) : 32 * c + 8 * lg;
+        q[c] = lc < heads ? *(const u32x4*)(src + 2 * d) : u32x4{0, 0, 0, 0};
+      }
+    }
     const float sc = F8 ? a.scale * a.c.ks[kvh] : a.scale;
 
-    f32x4 o[VE];
+    f32x4 o[ND];
 #pragma unroll
-    for (int t = 0; t < VE; ++t) o[t] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < ND; ++t) o[t] = f32x4{0, 0, 0, 0};
     float m = kNegInf, l = 0.0f;
 
     const char* kb = a.c.k + kvh * a.c.sh;
     const char* vb = a.c.v + kvh * a.c.sh;
+    auto load = [&](const char* base, const Place& p, const uint32_t (&from)[KI], char* to) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          uint32_t f = from[i];
+          asm volatile("" : "+v"(f));    // added by the load, not ahead of it
+          __builtin_amdgcn_global_load_lds(
+              (const __attribute__((address_space(1))) void*)(base + p.off[t] + f),
+              (__attribute__((address_space(3))) void*)(to + (t * KI + i) * 1024), 16, 0, 0);
+        }
+    };
 
-    // blocks 4 x + w of units x = b0 .. b1 - 1 are this wave's
-    const int x_end = min(b1, (sp.nb - w + 3) >> 2);
-    int x = b0;
-    while (x < x_end) {
-      // page and place of the two 16-key tiles of the next 64 blocks, one
-      // block a lane; -1 where a tile has no visible key or no page
-      const int xb = x, xe = min(x_end, x + 64);
-      int pg[2], in[2];
-      {
-        const int bi = 4 * (xb + lane) + w;
-        const int key = kDecKeys * (bi < sp.nb1 ? bi : sp.b2 + bi - sp.nb1);
+    // One block: the loads of K and V of block x (place p) have been started,
+    // in this order; NEXT: those of block x + 1 (place pn) follow into the same
+    // room as soon as each has been read, so that they fly while the block is
+    // worked on. Loads complete in their order: all but the newest N are done
+    // once vmcnt <= N. The reads are written with their waits (lds_read); left
+    // to the compiler, each would wait for every load in flight.
+    constexpr int LOADS = 2 * KI;        // of K, and of V
+    auto block = [&](auto next, int x, const Place& p, const Place& pn) {
+      constexpr bool NEXT = decltype(next)::value;
+      const int key = key_of(x);
+      // every key of the block visible and there
+      const bool whole = p.there[0] && p.there[1] && key + kDecKeys <= sp.L &&
+                         (key >= sp.lo || key + kDecKeys <= sp.nf);
+      f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+      wait_loads<LOADS>();               // all but V's
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int kt = key + 16 * t;
-          pg[t] = -1;
-          in[t] = 0;
-          const bool seen = xb + lane < xe && kt < sp.L && (kt + 16 > sp.lo || kt < sp.nf);
-          if (seen) {
-            const int e = kv_entry(a.t, kt);
-            const int p = row[e];
-            if (p >= 0 && p < a.t.n_pages) {
-              pg[t] = p;
-              in[t] = kt - e * a.t.ps;
-            } else {
-              atomicOr(a.err, kErrPage);
-            }
-          }
+      for (int c = 0; c < NC; c += 2) {
+        // 16 bits: steps c and c + 1; e4m3: both in one unit
+        u32x4 r[4];                      // [step][tile]
+        if constexpr (F8) {
+          lds_read_b128x2<16 * ROW>(r[0], r[1], my_at + (k_at ^ (32 * c)));
+        } else {
+          lds_read_b128x2<16 * ROW>(r[0], r[1], my_at + (k_at ^ (64 * c)));
+          lds_read_b128x2<16 * ROW>(r[2], r[3], my_at + (k_at ^ (64 * c + 64)));
         }
-      }
-      Raw r;
-      auto load_k = [&](int xx) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int p = max(0, __builtin_amdgcn_readlane(pg[t], xx - xb));
-          const int i = __builtin_amdgcn_readlane(in[t], xx - xb);
-          const char* b = kb + p * a.c.sp + i * a.c.st + koff;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int c = 0; c < Raw::KL; ++c) r.k[t][c] = *(const u32x4*)(b + 64 * c);
-        }
-      };
-      auto load_v = [&](int xx) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int p = max(0, __builtin_amdgcn_readlane(pg[t], xx - xb));
-          const int i = __builtin_amdgcn_readlane(in[t], xx - xb);
-          const char* b = vb + p * a.c.sp + i * a.c.st + voff;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t* dst = r.v[4 * t + j];
-            const char* src = b + j * a.c.st;
-            if constexpr (Raw::VB == 4) {
-              dst[0] = *(const uint32_t*)src;
-            } else if constexpr (Raw::VB == 8) {
-              const u32x2 y = *(const u32x2*)src;
-              dst[0] = y[0];
-              dst[1] = y[1];
-            } else {
-#pragma unroll
-              for (int h = 0; h < Raw::VB / 16; ++h) {
-                // 16-bit D = 256: the second half of the lane's d lies 256 bytes on
-                const u32x4 y = *(const u32x4*)(src + h * 256);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[4 * h + e] = y[e];
-              }
-            }
-          }
-        }
-      };
-      load_k(x);
-      load_v(x);
-      for (; x < xe; ++x) {
-        const int bi = 4 * x + w;
-        const int key = kDecKeys * (bi < sp.nb1 ? bi : sp.b2 + bi - sp.nb1);
-        const int p0 = __builtin_amdgcn_readlane(pg[0], x - xb);
-        const int p1 = __builtin_amdgcn_readlane(pg[1], x - xb);
-        // every key of the block visible and there
-        const bool whole = p0 >= 0 && p1 >= 0 && key + kDecKeys <= sp.L &&
-                           (key >= sp.lo || key + kDecKeys <= sp.nf);
-        f32x4 s[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          s[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
+          for (int t = 0; t < 2; ++t) {
             u32x4 ka;
             if constexpr (F8) {
-              const u32x4 raw = r.k[t][c >> 1];
-              const uint32_t x0 = raw[2 * (c & 1)], x1 = raw[2 * (c & 1) + 1];
-              ka = u32x4{from_e4m3<BF, false>(x0), from_e4m3<BF, true>(x0),
-                         from_e4m3<BF, false>(x1), from_e4m3<BF, true>(x1)};
+              const uint32_t y0 = r[t][2 * e], y1 = r[t][2 * e + 1];
+              ka = u32x4{from_e4m3<BF, false>(y0), from_e4m3<BF, true>(y0),
+                         from_e4m3<BF, false>(y1), from_e4m3<BF, true>(y1)};
             } else {
-              ka = r.k[t][c];
+              ka = r[2 * e + t];
             }
-            s[t] = mfma16<BF>(ka, q[c], s[t]);
+            s[t] = mfma16<BF>(ka, q[c + e], s[t]);
           }
-        }
-        if (x + 1 < xe) load_k(x + 1);
+      }
+      if (NEXT) load(kb, pn, k_from, my);          // K has been read
 
-        float sv[8];
-        uint32_t seen = 0xFF;
+      float sv[8];
+      uint32_t seen = 0xFF;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sv[j] = s[j >> 2][j & 3] * sc;
-        if (!whole) {
-          seen = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int kj = key + 16 * (j >> 2) + 4 * lg + (j & 3);
-            const bool ok = (j < 4 ? p0 : p1) >= 0 && kj < sp.L && (kj >= sp.lo || kj < sp.nf);
-            if (ok) seen |= 1u << j;
-            else sv[j] = kNegInf;
-          }
-        }
-        float bm = sv[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) bm = fmaxf(bm, sv[j]);
-        bm = max_across_rows(bm);
-        const float mn = fmaxf(m, bm);
-        const float mu = mn == kNegInf ? 0.0f : mn;
-        const float alpha = exp2_fast(m - mu);
-        m = mn;
-        float ps = 0.0f;
+      for (int j = 0; j < 8; ++j) sv[j] = s[j >> 2][j & 3] * sc;
+      if (!whole) {
+        seen = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          sv[j] = exp2_fast(sv[j] - mu);
-          ps += sv[j];
+          const int kj = key + 16 * (j >> 2) + 4 * lg + (j & 3);
+          const bool ok = p.there[j >> 2] & (kj < sp.L) & ((kj >= sp.lo) | (kj < sp.nf));
+          seen |= ok ? 1u << j : 0u;
+          sv[j] = ok ? sv[j] : kNegInf;
         }
-        l = l * alpha + ps;
+      }
+      float bm = sv[0];
 #pragma unroll
-        for (int t = 0; t < VE; ++t)
+      for (int j = 1; j < 8; ++j) bm = fmaxf(bm, sv[j]);
+      bm = max_across_rows(bm);
+      const float mn = fmaxf(m, bm);
+      const float mu = mn == kNegInf ? 0.0f : mn;
+      const float alpha = exp2_fast(m - mu);
+      m = mn;
+      float ps = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[t][i] *= alpha;
-        u32x4 pb;
+      for (int j = 0; j < 8; ++j) {
+        sv[j] = exp2_fast(sv[j] - mu);
+        ps += sv[j];
+      }
+      l = l * alpha + ps;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pb[j] = pack16<BF>(sv[2 * j], sv[2 * j + 1]);
+      for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] *= alpha;
+      u32x4 pb;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pb[j] = pack16<BF>(sv[2 * j], sv[2 * j + 1]);
+      // what lies in masked places is not to enter, NaN included: keys of
+      // pairs (2 j, 2 j + 1) of the lane
+      uint32_t keep[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        keep[j] = ((seen >> (2 * j)) & 1 ? 0xFFFFu : 0u) |
+                  ((seen >> (2 * j + 1)) & 1 ? 0xFFFF0000u : 0u);
 
-        if (!whole) {      // what lies in masked places is not to enter, NaN included
+      wait_loads<NEXT ? LOADS : 0>();    // all but the next K's
+      const uint32_t va0 = my_at + KB + v_at;
+      if constexpr (F8) {
+        constexpr int VW = D / 64;       // dwords of D / 16 values
+        uint32_t v[8][VW];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; j += 4) {
+          typename Dwords<VW>::type y[4];
+          lds_read_x4<VW, ROW>(y[0], y[1], y[2], y[3], va0 + 16 * (j >> 2) * ROW);
 #pragma unroll
-            for (int e = 0; e < Raw::VB / 4; ++e)
-              r.v[j][e] = (seen >> j) & 1 ? r.v[j][e] : 0;
+          for (int i = 0; i < 4; ++i) __builtin_memcpy(v[j + i], &y[i], 4 * VW);
         }
 #pragma unroll
-        for (int e = 0; e < VE / 2; ++e) {
-          // dword e: values d, d + 1 of the lane's 8 keys
+        for (int e = 0; e < ND / 2; ++e) {
+          // values d, d + 1 of the lane's 8 keys, turned to pairs of keys
           uint32_t y[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if constexpr (F8)
-              y[j] = e & 1 ? from_e4m3<BF, true>(r.v[j][e >> 1])
-                           : from_e4m3<BF, false>(r.v[j][e >> 1]);
-            else
-              y[j] = r.v[j][e];
-          }
+          for (int j = 0; j < 8; ++j)
+            y[j] = e & 1 ? from_e4m3<BF, true>(v[j][e >> 1]) : from_e4m3<BF, false>(v[j][e >> 1]);
           u32x4 lo, hi;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            lo[j] = pair_lo(y[2 * j], y[2 * j + 1]);
-            hi[j] = pair_hi(y[2 * j], y[2 * j + 1]);
+            lo[j] = pair_lo(y[2 * j], y[2 * j + 1]) & keep[j];
+            hi[j] = pair_hi(y[2 * j], y[2 * j + 1]) & keep[j];
           }
           o[2 * e] = mfma16<BF>(lo, pb, o[2 * e]);
           o[2 * e + 1] = mfma16<BF>(hi, pb, o[2 * e + 1]);
         }
-        if (x + 1 < xe) load_v(x + 1);
+      } else {
+#pragma unroll
+        for (int t = 0; t < ND; t += 2) {
+          u32x2 z[4];                    // [tile of O][16-key tile]
+          lds_read_tr16x4<16 * ROW>(z[0], z[1], z[2], z[3],
+                                    my_at + KB + (v_at ^ (32 * t)),
+                                    my_at + KB + (v_at ^ (32 * t + 32)));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            u32x4 va = {z[2 * e][0], z[2 * e][1], z[2 * e + 1][0], z[2 * e + 1][1]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) va[j] &= keep[j];
+            o[t + e] = mfma16<BF>(va, pb, o[t + e]);
+          }
+        }
       }
+      if (NEXT) load(vb, pn, v_from, my + KB);     // V has been read
+    };
+
+    if (b0 < x_end) {
+      Place p = place_of(b0);
+      load(kb, p, k_from, my);
+      load(vb, p, v_from, my + KB);
+      int x = b0;
+      for (; x + 1 < x_end; ++x) {
+        const Place pn = place_of(x + 1);
+        block(std::true_type{}, x, p, pn);
+        p = pn;
+      }
+      block(std::false_type{}, x, p, p);
     }
 
     // join the four waves
@@ -338,20 +422,24 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
       s_ml[w][1][lc] = l;
     }
     if (lc < heads) {
+      float* dst = (float*)my + lc * (D + 4);
+      // e4m3: row 4 lg + i of tile t is value (D / 16) row + t
+      if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < VH; ++h) {
-          float* dst = &s_o[w][lc][h * (D / VH) + VW * (4 * lg + i)];
+          for (int t = 0; t < ND; t += 4)
+            *(f32x4*)(dst + ND * (4 * lg + i) + t) =
+                f32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
+      } else {
 #pragma unroll
-          for (int t = 0; t < VW; t += 4)
-            *(f32x4*)(dst + t) = f32x4{o[h * VW + t][i], o[h * VW + t + 1][i],
-                                       o[h * VW + t + 2][i], o[h * VW + t + 3][i]};
-        }
+        for (int t = 0; t < ND; ++t) *(f32x4*)(dst + 16 * t + 4 * lg) = o[t];
+      }
     }
     __syncthreads();
     {
       // thread: head hh, values d0 .. d0 + D / 16 - 1
+      constexpr int VE = D / 16;
       const int hh = tid >> 4, d0 = (tid & 15) * VE;
       const bool whole_pair = b0 == 0 && b1 == ns;
       if (hh < heads) {
@@ -368,7 +456,7 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
           ll += f * s_ml[i][1][hh];
 #pragma unroll
           for (int t = 0; t < VE; t += 4) {
-            const f32x4 y = *(const f32x4*)&s_o[i][hh][d0 + t];
+            const f32x4 y = *(const f32x4*)((const float*)s_wave[i] + hh * (D + 4) + d0 + t);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[t + e] += f * y[e];
           }

@@ -35,8 +35,6 @@
 namespace moe {
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
 // keys of a tile, rows of a workgroup's tile
 template <int D>
 struct PreShape {

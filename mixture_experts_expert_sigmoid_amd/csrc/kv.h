@@ -59,7 +59,9 @@ struct AttnArgs {
 // slots, two a workgroup (the sequence it continues, the one it leaves open),
 // of 16 rows of D floats + 16 maxima + 16 sums; and one (first workgroup,
 // count) pair per (sequence, key-value head, 16 query heads).
-constexpr int dec_waves(int D, bool f8) { return D == 64 ? 4 : D == 128 && f8 ? 3 : 2; }
+constexpr int dec_waves(int D, bool f8) {        // per SIMD; bound by LDS
+  return D == 64 ? 4 : D == 128 ? (f8 ? 4 : 2) : (f8 ? 2 : 1);
+}
 constexpr int dec_wgs(int D, bool f8) { return 256 * dec_waves(D, f8); }
 constexpr int kDecMaxSeqs = 512;        // sequences per launch
 constexpr int kDecKeys = 32;            // keys of one wave's step
