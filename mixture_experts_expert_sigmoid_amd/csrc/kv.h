@@ -62,7 +62,7 @@ struct AttnArgs {
 constexpr int dec_waves(int D, bool f8) {        // per SIMD; bound by LDS
   return D == 64 ? 4 : D == 128 ? (f8 ? 4 : 2) : (f8 ? 2 : 1);
 }
-constexpr int dec_wgs(int D, bool f8) { return 256 * dec_waves(D, f8); }
+constexpr int dec_wgs(int D, bool f8) { return D == 64 ? 768 : 256 * (dec_waves(D, f8) < 2 ? 1 : 2); }
 constexpr int kDecMaxSeqs = 512;        // sequences per launch
 constexpr int kDecKeys = 32;            // keys of one wave's step
 size_t decode_ws_bytes(long n, int hq, int hkv, int D, bool f8);

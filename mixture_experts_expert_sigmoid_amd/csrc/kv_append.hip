@@ -1,7 +1,9 @@
-// New keys and values into the pages of a cache. One thread per 8 values:
-// a 16-byte load, the quantisation for e4m3 caches, an 8- or 16-byte store.
-// Bound by HBM for prompts (input read once, codes written once) and by the
-// launch for single tokens.
+// New keys and values into the pages of a cache. A workgroup takes a few rows
+// (tokens): one thread a row finds its page -- sequence, slot, start, table
+// entry: four or more dependent loads -- while the others' loads of the rows
+// are on their way, then all quantise (e4m3 caches) and store. Bound by HBM
+// for prompts (input read once, codes written once), by latency and launch for
+// single tokens.
 #include "common.h"
 #include "kv.h"
 
@@ -16,71 +18,146 @@ __device__ __forceinline__ float in_f32(uint32_t b) {
 
 // four quotients -> four e4m3 codes: saturated to +-448 first (the conversion
 // alone gives NaN beyond), NaN -> 0x7F
-__device__ __forceinline__ uint32_t pack4(const float (&q)[4]) {
+// (finite: there is none)
+__device__ __forceinline__ uint32_t pack4(const float (&q)[4], bool finite) {
   float c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(q[i], -448.0f), 448.0f);
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
   uint32_t o = (uint32_t)w;
+  if (finite) return o;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (q[i] != q[i]) o = (o & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
   return o;
 }
 
+constexpr int kMaxRows = 8;      // rows of a workgroup
+constexpr int kBatch = 4;        // 16-byte loads of a thread in flight
+
 // IN: type of the rows; Q: into an e4m3 cache
 template <int IN, bool Q>
-__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-  const int upr = a.c.D >> 3;                     // 16-byte units per row, a power of two
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
+  __shared__ long s_off[kMaxRows];                // place of the row's token; -1: none
+  const int upr = a.c.D >> 3;                     // 16-byte units per head, a power of two
   const int lg = __builtin_ctz(upr);
   const int per = 2 * a.c.hkv * upr;              // units per token
-  const long total = a.T * per, step = (long)gridDim.x * 256;
-  for (long u = (long)blockIdx.x * 256 + threadIdx.x; u < total; u += step) {
-    const long r = u / per;
-    const int x = (int)(u - r * per), c8 = x & (upr - 1);
-    const int kvh = x >> lg, val = kvh >= a.c.hkv, h = kvh - val * a.c.hkv;
-    // the sequence of row r: the last i with cu[i] <= r
-    int i = (int)r;
-    int first = (int)r;
-    if (a.cu) {
-      int lo = 0, hi = a.n - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= r) lo = mid; else hi = mid - 1;
-      }
-      i = lo;
-      first = a.cu[i];
-      if (r < first || r >= a.cu[i + 1]) continue;
-    }
-    const char* src = (val ? a.v + r * a.v_row + h * a.v_head : a.k + r * a.k_row + h * a.k_head) +
-                      c8 * 16;
-    const uint4 in = *(const uint4*)src;
-    const int slot = kv_slot(a.slots, i, a.t.n_slots, a.err);
-    const int at = a.start[i];
-    if (slot < 0 || at < 0) continue;
-    const long pos = (long)at + (r - first);
-    int page = -1;
-    if (pos < (long)a.t.max_pages * a.t.ps) page = a.t.table[slot * a.t.ld + pos / a.t.ps];
-    if (page < 0 || page >= a.t.n_pages) {
-      atomicOr(a.err, kErrPage);
-      continue;
-    }
-    char* dst = (val ? a.c.v : a.c.k) + page * a.c.sp + h * a.c.sh + (pos % a.t.ps) * a.c.st;
-    if (Q) {
-      const float s = (val ? a.c.vs : a.c.ks)[h];
-      const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-      uint32_t o[2];
+  const int tid = threadIdx.x;
+  const long r0 = (long)blockIdx.x * rows;
+  const int nr = (int)min((long)rows, a.T - r0);
+
+  // unit x of row `row`, 256 units on a time
+  int row = tid / per, x = tid - row * per;
+  const int step_row = 256 / per, step_x = 256 - step_row * per;
+  bool first = true;
+  while (true) {
+    int br[kBatch], bx[kBatch];
+    uint4 in[kBatch];
+    bool any = false;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float f[4] = {in_f32<IN>(w[2 * j] & 0xFFFF) / s, in_f32<IN>(w[2 * j] >> 16) / s,
-                            in_f32<IN>(w[2 * j + 1] & 0xFFFF) / s,
-                            in_f32<IN>(w[2 * j + 1] >> 16) / s};
-        o[j] = pack4(f);
+    for (int k = 0; k < kBatch; ++k) {
+      br[k] = row;
+      bx[k] = x;
+      in[k] = make_uint4(0, 0, 0, 0);
+      if (row < nr) {
+        const int kvh = x >> lg, val = kvh >= a.c.hkv, h = kvh - val * a.c.hkv;
+        const long r = r0 + row;
+        in[k] = *(const uint4*)((val ? a.v + r * a.v_row + h * a.v_head
+                                     : a.k + r * a.k_row + h * a.k_head) +
+                                (x & (upr - 1)) * 16);
+        any = true;
       }
-      *(uint2*)(dst + c8 * 8) = make_uint2(o[0], o[1]);
-    } else {
-      *(uint4*)(dst + c8 * 16) = in;
+      row += step_row;
+      x += step_x;
+      if (x >= per) {
+        x -= per;
+        ++row;
+      }
+    }
+    if (first) {
+      first = false;
+      if (tid < nr) {
+        // the sequence of row r: the last i with cu[i] <= r
+        const long r = r0 + tid;
+        int i = (int)r, at0 = (int)r;
+        bool have = true;
+        if (a.cu) {
+          int lo = 0, hi = a.n - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.cu[mid] <= r) lo = mid; else hi = mid - 1;
+          }
+          i = lo;
+          at0 = a.cu[i];
+          have = r >= at0 && r < a.cu[i + 1];
+        }
+        long off = -1;
+        if (have) {
+          const int start = a.start[i], slot = kv_slot(a.slots, i, a.t.n_slots, a.err);
+          if (slot >= 0 && start >= 0) {
+            const long pos = (long)start + (r - at0);
+            int page = -1, e = 0;
+            if (pos < (long)a.t.max_pages * a.t.ps) {
+              e = kv_entry(a.t, (int)pos);
+              page = a.t.table[slot * a.t.ld + e];
+            }
+            if (page >= 0 && page < a.t.n_pages)
+              off = page * a.c.sp + (pos - (long)e * a.t.ps) * a.c.st;
+            else
+              atomicOr(a.err, kErrPage);
+          }
+        }
+        s_off[tid] = off;
+      }
+      __syncthreads();
+    }
+    if (!any) return;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (br[k] >= nr) continue;
+      const long off = s_off[br[k]];
+      if (off < 0) continue;
+      const int kvh = bx[k] >> lg, val = kvh >= a.c.hkv, h = kvh - val * a.c.hkv;
+      const int c8 = bx[k] & (upr - 1);
+      char* dst = (val ? a.c.v : a.c.k) + off + h * a.c.sh;
+      if (Q) {
+        // x / s: with y = RN(1 / s), q0 = RN(x y) and the residual x - q0 s,
+        // exact by FMA, RN(q0 + residual y) is the correctly rounded quotient
+        // (Markstein's theorem) where nothing leaves the normal range or the
+        // quotient is far below the least code; other lanes divide. Three
+        // operations a value instead of the division's ten.
+        const float s = (val ? a.c.vs : a.c.ks)[h];
+        const float as = fabsf(s);
+        const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+        float f[8];
+        bool fast = as >= 0x1p-60f && as <= 0x1p60f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[j] = in_f32<IN>(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFF);
+          fast &= f[j] == 0.0f || (fabsf(f[j]) >= 0x1p-60f && fabsf(f[j]) <= 0x1p60f);
+        }
+        if (fast) {
+          const float y = 1.0f / s;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float q0 = __fmul_rn(f[j], y);
+            f[j] = __builtin_fmaf(__builtin_fmaf(-q0, s, f[j]), y, q0);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = f[j] / s;
+        }
+        uint32_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float q[4] = {f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]};
+          o[j] = pack4(q, fast);
+        }
+        *(uint2*)(dst + c8 * 8) = make_uint2(o[0], o[1]);
+      } else {
+        *(uint4*)(dst + c8 * 16) = in[k];
+      }
     }
   }
 }
@@ -88,16 +165,17 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 }  // namespace
 
 hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s) {
-  const long total = a.T * 2 * a.c.hkv * (a.c.D >> 3);
-  const long blocks = (total + 255) / 256;
-  const int grid = (int)(blocks < 16384 ? blocks : 16384);
+  // a row a workgroup as long as there are few, so that single tokens spread
+  // over the CUs; more of them share one lookup's latency for prompts
+  const int rows = (int)(a.T >= 1024 * kMaxRows ? kMaxRows : a.T < 2048 ? 1 : a.T / 1024);
+  const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
   const bool q = a.c.fmt == KV_E4M3;
   if (!q)
-    append_kernel<KV_BF16, false><<<grid, 256, 0, s>>>(a);   // bits only, either type
+    append_kernel<KV_BF16, false><<<grid, 256, 0, s>>>(a, rows);   // bits only, either type
   else if (fmt == KV_BF16)
-    append_kernel<KV_BF16, true><<<grid, 256, 0, s>>>(a);
+    append_kernel<KV_BF16, true><<<grid, 256, 0, s>>>(a, rows);
   else
-    append_kernel<KV_F16, true><<<grid, 256, 0, s>>>(a);
+    append_kernel<KV_F16, true><<<grid, 256, 0, s>>>(a, rows);
   return hipGetLastError();
 }
 

@@ -278,13 +278,13 @@ __global__ __launch_bounds__(kThreads) void fork_plan_kernel(KvTable t, const in
   }
 }
 
-// second launch: the table rows, lengths and counts of the shared pages
-__global__ __launch_bounds__(256) void fork_rows_kernel(KvTable t, const int* src,
-                                                        const int* dst, ForkPlan p) {
-  const int i = blockIdx.x;
+// second launch, beside the copies: the table rows, lengths and counts of the
+// shared pages; one workgroup per pair
+__device__ void fork_rows(const KvTable& t, const int* src, const int* dst, const ForkPlan& p,
+                          int i) {
   const int L = p.len[i];
   if (L < 0) return;
-  const int *from = t.table + src[i] * t.ld;
+  const int* from = t.table + src[i] * t.ld;
   int* to = t.table + dst[i] * t.ld;
   const int whole = L / t.ps;
   for (int j = threadIdx.x; j < whole; j += 256) {
@@ -300,25 +300,21 @@ __global__ __launch_bounds__(256) void fork_rows_kernel(KvTable t, const int* sr
 
 // ----------------------------------------------------------- page contents
 // Copies page from[i] to page to[i] in every array of cl. A workgroup moves
-// 16 KB at a time, four 16-byte loads of each thread in flight. n_dev: the
-// number of pairs in device memory, or NULL (then n). Bound by HBM: every
-// byte moved is read once and written once.
-constexpr int kPart = 1024;             // 16-byte units of one workgroup's step
-
-__global__ __launch_bounds__(256) void copy_pages_kernel(CopyLayers cl, const int* from,
-                                                         const int* to, long n,
-                                                         const int* n_dev, int n_pages,
-                                                         int* err) {
+// 256 x NU units of 16 bytes at a time, NU loads of each thread in flight.
+// n_dev: the number of pairs in device memory, or NULL (then n). Bound by HBM:
+// every byte moved is read once and written once.
+template <int NU>
+__device__ void copy_pages(const CopyLayers& cl, const int* from, const int* to, long n,
+                           const int* n_dev, int n_pages, int* err, int wg, int wgs) {
   if (n_dev) n = *n_dev;
   const int rows = cl.hkv * cl.ps, upr = cl.row_bytes >> 4;
-  const int units = rows * upr, parts = (units + kPart - 1) / kPart;
+  const int units = rows * upr, parts = (units + 256 * NU - 1) / (256 * NU);
   const int lg = __builtin_ctz(upr);    // 4..32 units in a row
-  const long items = n * parts * cl.n;
-  for (long it = blockIdx.x; it < items; it += gridDim.x) {
-    const long pp = it / cl.n;
-    const int arr = (int)(it - pp * cl.n);
-    const long pair = pp / parts;
-    const int part = (int)(pp - pair * parts);
+  const int per = parts * cl.n;         // items of a pair
+  const long items = n * per;
+  for (long it = wg; it < items; it += wgs) {
+    const long pair = it / per;
+    const int rest = (int)(it - pair * per), part = rest / cl.n, arr = rest - part * cl.n;
     const int a = from[pair], b = to[pair];
     if (a < 0 || b < 0) continue;
     if (a >= n_pages || b >= n_pages) {
@@ -327,11 +323,11 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(CopyLayers cl, const in
     }
     const char* s = cl.p[arr] + a * cl.sp;
     char* d = cl.p[arr] + b * cl.sp;
-    uint4 v[4];
-    long off[4];
+    uint4 v[NU];
+    long off[NU];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = part * kPart + k * 256 + threadIdx.x;
+    for (int k = 0; k < NU; ++k) {
+      const int u = (part * NU + k) * 256 + threadIdx.x;
       if (cl.linear) {
         off[k] = (long)u << 4;
       } else {
@@ -341,25 +337,59 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(CopyLayers cl, const in
       if (u < units) v[k] = *(const uint4*)(s + off[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = part * kPart + k * 256 + threadIdx.x;
+    for (int k = 0; k < NU; ++k) {
+      const int u = (part * NU + k) * 256 + threadIdx.x;
       if (u < units) *(uint4*)(d + off[k]) = v[k];
     }
   }
 }
 
+// 16 KB a step for many pages, 4 KB for few, which then spread over more CUs
+constexpr int kMany = 4, kFew = 1;
 // enough workgroups for the copies' loads to cover the memory latency; a
 // call with fewer parts launches one each
 constexpr long kCopyGrid = 4096;
 
+long copy_items(const CopyLayers& cl, long n, int nu) {
+  const long units = (long)cl.hkv * cl.ps * (cl.row_bytes >> 4);
+  return n * ((units + 256 * nu - 1) / (256 * nu)) * cl.n;
+}
+int copy_nu(const CopyLayers& cl, long n) {
+  return copy_items(cl, n, kMany) >= 1024 ? kMany : kFew;
+}
+int copy_grid(const CopyLayers& cl, long n, int nu) {
+  const long items = copy_items(cl, n, nu);
+  return (int)(items < kCopyGrid ? items : kCopyGrid);
+}
+
+template <int NU>
+__global__ __launch_bounds__(256) void copy_pages_kernel(CopyLayers cl, const int* from,
+                                                         const int* to, long n,
+                                                         const int* n_dev, int n_pages,
+                                                         int* err) {
+  copy_pages<NU>(cl, from, to, n, n_dev, n_pages, err, blockIdx.x, gridDim.x);
+}
+
+// the pairs' rows by the first n workgroups, copies by the others
+template <int NU>
+__global__ __launch_bounds__(256) void fork_kernel(CopyLayers cl, KvTable t, const int* src,
+                                                   const int* dst, int n, ForkPlan p) {
+  if ((int)blockIdx.x < n)
+    fork_rows(t, src, dst, p, blockIdx.x);
+  else
+    copy_pages<NU>(cl, p.from, p.to, n, nullptr, t.n_pages, nullptr, blockIdx.x - n,
+                   gridDim.x - n);
+}
+
 hipError_t copy_all(const CopyLayers* cl, int n_cl, const int* from, const int* to, long n,
                     const int* n_dev, int n_pages, int* err, hipStream_t s) {
   for (int i = 0; i < n_cl; ++i) {
-    const long units = (long)cl[i].hkv * cl[i].ps * (cl[i].row_bytes >> 4);
-    const long items = n * ((units + kPart - 1) / kPart) * cl[i].n;
-    const int grid = (int)(items < kCopyGrid ? items : kCopyGrid);
+    const int nu = copy_nu(cl[i], n), grid = copy_grid(cl[i], n, nu);
     if (grid == 0) continue;
-    copy_pages_kernel<<<grid, 256, 0, s>>>(cl[i], from, to, n, n_dev, n_pages, err);
+    if (nu == kMany)
+      copy_pages_kernel<kMany><<<grid, 256, 0, s>>>(cl[i], from, to, n, n_dev, n_pages, err);
+    else
+      copy_pages_kernel<kFew><<<grid, 256, 0, s>>>(cl[i], from, to, n, n_dev, n_pages, err);
   }
   return hipGetLastError();
 }
@@ -404,10 +434,18 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const int* refs, int P, 
   __shared__ int s_cnt[kWaves];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   long all = 0, before = 0;
-  for (int i = threadIdx.x; i < segs; i += kThreads) {
-    const int c = pl.seg_used[i];
-    all += c;
-    if (i < (int)blockIdx.x) before += c;
+  if (segs == 1) {                       // counted here: no launch before this one
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const long p = k * kThreads + threadIdx.x;
+      all += p < P ? refs[p] > 0 : 0;
+    }
+  } else {
+    for (int i = threadIdx.x; i < segs; i += kThreads) {
+      const int c = pl.seg_used[i];
+      all += c;
+      if (i < (int)blockIdx.x) before += c;
+    }
   }
   long U, base;
   block_scan(all, s_w, &U);
@@ -415,7 +453,8 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const int* refs, int P, 
   // used(U): the segments before U's, and the used pages of its own below U
   const int useg = (int)(U / kSeg);
   long part = 0;
-  for (int i = threadIdx.x; i < segs && i < useg; i += kThreads) part += pl.seg_used[i];
+  if (segs > 1)
+    for (int i = threadIdx.x; i < segs && i < useg; i += kThreads) part += pl.seg_used[i];
   for (long p = (long)useg * kSeg + threadIdx.x; p < U; p += kThreads) part += refs[p] > 0;
   long used_u;
   block_scan(part, s_w, &used_u);
@@ -454,9 +493,9 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const int* refs, int P, 
 }
 
 // table entries and counts follow the pages
-__global__ __launch_bounds__(256) void remap_kernel(KvTable t, CompactPlan pl) {
+__device__ void remap(const KvTable& t, const CompactPlan& pl, int wg, int wgs) {
   const int U = pl.hdr[0], K = pl.hdr[1];
-  const long stride = (long)gridDim.x * 256, tid = (long)blockIdx.x * 256 + threadIdx.x;
+  const long stride = (long)wgs * 256, tid = (long)wg * 256 + threadIdx.x;
   for (long i = tid; i < K; i += stride) {
     const int h = pl.holes[i], m = pl.movers[i];
     t.refs[h] = t.refs[m];
@@ -473,6 +512,17 @@ __global__ __launch_bounds__(256) void remap_kernel(KvTable t, CompactPlan pl) {
       if (r >= 0 && r < K && pl.movers[r] == p) *e = pl.holes[r];
     }
   }
+}
+
+// the tables by the first `remaps` workgroups, copies by the others
+template <int NU>
+__global__ __launch_bounds__(256) void compact_kernel(CopyLayers cl, KvTable t, CompactPlan pl,
+                                                      int remaps) {
+  if ((int)blockIdx.x < remaps)
+    remap(t, pl, blockIdx.x, remaps);
+  else
+    copy_pages<NU>(cl, pl.movers, pl.holes, 0, pl.hdr + 1, t.n_pages, nullptr,
+                   blockIdx.x - remaps, gridDim.x - remaps);
 }
 
 inline size_t al16(size_t b) { return (b + 15) & ~(size_t)15; }
@@ -520,8 +570,12 @@ hipError_t launch_cache_fork(const CopyLayers* cl, int n_cl, const KvTable& t, c
   const size_t a = al16((size_t)n * 4);
   ForkPlan p{(int*)w, (int*)(w + a), (int*)(w + 2 * a)};
   fork_plan_kernel<<<1, kThreads, 0, s>>>(t, src, dst, (int)n, p, seg, err);
-  fork_rows_kernel<<<(int)n, 256, 0, s>>>(t, src, dst, p);
-  return copy_all(cl, n_cl, p.from, p.to, n, nullptr, t.n_pages, nullptr, s);
+  const int nu = copy_nu(cl[0], n), grid = (int)n + copy_grid(cl[0], n, nu);
+  if (nu == kMany)
+    fork_kernel<kMany><<<grid, 256, 0, s>>>(cl[0], t, src, dst, (int)n, p);
+  else
+    fork_kernel<kFew><<<grid, 256, 0, s>>>(cl[0], t, src, dst, (int)n, p);
+  return copy_all(cl + 1, n_cl - 1, p.from, p.to, n, nullptr, t.n_pages, nullptr, s);
 }
 
 hipError_t launch_cache_compact(const CopyLayers* cl, int n_cl, const KvTable& t, int* n_used,
@@ -536,13 +590,19 @@ hipError_t launch_cache_compact(const CopyLayers* cl, int n_cl, const KvTable& t
   pl.holes = (int*)w;
   pl.movers = (int*)(w + a);
   pl.rank = (int*)(w + 2 * a);
-  count_used_kernel<<<segs, kThreads, 0, s>>>(t.refs, t.n_pages, pl.seg_used);
+  if (segs > 1) count_used_kernel<<<segs, kThreads, 0, s>>>(t.refs, t.n_pages, pl.seg_used);
   rank_kernel<<<segs, kThreads, 0, s>>>(t.refs, t.n_pages, segs, pl, n_used);
   const long entries = (long)t.n_slots * t.max_pages;
   const long blocks = (entries + 1023) / 1024;
-  remap_kernel<<<(int)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(t, pl);
+  const int remaps = (int)(blocks < 1024 ? blocks : 1024);
   // at most half of the pool moves
-  return copy_all(cl, n_cl, pl.movers, pl.holes, t.n_pages / 2, pl.hdr + 1, t.n_pages, nullptr,
+  const long most = t.n_pages / 2;
+  const int nu = copy_nu(cl[0], most), grid = remaps + copy_grid(cl[0], most, nu);
+  if (nu == kMany)
+    compact_kernel<kMany><<<grid, 256, 0, s>>>(cl[0], t, pl, remaps);
+  else
+    compact_kernel<kFew><<<grid, 256, 0, s>>>(cl[0], t, pl, remaps);
+  return copy_all(cl + 1, n_cl - 1, pl.movers, pl.holes, most, pl.hdr + 1, t.n_pages, nullptr,
                   s);
 }
 
