@@ -13,15 +13,18 @@ hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
 
 namespace {
 inline size_t al16(size_t b) { return (b + 15) & ~(size_t)15; }
-size_t dec_part_bytes(int D, bool f8) {
-  return (size_t)dec_wgs(D, f8) * 2 * (32 + 16 * D) * 4;
+size_t dec_part_bytes(long pairs, int g, int D, bool f8) {
+  const size_t teams = (size_t)dec_wgs(D, f8) * 4 / dec_team(pairs, D, f8);
+  return teams * 2 * (32 + (g < 16 ? g : 16) * D) * 4;
 }
 }  // namespace
 
 size_t decode_ws_bytes(long n, int hq, int hkv, int D, bool f8) {
+  // the first launch of a large batch has the most pairs
   const long m = n < kDecMaxSeqs ? n : kDecMaxSeqs;
-  const int ht = (hq / hkv + 15) / 16;
-  return dec_part_bytes(D, f8) + al16((size_t)m * hkv * ht * 8);
+  const int g = hq / hkv;
+  const long pairs = m * hkv * ((g + 15) / 16);
+  return dec_part_bytes(pairs, g, D, f8) + al16((size_t)pairs * 8);
 }
 
 hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
@@ -39,7 +42,8 @@ hipError_t launch_attn_decode(const AttnArgs& all, int fmt, hipStream_t s) {
     a.q += b * a.q_row;
     a.out += b * a.o_row;
     if (a.lse) a.lse += b * a.hq;
-    a.meta = (int*)((char*)a.part + dec_part_bytes(a.c.D, a.c.fmt == KV_E4M3));
+    const long pairs = (long)a.n * a.c.hkv * ((a.g + 15) / 16);
+    a.meta = (int*)((char*)a.part + dec_part_bytes(pairs, a.g, a.c.D, a.c.fmt == KV_E4M3));
     hipError_t e = a.c.D == 64    ? launch_decode_64(a, fmt, s)
                    : a.c.D == 128 ? launch_decode_128(a, fmt, s)
                                   : launch_decode_256(a, fmt, s);

@@ -16,11 +16,14 @@
 // transposed (ds_read_b64_tr_b16) in that key order; e4m3 values are expanded
 // and turned round in the lane.
 //
-// Split. The keys that each sequence sees are cut into units of 128 (32 per
-// wave); the units of all (sequence, key-value head) pairs, laid end to end,
-// are dealt out evenly to the workgroups whatever the lengths. A workgroup
-// finishes every pair that lies wholly in its run; of the first and the last
-// it leaves fp32 partial results that the join kernel adds in order.
+// Split. The keys that each sequence sees are cut into units; the units of all
+// (sequence, key-value head) pairs, laid end to end, are dealt out evenly to
+// teams whatever the lengths. A team finishes every pair that lies wholly in
+// its run; of the first and the last it leaves fp32 partial results that the
+// join kernel adds in order. A team is a workgroup (units of four blocks, a
+// wave each, joined through LDS), or a single wave where there are many pairs:
+// short contexts then run side by side instead of four waves waiting for the
+// same few loads.
 //
 // Bound: HBM reads of K and V; short contexts by latency (length -> table ->
 // keys -> join).
@@ -32,10 +35,7 @@
 namespace moe {
 namespace {
 
-constexpr int kDecUnit = 4 * kDecKeys;
-constexpr int kDecPartRow = 32;       // maxima and sums before the D floats of 16 heads
-
-__device__ __host__ inline size_t dec_slot_floats(int D) { return (size_t)kDecPartRow + 16 * D; }
+constexpr int kDecPartRow = 32;       // maxima and sums of 16 heads, before their D floats each
 
 // what a query at position L - 1 sees, as blocks of 32 keys: blocks 0..nb1-1
 // (first keys), then those from b2 on up to the length
@@ -53,8 +53,9 @@ __device__ __forceinline__ DecSpan dec_span(int L, int window, int first) {
   s.nb = s.nb1 + (L + kDecKeys - 1) / kDecKeys - s.b2;
   return s;
 }
+template <int TS>
 __device__ __forceinline__ int dec_units(const DecSpan& s) {
-  const int u = (s.nb + 3) >> 2;
+  const int u = (s.nb + TS - 1) / TS;
   return u > 0 ? u : 1;               // a sequence without keys still gets its row written
 }
 
@@ -101,7 +102,7 @@ __device__ __forceinline__ void lds_read_x4(Words& a, Words& b, Words& c, Words&
 #undef MOE_READ4
 }
 
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int TS>
 __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(AttnArgs a) {
   constexpr int NC = D / 32;             // 32-deep steps of the first product
   constexpr int ND = D / 16;             // 16-row tiles of O^T
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
     if (i < n) {
       const int L = kv_len(a.t, kv_slot(a.slots, i, a.t.n_slots, a.err));
       s_len[i] = L;
-      un[k] = dec_units(dec_span(L, a.window, a.first));
+      un[k] = dec_units<TS>(dec_span(L, a.window, a.first));
     }
   }
   int incl = un[0] + un[1];
@@ -150,10 +151,11 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
   __syncthreads();
 
   const long U = (long)s_pref[n] * HT;
-  const long W = U < (long)gridDim.x ? U : (long)gridDim.x;
-  if ((long)blockIdx.x >= W) return;
-  long u = (long)blockIdx.x * U / W;
-  const long u_end = ((long)blockIdx.x + 1) * U / W;
+  const long teams = (long)gridDim.x * (4 / TS), team = TS == 4 ? blockIdx.x : 4 * blockIdx.x + w;
+  const long W = U < teams ? U : teams;
+  if (team >= W) return;
+  long u = team * U / W;
+  const long u_end = (team + 1) * U / W;
 
   // the sequence of unit u: the last i with pref[i] * HT <= u
   int seq = 0;
@@ -198,10 +200,11 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
     const int slot = a.slots ? a.slots[seq] : seq;
     const int* row = a.t.table + (long)(slot < 0 || slot >= a.t.n_slots ? 0 : slot) * a.t.ld;
 
-    // blocks 4 x + w of units x = b0 .. b1 - 1 are this wave's
-    const int x_end = __builtin_amdgcn_readfirstlane(min(b1, (sp.nb - w + 3) >> 2));
+    // blocks TS x + (w of a team of four) of units x = b0 .. b1 - 1 are this wave's
+    const int wt = TS == 4 ? w : 0;
+    const int x_end = __builtin_amdgcn_readfirstlane(min(b1, (sp.nb - wt + TS - 1) / TS));
     auto key_of = [&](int x) {
-      const int bi = 4 * x + w;
+      const int bi = TS * x + wt;
       return kDecKeys * (bi < sp.nb1 ? bi : sp.b2 + bi - sp.nb1);
     };
     // Byte offset in the cache of the two 16-key tiles of the next 64 blocks,
@@ -415,33 +418,77 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
       block(std::false_type{}, x, p, p);
     }
 
-    // join the four waves
     l = xor32_reduce(xor16_reduce(l, OpSum{}), OpSum{});
-    if (lg == 0) {
-      s_ml[w][0][lc] = m;
-      s_ml[w][1][lc] = l;
+    const bool whole_pair = b0 == 0 && b1 == ns;
+    const int hs = min(16, a.g);         // rows of a slot
+    float* const slot_p = a.part + (2 * team + (b0 == 0)) * (kDecPartRow + (long)hs * D);
+    if (b0 == 0 && (TS == 4 ? tid : lane) == 0) {
+      // the team of the pair's last unit: the largest w with w U / W <= unit
+      const long last = (long)pre * HT + (long)(hti + 1) * ns - 1;
+      const long wl = ((last + 1) * W - 1) / U;
+      int* me = a.meta + 2 * ((long)seq * HT + hti);
+      me[0] = (int)team;
+      me[1] = (int)(wl - team) + 1;
     }
-    if (lc < heads) {
-      float* dst = (float*)my + lc * (D + 4);
-      // e4m3: row 4 lg + i of tile t is value (D / 16) row + t
-      if constexpr (F8) {
+    const float vs = F8 ? a.c.vs[kvh] : 1.0f;
+    if constexpr (TS == 1) {
+      if (lc < heads) {
+        const int head = kvh * a.g + hbase + lc;
+        const float inv = l == 0.0f ? 0.0f : vs / l;     // no visible key: 0
+        char* dst = a.out + seq * a.o_row + head * a.o_head;
+        float* part = slot_p + kDecPartRow + lc * D;
+        // four values of the head from d on; e4m3: row 4 lg + i of tile t is
+        // value (D / 16) row + t
+        auto put = [&](int d, f32x4 y) {
+          if (whole_pair)
+            *(u32x2*)(dst + 2 * d) = u32x2{pack16<BF>(y[0] * inv, y[1] * inv),
+                                           pack16<BF>(y[2] * inv, y[3] * inv)};
+          else
+            *(f32x4*)(part + d) = y;
+        };
+        if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int t = 0; t < ND; t += 4)
-            *(f32x4*)(dst + ND * (4 * lg + i) + t) =
-                f32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
-      } else {
+            for (int t = 0; t < ND; t += 4)
+              put(ND * (4 * lg + i) + t, f32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]});
+        } else {
 #pragma unroll
-        for (int t = 0; t < ND; ++t) *(f32x4*)(dst + 16 * t + 4 * lg) = o[t];
+          for (int t = 0; t < ND; ++t) put(16 * t + 4 * lg, o[t]);
+        }
+        if (lg == 0) {
+          if (!whole_pair) {
+            slot_p[lc] = m;
+            slot_p[16 + lc] = l;
+          } else if (a.lse) {
+            a.lse[(long)seq * a.hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+          }
+        }
       }
-    }
-    __syncthreads();
-    {
+    } else {
+      // join the four waves
+      if (lg == 0) {
+        s_ml[w][0][lc] = m;
+        s_ml[w][1][lc] = l;
+      }
+      if (lc < heads) {
+        float* dst = (float*)my + lc * (D + 4);
+        if constexpr (F8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < ND; t += 4)
+              *(f32x4*)(dst + ND * (4 * lg + i) + t) =
+                  f32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
+        } else {
+#pragma unroll
+          for (int t = 0; t < ND; ++t) *(f32x4*)(dst + 16 * t + 4 * lg) = o[t];
+        }
+      }
+      __syncthreads();
       // thread: head hh, values d0 .. d0 + D / 16 - 1
       constexpr int VE = D / 16;
       const int hh = tid >> 4, d0 = (tid & 15) * VE;
-      const bool whole_pair = b0 == 0 && b1 == ns;
       if (hh < heads) {
         float mm = kNegInf;
 #pragma unroll
@@ -463,8 +510,7 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
         }
         const int head = kvh * a.g + hbase + hh;
         if (whole_pair) {
-          float inv = ll == 0.0f ? 0.0f : 1.0f / ll;     // no visible key: 0
-          if (F8 && ll != 0.0f) inv *= a.c.vs[kvh];
+          const float inv = ll == 0.0f ? 0.0f : vs / ll;       // no visible key: 0
           char* dst = a.out + seq * a.o_row + head * a.o_head + 2 * d0;
 #pragma unroll
           for (int t = 0; t < VE; t += 4) {
@@ -475,7 +521,6 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
           if (a.lse && (tid & 15) == 0)
             a.lse[(long)seq * a.hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
         } else {
-          float* slot_p = a.part + (2 * (long)blockIdx.x + (b0 == 0)) * dec_slot_floats(D);
           if ((tid & 15) == 0) {
             slot_p[hh] = mm;
             slot_p[16 + hh] = ll;
@@ -486,22 +531,14 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
                 f32x4{acc[t], acc[t + 1], acc[t + 2], acc[t + 3]};
         }
       }
-      if (b0 == 0 && tid == 0) {
-        // the workgroup of the pair's last unit: the largest w with w U / W <= unit
-        const long last = (long)pre * HT + (long)(hti + 1) * ns - 1;
-        const long wl = ((last + 1) * W - 1) / U;
-        int* me = a.meta + 2 * ((long)seq * HT + hti);
-        me[0] = blockIdx.x;
-        me[1] = (int)(wl - blockIdx.x) + 1;
-      }
+      __syncthreads();
     }
-    __syncthreads();
     u += b1 - b0;
     if (hti == HT - 1 && b1 == ns) ++seq;
   }
 }
 
-// Joins the parts of the pairs that more than one workgroup had, in their
+// Joins the parts of the pairs that more than one team had, in their
 // order, eight parts' loads in flight: up to eight parts by one wave a head (a
 // lane has D / 64 values), more by four waves, each every fourth part.
 template <bool BF, bool F8, int D>
@@ -510,13 +547,13 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
   __shared__ float s_ml[4][2];
   __shared__ float s_o[4][D];
   const int ht = (a.g + 15) >> 4, HT = a.c.hkv * ht;
-  const int wg0 = a.meta[2 * (long)blockIdx.x], cnt = a.meta[2 * (long)blockIdx.x + 1];
+  const int team0 = a.meta[2 * (long)blockIdx.x], cnt = a.meta[2 * (long)blockIdx.x + 1];
   if (cnt <= 1) return;
   const int seq = blockIdx.x / HT, hti = blockIdx.x - seq * HT;
   const int kvh = hti / ht, hbase = (hti - kvh * ht) * 16;
   const int heads = min(16, a.g - hbase);
   const int lane = lane_id(), w = threadIdx.x >> 6;
-  const size_t sf = dec_slot_floats(D);
+  const size_t sf = kDecPartRow + (size_t)min(16, a.g) * D;
 
   struct State {
     float m, l, o[E];
@@ -527,7 +564,7 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int i = first + stride * k, ii = i < cnt ? i : first;
-      const float* p = a.part + (2 * (size_t)(wg0 + ii) + (ii == 0)) * sf;
+      const float* p = a.part + (2 * (size_t)(team0 + ii) + (ii == 0)) * sf;
       pm[k] = i < cnt ? p[hh] : kNegInf;
       pl[k] = p[16 + hh];
 #pragma unroll
@@ -608,13 +645,17 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
 template <bool BF, bool F8, int D>
 hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   const int ht = (a.g + 15) / 16, HT = a.c.hkv * ht;
+  const long pairs = (long)a.n * HT;
+  const int ts = dec_team(pairs, D, F8);
   const long cap = (long)a.t.max_pages * a.t.ps;
   const long seen = a.window ? (long)a.window + a.first + 2 * kDecKeys : cap;
-  const long units = ((seen < cap ? seen : cap) + kDecUnit - 1) / kDecUnit + 1;
-  const long bound = (long)a.n * HT * units;
+  const long units = ((seen < cap ? seen : cap) + ts * kDecKeys - 1) / (ts * kDecKeys) + 1;
+  const long bound = (pairs * units * ts + 3) / 4;         // workgroups with anything to do
   const int wgs = dec_wgs(D, F8), grid = (int)(bound < wgs ? bound : wgs);
-  attn_decode_kernel<BF, F8, D><<<grid, 256, 0, s>>>(a);
-  const long pairs = (long)a.n * HT;
+  if (ts == 1)
+    attn_decode_kernel<BF, F8, D, 1><<<grid, 256, 0, s>>>(a);
+  else
+    attn_decode_kernel<BF, F8, D, 4><<<grid, 256, 0, s>>>(a);
   const dim3 jg((unsigned)pairs, pairs >= 256 ? 1 : (a.g < 16 ? a.g : 16));
   decode_join_kernel<BF, F8, D><<<jg, 256, 0, s>>>(a);
   return hipGetLastError();

@@ -54,15 +54,27 @@ struct AttnArgs {
   int* meta;
 };
 
-// Decode: dec_wgs workgroups, as many as are resident at once on 256 CUs, so
-// that an even share of the keys for each is one even pass; partial-result
-// slots, two a workgroup (the sequence it continues, the one it leaves open),
-// of 16 rows of D floats + 16 maxima + 16 sums; and one (first workgroup,
-// count) pair per (sequence, key-value head, 16 query heads).
-constexpr int dec_waves(int D, bool f8) {        // per SIMD; bound by LDS
+// Decode: dec_wgs workgroups, all resident at once on 256 CUs, so that an even
+// share of the keys for each is one even pass. More than two of them a CU read
+// slower: scattered 16 KB pieces at 5.5 TB/s by 512 workgroups and at 4.9 by
+// 1024 (three a CU for head_dim 64, whose pieces are half as long).
+constexpr int dec_waves(int D, bool f8) {        // per SIMD, as LDS allows
   return D == 64 ? 4 : D == 128 ? (f8 ? 4 : 2) : (f8 ? 2 : 1);
 }
-constexpr int dec_wgs(int D, bool f8) { return D == 64 ? 768 : 256 * (dec_waves(D, f8) < 2 ? 1 : 2); }
+constexpr int dec_wgs(int D, bool f8) {
+  return D == 64 ? 768 : dec_waves(D, f8) < 2 ? 256 : 512;
+}
+// waves of a team: one where there are enough (sequence, key-value head, 16
+// query heads) pairs for half of the single waves, else a workgroup. With one
+// wave: 512 x 64 keys x 8 heads 46 -> 35.5 us, 256 x 100 keys 33 -> 30.6, 64
+// query heads a key-value head 123 -> 80; with a quarter as many pairs as
+// waves it lost (64 x 2000 keys of 8 heads 75 -> 80 us).
+constexpr int dec_team(long pairs, int D, bool f8) {
+  return pairs * 2 >= 4L * dec_wgs(D, f8) ? 1 : 4;
+}
+// Workspace: partial-result slots, two a team (the pair it continues, the one
+// it leaves open), of min(16, g) rows of D floats + 16 maxima + 16 sums; and
+// one (first team, count) per pair.
 constexpr int kDecMaxSeqs = 512;        // sequences per launch
 constexpr int kDecKeys = 32;            // keys of one wave's step
 size_t decode_ws_bytes(long n, int hq, int hkv, int D, bool f8);

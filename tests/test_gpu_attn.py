@@ -179,6 +179,38 @@ def test_decode_many_sequences():
     check(lse, want[1], want[3], "lse")
 
 
+# Enough (sequence, key-value head, 16 query heads) pairs that each is one
+# wave's work: lens are n random lengths up to the given one and one long one.
+MANY = {
+    "d64": ("f16", "f16", 64, 12, 4, 16, "pad", 400, 60, 3001, 0, 0),
+    "d64_e4m3": ("bf16", "e4m3", 64, 8, 8, 32, "heads", 200, 50, 2000, 0, 0),
+    "d128": ("bf16", "bf16", 128, 16, 8, 16, "dense", 140, 70, 5000, 0, 0),
+    "d128_e4m3_window": ("f16", "e4m3", 128, 8, 8, 16, "pad", 140, 300, 900, 50, 5),
+    "d128_64_heads_share": ("bf16", "bf16", 128, 128, 2, 16, "dense", 130, 40, 1500, 0, 0),
+    "d256": ("bf16", "bf16", 256, 6, 2, 16, "dense", 260, 40, 1800, 0, 0),
+    "d256_e4m3": ("f16", "e4m3", 256, 8, 4, 16, "heads", 260, 40, 700, 30, 0),
+}
+
+
+@pytest.mark.parametrize("name", list(MANY))
+def test_decode_many_pairs(name):
+    dt, kv, D, hq, hkv, ps, how, n, top, long, window, first = MANY[name]
+    print(f"[case] decode many {name}", flush=True)
+    rng = np.random.default_rng(len(name) * 11 + D)
+    lens = [int(x) for x in rng.integers(1, top, n)]
+    lens[n // 3] = long
+    pool = Pool(rng, kv=kv, hkv=hkv, D=D, ps=ps, lens=lens)
+    rows = [1] * n
+    _hide(pool, range(n), rows, window, first)
+    q = _q(rng, n, hq, D, dt)
+    scale = D ** -0.5
+    out, lse, err = _run("decode", pool, None, rows, q, hq, window, first, scale, dt, how)
+    want = _reference(pool, range(n), rows, q, hq, window, first, scale, dt)
+    assert err == 0
+    check(lse, want[1], want[3], "lse")
+    print("  worst error / bar: %.3f" % check(out, want[0], want[2], "out"), flush=True)
+
+
 def test_decode_missing_page_is_masked_and_flagged():
     rng = np.random.default_rng(5)
     pool = Pool(rng, kv="bf16", hkv=2, D=128, ps=16, lens=[100])
