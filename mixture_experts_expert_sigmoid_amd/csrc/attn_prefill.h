@@ -48,7 +48,7 @@ struct PreTile {
   int tile, rows;              // tile of PreShape::ROWS rows, rows of the sequence
   int p_min, p_max;            // positions of its first and last row
   int lo_min, lo_max;          // first key of the window at those
-  int nb1, b2, nb;             // key tiles: 0..nb1-1, then b2 .. b2 + nb - nb1 - 1
+  int ng1, b2, nb;             // 16-key groups: 0..ng1-1, then b2 and on; tiles of them
 };
 
 __device__ __forceinline__ int pre_cu(const AttnArgs& a, int i) {
@@ -80,17 +80,20 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   t.m = max(0, pre_cu(a, t.seq + 1) - t.q0);
   t.rows = t.m * g;
   if (t.tile * ROWS >= t.rows) return false;
-  t.slot = kv_slot(a.slots, t.seq, a.t.n_slots, a.err);
-  t.L = kv_len(a.t, t.slot);
+  // (uniform, told so: loads behind the error word's atomic are not taken for it)
+  t.slot = __builtin_amdgcn_readfirstlane(kv_slot(a.slots, t.seq, a.t.n_slots, a.err));
+  t.L = __builtin_amdgcn_readfirstlane(kv_len(a.t, t.slot));
   const int r1 = min(t.rows, (t.tile + 1) * ROWS) - 1;
   t.p_min = t.L - t.m + t.tile * ROWS / g;
   t.p_max = t.L - t.m + r1 / g;
   t.lo_min = a.window ? max(0, t.p_min - a.window + 1) : 0;
   t.lo_max = a.window ? max(0, t.p_max - a.window + 1) : 0;
-  t.b2 = t.lo_min / BN;
-  t.nb1 = min(t.b2, (min(a.first, t.lo_min) + BN - 1) / BN);
-  const int end = (max(0, t.p_max + 1) + BN - 1) / BN;
-  t.nb = t.nb1 + max(0, end - t.b2);
+  // the groups of the first keys and those of the window lie end to end, so
+  // that the few first keys do not take a tile of their own
+  t.b2 = t.lo_min / 16;
+  t.ng1 = min(t.b2, (min(a.first, t.lo_min) + 15) / 16);
+  const int end = (max(0, t.p_max + 1) + 15) / 16;
+  t.nb = (t.ng1 + max(0, end - t.b2) + BN / 16 - 1) / (BN / 16);
   return true;
 }
 
@@ -147,16 +150,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const float thr = fminf(8.0f / sc, 1e30f);
 
   // this lane's row
-  const int r = t.tile * ROWS + w * 32 + l31;
-  const bool have = r < t.rows;
-  const int tok = have ? r / a.g : 0;
-  const int head = kvh * a.g + (have ? r - tok * a.g : 0);
-  const int pos = have ? t.L - t.m + tok : -1;
-  const int lo = a.window ? pos - a.window + 1 : 0;
-  const long qrow = t.q0 + tok;
+  struct Row {
+    bool have;
+    int head;
+    long q;                                      // of q and out
+  };
+  const int row_of = t.tile * ROWS + w * 32;
+  int tok = row_of + l31 < t.rows ? (row_of + l31) / a.g : -1;
+  auto row_at = [&] {
+    asm volatile("" : "+v"(tok));                // not kept in registers beside it
+    const int k = max(tok, 0);
+    return Row{tok >= 0, kvh * a.g + (tok >= 0 ? row_of + l31 - k * a.g : 0), (long)t.q0 + k};
+  };
+  auto pos_of = [&] {
+    asm volatile("" : "+v"(tok));
+    return tok >= 0 ? t.L - t.m + tok : -1;
+  };
   u32x4 q[NC];
   {
-    const char* p = a.q + qrow * a.q_row + head * a.q_head + 16 * half;
+    const Row y0 = row_at();
+    const char* p = a.q + y0.q * a.q_row + y0.head * a.q_head + 16 * half;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const u32x4 y = *(const u32x4*)(p + 32 * c);
@@ -177,12 +190,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const char* vb = a.c.v + kvh * a.c.sh;
   const int grp = w * WR / 16;                   // 16-key group that this wave brings from
 
-  auto key_of = [&](int x) { return BN * (x < t.nb1 ? x : t.b2 + x - t.nb1); };
-  // tiles of which every row sees every key (some of the first keys' tiles
-  // may be such too, and are treated as if not)
-  const int whole0 = t.nb1 - t.b2 + (t.lo_max + BN - 1) / BN;
-  const int whole1 = t.nb1 - t.b2 + (t.p_min + 1) / BN;
-  auto whole = [&](int x) { return x >= t.nb1 && x >= whole0 && x < whole1; };
+  constexpr int GT = BN / 16;                    // groups of a tile
+  auto group_key = [&](int i) { return 16 * (i < t.ng1 ? i : t.b2 + i - t.ng1); };
+  // tiles of which every row sees every key (the first keys' may be such too,
+  // and are treated as if not)
+  const int whole0 =
+      (t.ng1 + max(0, (t.lo_max + 15) / 16 - t.b2) + GT - 1) / GT;
+  const int whole1 = (t.ng1 - t.b2 + (t.p_min + 1) / 16) / GT;
+  auto whole = [&](int x) { return x >= whole0 && x < whole1; };
 
   // Byte offset in the cache of the wave's group of the next 64 tiles, a tile
   // a lane; kMissing: no page, kUnseen: nothing of it is visible. One lookup a
@@ -194,7 +209,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   };
   int at0 = x0;
   auto lookup = [&](int x) {
-    const int key = key_of(x) + 16 * grp;
+    const int key = group_key(GT * x + grp);
     if (x >= x1 || key > t.p_max || !(key + 16 > t.lo_min || key < a.first)) return kUnseen;
     const int i = kv_entry(a.t, key), e = row[i];
     return e >= 0 && e < a.t.n_pages ? e * a.c.sp + (key - i * a.t.ps) * a.c.st : kMissing;
@@ -229,8 +244,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     return x;
   };
   // a unit of V of a tile that is not whole, as it is to be staged
-  auto clean = [&](u32x4 v, int key, int kr, bool ok) {
-    const int j = key + kr;
+  auto clean = [&](u32x4 v, int j, bool ok) {      // of key j
     if (!ok || j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
     if ((carry(v[0]) | carry(v[1]) | carry(v[2]) | carry(v[3])) & 0x80008000u) {
       s_bad = 1;
@@ -245,19 +259,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // applied to the units read. e4m3 ones go through registers, expanded on
   // arrival. A lane's offset stays below 2^31 (16 stride_tok < 2^30).
   constexpr int RPL = 64 / GPR;
-  const int l_row = lane / GPR, w_row = (w * WR) & 15;
-  uint32_t k_from[NL], v_from[NL];
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int rr = w_row + i * RPL + l_row;
-    k_from[i] = (uint32_t)rr * (uint32_t)a.c.st + 16 * (lane % GPR ^ (F8 ? 0 : k_swz(rr)));
-    v_from[i] = (uint32_t)rr * (uint32_t)a.c.st + 16 * (lane % GPR ^ (F8 ? 0 : v_swz(rr)));
-  }
+  const int l_row = ((w * WR) & 15) + lane / GPR;
+  const uint32_t l_at = (uint32_t)l_row * (uint32_t)a.c.st;
+  // the lane's unit in load 0; the swizzles are exclusive ors of row bits
+  const uint32_t k_unit = 16 * (lane % GPR ^ (F8 ? 0 : k_swz(l_row)));
+  const uint32_t v_unit = 16 * (lane % GPR ^ (F8 ? 0 : v_swz(l_row)));
   u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];
-  auto issue = [&](const char* p, const uint32_t (&from)[NL], char* to, u32x4* raw) {
+  auto issue = [&](const char* p, uint32_t unit, auto swz, char* to, u32x4* raw) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      uint32_t f = from[i];
+    for (int i = 0; i < NL; ++i, p += RPL * a.c.st) {
+      uint32_t f = l_at + (unit ^ (F8 ? 0 : 16 * swz(i * RPL)));
       asm volatile("" : "+v"(f));                // added by the load, not ahead of it
       if constexpr (F8)
         raw[i] = *(const u32x4*)(p + f);
@@ -274,9 +285,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
       s_gone = x;
       miss[w] = x;
     }
-    issue(kb + gr.off, k_from, to, rk);
+    issue(kb + gr.off, k_unit, k_swz, to, rk);
   };
-  auto issue_v = [&](const Group& gr, char* to) { issue(vb + gr.off, v_from, to, rv); };
+  auto issue_v = [&](const Group& gr, char* to) { issue(vb + gr.off, v_unit, v_swz, to, rv); };
   auto expand = [&](const u32x4& raw, u32x4 (&y)[2]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -302,7 +313,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   };
   // takes masked values out of V
   auto finish_v = [&](int x, const Group& gr, char* to) {
-    const int key = key_of(x);
+    const int key = group_key(GT * x + grp) - 16 * grp;
     const bool as_is = whole(x) && gr.state >= 0;
     if constexpr (F8) {
 #pragma unroll
@@ -312,7 +323,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
         expand(rv[i], y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!as_is) y[h] = clean(y[h], key, kr, gr.state >= 0);
+          if (!as_is) y[h] = clean(y[h], key + kr, gr.state >= 0);
           *(u32x4*)(to + kr * (2 * D) + 16 * ((2 * u + h) ^ v_swz(kr))) = y[h];
         }
       }
@@ -321,7 +332,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
       for (int i = 0; i < NL; ++i) {
         const int up = i * 64 + lane, kr = w * WR + up / GPR;
         u32x4* p = (u32x4*)(to + (w * WR * UPR + up) * 16);
-        *p = clean(*p, key, kr, gr.state >= 0);
+        *p = clean(*p, key + kr, gr.state >= 0);
       }
     }
   };
@@ -374,8 +385,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
         const int k = min(max(c, 0), 64), cnt = 4 * (k >> 3) + min(k & 7, 4);
         return (uint32_t)((1ull << cnt) - 1);
       };
-      const int at = key_of(x) + 4 * half;
+      const int pos = pos_of(), lo = a.window ? pos - a.window + 1 : 0;
+      const int at = 16 * (t.b2 - t.ng1 + GT * x) + 4 * half;
       uint32_t see = below(pos + 1 - at) & (~below(lo - at) | below(a.first - at));
+      if (GT * x < t.ng1) {                      // groups of the first keys
+        const uint32_t own = below(16 * (t.ng1 - GT * x));
+        see = (see & ~own) | (own & below(min(pos + 1, a.first) - 16 * GT * x - 4 * half));
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) see &= (gone >> i) & 1 ? ~(0xFFu << (8 * i)) : ~0u;
 #pragma unroll
@@ -424,6 +440,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     auto element = [&](int e) {
       const float pe = exp2_fast(__builtin_fmaf(s[e >> 4][e & 15], sc, neg));
       l += pe;
+      asm volatile("" : "+v"(l));                // added here: sunk below, all P would stay
       if (e & 1) pb[e >> 3][(e & 7) >> 1] = pack16<BF>(p0, pe);
       p0 = pe;
     };
@@ -517,10 +534,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // for the rows that see their key
   __syncthreads();
   if (s_bad) {
+    const int pos = pos_of(), lo = a.window ? pos - a.window + 1 : 0;
     for (int xx = x0; xx < x1; ++xx) {
       if (whole(xx)) continue;
-      const int key = key_of(xx);
-      for (int j = key; j < key + BN; ++j) {
+      for (int i = 0; i < BN; ++i) {
+        const int j = group_key(GT * xx + i / 16) + i % 16;
         if (j > t.p_max || !(j >= t.lo_min || j < a.first)) continue;
         const int e = kv_entry(a.t, j), p = row[e];
         if (p < 0 || p >= a.t.n_pages) continue;
@@ -565,11 +583,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   }
 
   l = xor32_reduce(l, OpSum{});
-  if (!have) return;
+  const Row me = row_at();
+  if (!me.have) return;
   if (parts == 1) {
     float inv = l == 0.0f ? 0.0f : 1.0f / l;     // no visible key: 0
     if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
-    char* dst = a.out + qrow * a.o_row + head * a.o_head;
+    char* dst = a.out + me.q * a.o_row + me.head * a.o_head;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -578,9 +597,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
                          pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
         *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
       }
-    if (a.lse && half == 0) a.lse[qrow * a.hq + head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && half == 0) a.lse[me.q * a.hq + me.head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
   } else {
-    const long rows = a.T * a.hq, ri = qrow * a.hq + head;
+    const long rows = a.T * a.hq, ri = me.q * a.hq + me.head;
     float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
