@@ -584,21 +584,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
 
   l = xor32_reduce(l, OpSum{});
   const Row me = row_at();
-  if (!me.have) return;
   if (parts == 1) {
+    // turned round through the wave's share of LDS, so that stores take whole
+    // rows; the 16-byte units of a row are swizzled by its number
     float inv = l == 0.0f ? 0.0f : 1.0f / l;     // no visible key: 0
     if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
-    char* dst = a.out + me.q * a.o_row + me.head * a.o_head;
+    constexpr int RB = 2 * D, WB = 32 * RB;
+    static_assert(TB >= WB && TB <= 2 * WB, "a buffer holds one or two waves' rows");
+    char* const mine =
+        TB == WB ? (w < 2 ? (w ? s_k1 : s_k0) : (w == 2 ? s_v0 : s_v1))
+                 : (w < 2 ? s_k0 : s_k1) + (w & 1) * WB;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const u32x2 y = {pack16<BF>(o[d][i] * inv, o[d][i + 1] * inv),
                          pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        *(u32x2*)(dst + 2 * (32 * d + 2 * i + 4 * half)) = y;
+        *(u32x2*)(mine + l31 * RB + 16 * ((4 * d + (i >> 2)) ^ (l31 & (UPR - 1))) + 8 * half) = y;
       }
-    if (a.lse && half == 0) a.lse[me.q * a.hq + me.head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
-  } else {
+#pragma unroll
+    for (int i = 0; i < UPR / 2; ++i) {
+      const int rr = i * (64 / UPR) + lane / UPR, u = lane % UPR;
+      const int tk = __shfl(tok, rr);
+      const u32x4 y = *(const u32x4*)(mine + rr * RB + 16 * (u ^ (rr & (UPR - 1))));
+      if (tk >= 0)
+        *(u32x4*)(a.out + ((long)t.q0 + tk) * a.o_row +
+                  (kvh * a.g + row_of + rr - tk * a.g) * a.o_head + 16 * u) = y;
+    }
+    if (a.lse && half == 0 && me.have)
+      a.lse[me.q * a.hq + me.head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
+  } else if (me.have) {
     const long rows = a.T * a.hq, ri = me.q * a.hq + me.head;
     float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
 #pragma unroll
