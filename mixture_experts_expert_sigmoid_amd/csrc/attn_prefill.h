@@ -423,8 +423,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // after another, each with the read of the operand that is due kAhead of
   // them later and a share of the exponentials behind it: the order is kept
   // as written, since the reads' latency (some 130 cycles) and the vector
-  // work both have to go under matrix instructions of 32 cycles.
-  constexpr int kAhead = 4;
+  // work both have to go under matrix instructions of 32 cycles. kAhead: as
+  // far as the registers reach (6000 tokens, TFLOP/s at 2 / 3 / 4 / 5:
+  // head_dim 64 e4m3 743 709 650; 256 711 734 750 751; 128 e4m3, two long
+  // chunks, 3 against 4: 906 872).
+  constexpr int kAhead = D == 64 ? (F8 ? 2 : 3) : (F8 ? 3 : 5);
   auto products = [&](auto next, f32x16 (&s)[NA], f32x16 (&sn)[NA], const char* kn,
                       const char* vx) {
     constexpr bool NEXT = decltype(next)::value;
