@@ -67,7 +67,13 @@ size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
 
 hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
   AttnArgs a = all;
-  a.n_split = prefill_splits(a.n, a.T, a.hq, a.hq / a.g);
+  // no more parts than the most keys that a tile can see give (four tiles of
+  // keys each), so that calls over short tables need no join
+  const long cap = (long)a.t.max_pages * a.t.ps;
+  const long span = a.window ? (long)a.window + a.first + kPreRows / a.g + 64 : cap;
+  const long most = (span < cap ? span : cap) / (4 * (a.c.D == 256 ? 32 : 64));
+  const int split = prefill_splits(a.n, a.T, a.hq, a.hq / a.g);
+  a.n_split = most < 1 ? 1 : most < split ? (int)most : split;
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);

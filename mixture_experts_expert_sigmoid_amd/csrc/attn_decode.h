@@ -23,7 +23,8 @@
 // join kernel adds in order. A team is a workgroup (units of four blocks, a
 // wave each, joined through LDS), or a single wave where there are many pairs:
 // short contexts then run side by side instead of four waves waiting for the
-// same few loads.
+// same few loads. Few pairs that are short by their table or window are not
+// split: a workgroup each, and no join kernel (a third of such a call).
 //
 // Bound: HBM reads of K and V; short contexts by latency (length -> table ->
 // keys -> join).
@@ -154,12 +155,16 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
   const long teams = (long)gridDim.x * (4 / TS), team = TS == 4 ? blockIdx.x : 4 * blockIdx.x + w;
   const long W = U < teams ? U : teams;
   if (team >= W) return;
-  long u = team * U / W;
-  const long u_end = (team + 1) * U / W;
-
-  // the sequence of unit u: the last i with pref[i] * HT <= u
+  long u = team * U / W, u_end = (team + 1) * U / W;
   int seq = 0;
-  {
+  if (TS == 4 && a.whole) {
+    // a pair for each workgroup
+    seq = blockIdx.x / HT;
+    const int pre = s_pref[seq], ns = s_pref[seq + 1] - pre;
+    u = (long)pre * HT + (blockIdx.x - seq * HT) * ns;
+    u_end = u + ns;
+  } else {
+    // the sequence of unit u: the last i with pref[i] * HT <= u
     int hi = n - 1;
     while (seq < hi) {
       const int mid = (seq + hi + 1) >> 1;
@@ -643,7 +648,8 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
 }
 
 template <bool BF, bool F8, int D>
-hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
+hipError_t run_decode(const AttnArgs& all, hipStream_t s) {
+  AttnArgs a = all;
   const int ht = (a.g + 15) / 16, HT = a.c.hkv * ht;
   const long pairs = (long)a.n * HT;
   const int ts = dec_team(pairs, D, F8);
@@ -652,10 +658,14 @@ hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   const long units = ((seen < cap ? seen : cap) + ts * kDecKeys - 1) / (ts * kDecKeys) + 1;
   const long bound = (pairs * units * ts + 3) / 4;         // workgroups with anything to do
   const int wgs = dec_wgs(D, F8), grid = (int)(bound < wgs ? bound : wgs);
-  if (ts == 1)
+  a.whole = ts == 4 && pairs <= wgs && dec_whole(pairs, units - 1, D, F8);
+  if (a.whole)
+    attn_decode_kernel<BF, F8, D, 4><<<(unsigned)pairs, 256, 0, s>>>(a);
+  else if (ts == 1)
     attn_decode_kernel<BF, F8, D, 1><<<grid, 256, 0, s>>>(a);
   else
     attn_decode_kernel<BF, F8, D, 4><<<grid, 256, 0, s>>>(a);
+  if (a.whole) return hipGetLastError();
   const dim3 jg((unsigned)pairs, pairs >= 256 ? 1 : (a.g < 16 ? a.g : 16));
   decode_join_kernel<BF, F8, D><<<jg, 256, 0, s>>>(a);
   return hipGetLastError();

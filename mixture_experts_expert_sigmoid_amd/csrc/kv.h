@@ -49,6 +49,8 @@ struct AttnArgs {
   const int* cu;
   long T;
   int n_split;
+  // decode: every pair is one team's
+  int whole;
   // partial results of split rows
   float* part;
   int* meta;
@@ -71,6 +73,16 @@ constexpr int dec_wgs(int D, bool f8) {
 // waves it lost (64 x 2000 keys of 8 heads 75 -> 80 us).
 constexpr int dec_team(long pairs, int D, bool f8) {
   return pairs * 2 >= 4L * dec_wgs(D, f8) ? 1 : 4;
+}
+// Pairs not split, a workgroup each and no join, if the table or the window
+// leaves each of them few units (keys in 128s). Split / not, us: one sequence
+// of 500 keys of 8 heads 10.6 / 8.8, of 1000 10.5 / 12.1, e4m3 10.6 / 13.0; 4 x
+// 400 keys of head_dim 256 13.5 / 15.3, of 250 12.6 / 11.1. With half as many
+// pairs as workgroups and more, 32 x 50..1000 keys 23.5 / 17.4, 56 x 50..1000
+// 35 / 31.7.
+constexpr bool dec_whole(long pairs, long units, int D, bool f8) {
+  const int many = pairs * 2 >= dec_wgs(D, f8) ? 2 : 1;
+  return units <= 4 * many && units * (f8 ? D : 2 * D) <= 1024 * many;
 }
 // Workspace: partial-result slots, two a team (the pair it continues, the one
 // it leaves open), of min(16, g) rows of D floats + 16 maxima + 16 sums; and
