@@ -298,6 +298,29 @@ def test_prefill(name):
     print("  worst error / bar: %.3f" % check(out, want[0], want[2], "out"), flush=True)
 
 
+# The same calls over tables with room for long contexts: what the table can
+# hold decides whether keys are split and joined.
+@pytest.mark.parametrize("kind,name", [("decode", n) for n in DECODE] +
+                         [("prefill", n) for n in PREFILL])
+def test_wide_tables(kind, name):
+    print(f"[case] wide {kind} {name}", flush=True)
+    if kind == "decode":
+        dt, kv, D, hq, hkv, ps, layout, how, lens, window, first = DECODE[name]
+        rows = [1] * len(lens)
+    else:
+        dt, kv, D, hq, hkv, ps, layout, how, lens, rows, window, first = PREFILL[name]
+    rng = np.random.default_rng(len(name) * 5 + D)
+    pool = Pool(rng, kv=kv, hkv=hkv, D=D, ps=ps, lens=lens, layout=layout,
+                max_pages=1 + 32768 // ps)
+    _hide(pool, range(len(lens)), rows, window, first)
+    q = _q(rng, sum(rows), hq, D, dt)
+    out, lse, err = _run(kind, pool, None, rows, q, hq, window, first, D ** -0.5, dt, how)
+    want = _reference(pool, range(len(lens)), rows, q, hq, window, first, D ** -0.5, dt)
+    assert err == 0
+    check(lse, want[1], want[3], "lse")
+    print("  worst error / bar: %.3f" % check(out, want[0], want[2], "out"), flush=True)
+
+
 @pytest.mark.parametrize("dt,kv,D", [("bf16", "bf16", 128), ("f16", "f16", 64),
                                      ("bf16", "e4m3", 128), ("bf16", "bf16", 256)])
 @pytest.mark.parametrize("window", [0, 24])
