@@ -382,6 +382,9 @@ _KV_FMT = {torch.bfloat16: MOE_KV_BF16, torch.float16: MOE_KV_F16,
            torch.float8_e4m3fn: MOE_KV_E4M3}
 
 
+_INT32 = torch.int32
+
+
 def _kv_fmt(t: torch.Tensor, where: str) -> int:
     fmt = _KV_FMT.get(t.dtype)
     if fmt is None:
@@ -393,14 +396,14 @@ def _i32(t: Optional[torch.Tensor], n: int, where: str):
     """Pointer of a contiguous int32 list of at least n entries (or None)."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.numel() < n or not t.is_contiguous():
         raise MoeError(-2, where, f"wants {n} contiguous int32, got {t.dtype} "
                                   f"{tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _bytes(ws: Optional[torch.Tensor]) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    return 0 if ws is None else ws.nbytes
 
 
 def kv_cache(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
@@ -444,24 +447,26 @@ def _rows(t: torch.Tensor, where: str, shape, D: int):
     """Strides (row, head) of a [rows][heads][head_dim] tensor. A dimension of
     one entry has no stride of its own."""
     st = t.stride()
-    if t.shape != shape or len(st) != 3 or shape[2] != D or st[2] != 1:
+    if len(st) != 3 or shape[2] != D or st[2] != 1 or t.shape != shape:
         raise MoeError(-2, where, f"wants {tuple(shape)} of [rows][heads][{D}] with contiguous "
                                   f"rows, got {tuple(t.shape)} strides {st}")
-    rows, heads, _ = shape
-    return (st[0] if rows > 1 else heads * D), (st[1] if heads > 1 else D)
+    if shape[0] > 1 and shape[1] > 1:
+        return st
+    return (st[0] if shape[0] > 1 else shape[1] * D), (st[1] if shape[1] > 1 else D)
 
 
 def _attn(where, cache: MoeKvCache, q, out, scale, window, n_first, lse) -> MoeAttn:
-    shape, D = q.shape, cache.head_dim
+    shape, D, fmt = q.shape, cache.head_dim, _KV_FMT.get(q.dtype)
     if out.dtype is not q.dtype:
         raise MoeError(-2, where, "out and q differ in type")
-    qr, qh = _rows(q, where, shape, D)
-    orow, ohead = _rows(out, where, shape, D)
+    if fmt is None:
+        raise MoeError(-3, where, f"dtype {q.dtype}")
+    qs, os_ = _rows(q, where, shape, D), _rows(out, where, shape, D)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
                             or not lse.is_contiguous()):
         raise MoeError(-2, where, "lse is fp32 [rows][heads], contiguous")
-    return MoeAttn(_kv_fmt(q, where), shape[1], q.data_ptr(), qr, qh, out.data_ptr(), orow,
-                   ohead, None if lse is None else lse.data_ptr(), scale, window, n_first)
+    return MoeAttn(fmt, shape[1], q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
+                   None if lse is None else lse.data_ptr(), scale, window, n_first)
 
 
 def moe_attn_decode_workspace_size(cache: MoeKvCache, n: int, n_heads: int) -> int:

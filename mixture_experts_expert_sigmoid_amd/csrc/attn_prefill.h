@@ -97,9 +97,13 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   return true;
 }
 
-// parts that a tile's keys are split into: at least four key tiles each
+// Parts that a tile's keys are split into: at least four key tiles each, and no
+// more than pay. With nb tiles of a time t, nb t / p + p c is least at p =
+// sqrt(nb t / c); the cost c of a part is that of its fp32 rows written and
+// read back, so t / c is split_gain, a constant over the rows of the call.
 __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
-  return max(1, min(a.n_split, nb >> 2));
+  if (a.n_split == 1) return 1;
+  return max(1, min(min(a.n_split, nb >> 2), (int)sqrtf((float)nb * a.split_gain)));
 }
 
 template <bool BF, bool F8, int D>
@@ -427,6 +431,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // far as the registers reach (6000 tokens, TFLOP/s at 2 / 3 / 4 / 5:
   // head_dim 64 e4m3 743 709 650; 256 711 734 750 751; 128 e4m3, two long
   // chunks, 3 against 4: 906 872).
+  // kLag: an exponential's result is taken up so many of them later, so that
+  // the wave does not stand still for it (head_dim 128 0 / 2: 924 / 942
+  // TFLOP/s; 64, with three waves a SIMD: 843 / 831; chunks over e4m3: 866 / 853).
+  constexpr int kLag = D == 64 || F8 ? 0 : 2;
   constexpr int kAhead = D == 64 ? (F8 ? 2 : 3) : (F8 ? 3 : 5);
   auto products = [&](auto next, f32x16 (&s)[NA], f32x16 (&sn)[NA], const char* kn,
                       const char* vx) {
@@ -435,17 +443,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     asm volatile("" : "+v"(k_at), "+v"(v_at));   // not 2 x NC addresses kept in registers
     const float neg = m == kNegInf ? 0.0f : -m * sc;
     u32x4 op[MQ + MV], pb[2 * NA];
-    float p0 = 0.0f;
+    float pend[kLag + 1], p0 = 0.0f;
     auto read = [&](int i) {
       op[i] = i < MQ ? read_k(kn, i / NA, i % NA) : read_v(vx, (i - MQ) / ND, (i - MQ) % ND);
     };
     // probabilities come before the step that needs them: 8 for each ND of MV
-    auto element = [&](int e) {
-      const float pe = exp2_fast(__builtin_fmaf(s[e >> 4][e & 15], sc, neg));
+    auto add = [&](int e) {
+      const float pe = pend[e % (kLag + 1)];
       l += pe;
       asm volatile("" : "+v"(l));                // added here: sunk below, all P would stay
       if (e & 1) pb[e >> 3][(e & 7) >> 1] = pack16<BF>(p0, pe);
       p0 = pe;
+    };
+    constexpr int LAG = NEXT ? kLag : 0;
+    auto element = [&](int e) {
+      pend[e % (kLag + 1)] = exp2_fast(__builtin_fmaf(s[e >> 4][e & 15], sc, neg));
+      if (e >= LAG) add(e - LAG);
+      if (e == NE - 1)
+#pragma unroll
+        for (int i = NE - LAG; i < NE; ++i) add(i);
     };
     if (!NEXT) {
 #pragma unroll
@@ -633,49 +649,70 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   }
 }
 
-// Joins the parts of split tiles: one wave per (token, query head).
+// Joins the parts of split tiles: a workgroup for each 16 rows of a tile, 16
+// lanes a row, the parts in order.
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
-  constexpr int ROWS = PreShape<D>::ROWS;
-  constexpr int E = D / 64;
-  const long rows = a.T * a.hq;
-  const long ri = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (ri >= rows) return;
-  const int tok = (int)(ri / a.hq), head = (int)(ri - (long)tok * a.hq);
+  constexpr int ROWS = PreShape<D>::ROWS, V = D / 16;
   PreTile t;
-  t.seq = pre_last(a, [&](int, int cu) { return cu <= tok; });
-  t.tile = ((tok - pre_cu(a, t.seq)) * a.g + head % a.g) / ROWS;
+  const int kvh = blockIdx.x % a.c.hkv, tt = (int)(blockIdx.x / a.c.hkv);
+  t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
+  t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
   if (!pre_span<D>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if (parts == 1) return;
-  const int lane = lane_id();
+  const int r = t.tile * ROWS + (int)blockIdx.y * 16 + (threadIdx.x >> 4);
+  if (r >= t.rows) return;
+  const int d0 = (int)(threadIdx.x & 15) * V, tok = r / a.g, head = kvh * a.g + r - tok * a.g;
+  const long rows = a.T * a.hq, ri = ((long)t.q0 + tok) * a.hq + head;
   const float* ml = a.part + (long)a.n_split * rows * D + ri * 2;
-  const float pm = lane < parts ? ml[(long)lane * rows * 2] : kNegInf;
-  const float pl = lane < parts ? ml[(long)lane * rows * 2 + 1] : 0.0f;
-  const float m = wave_max(pm);
+  // maxima and sums: part 16 i + lane of the 16; factor i for those parts
+  const int l16 = threadIdx.x & 15;
+  constexpr int MP = kPreMaxParts / 16;
+  float pm[MP], pl[MP], m = kNegInf, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < MP; ++i) {
+    const int at = 16 * i + l16;
+    pm[i] = at < parts ? ml[(long)at * rows * 2] : kNegInf;
+    pl[i] = at < parts ? ml[(long)at * rows * 2 + 1] : 0.0f;
+    m = fmaxf(m, pm[i]);
+  }
+  for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
   const float mu = m == kNegInf ? 0.0f : m;
-  const float f = exp2_fast(pm - mu);
-  const float l = wave_sum(f * pl);
-  float acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int i = 0; i < parts; ++i) {
-    const float fi = __shfl(f, i);
-    const float* p = a.part + ((long)i * rows + ri) * D + lane * E;
+  for (int i = 0; i < MP; ++i) {
+    pm[i] = exp2_fast(pm[i] - mu);
+    l += pm[i] * pl[i];
+  }
+  for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
+  float acc[V];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += fi * p[e];
+  for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < MP; ++i) {
+    const int end = min(16, parts - 16 * i);
+#pragma unroll 4
+    for (int j = 0; j < end; ++j) {
+      const float f = __shfl(pm[i], j, 16);
+      const float* p = a.part + ((long)(16 * i + j) * rows + ri) * D + d0;
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const f32x4 y = *(const f32x4*)(p + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[e + k] += f * y[k];
+      }
+    }
   }
   float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (F8 && l != 0.0f) inv *= a.c.vs[head / a.g];
-  char* dst = a.out + (long)tok * a.o_row + head * a.o_head;
-  if constexpr (E == 1) {
-    *(uint16_t*)(dst + 2 * lane) = (uint16_t)pack16<BF>(acc[0] * inv, 0.0f);
-  } else {
+  if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
+  char* dst = a.out + ((long)t.q0 + tok) * a.o_row + head * a.o_head + 2 * d0;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *(uint32_t*)(dst + 2 * (lane * E + e)) = pack16<BF>(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < V; e += 4) {
+    const u32x2 y = {pack16<BF>(acc[e] * inv, acc[e + 1] * inv),
+                     pack16<BF>(acc[e + 2] * inv, acc[e + 3] * inv)};
+    *(u32x2*)(dst + 2 * e) = y;
   }
-  if (a.lse && lane == 0) a.lse[ri] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+  if (a.lse && d0 == 0) a.lse[ri] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <bool BF, bool F8, int D>
@@ -684,7 +721,8 @@ hipError_t run_prefill(const AttnArgs& a, hipStream_t s) {
   attn_prefill_kernel<BF, F8, D>
       <<<dim3((unsigned)(tiles * a.c.hkv), a.n_split), 256, 0, s>>>(a);
   if (a.n_split > 1)
-    prefill_join_kernel<BF, F8, D><<<(unsigned)((a.T * a.hq + 3) / 4), 256, 0, s>>>(a);
+    prefill_join_kernel<BF, F8, D>
+        <<<dim3((unsigned)(tiles * a.c.hkv), PreShape<D>::ROWS / 16), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -49,6 +49,7 @@ struct AttnArgs {
   const int* cu;
   long T;
   int n_split;
+  float split_gain;      // see pre_parts
   // decode: every pair is one team's
   int whole;
   // partial results of split rows
@@ -99,6 +100,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, int fmt, hipStream_t s);
 constexpr int kPreRows = 128;
 // tiles that n sequences of T tokens can have, per key-value head
 inline long prefill_tiles(long n, long T, int g) { return T * g / kPreRows + n; }
+constexpr int kPreMaxParts = 64;
 int prefill_splits(long n, long T, int hq, int hkv);
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
