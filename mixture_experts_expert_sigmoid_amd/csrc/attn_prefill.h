@@ -228,9 +228,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     const int hi32 = __builtin_amdgcn_readlane((int)(offs >> 32), x - at0);
     return Group{(long)(((uint64_t)(uint32_t)max(hi32, 0) << 32) | lo32), hi32};
   };
-  // swizzle of 16-byte units by row (of the tile)
+  // Swizzle of 16-byte units by row (of the tile). Half a wave reads one unit of
+  // 32 rows of K in turn, and 64 bytes of four rows of V, which have to lie in
+  // different banks.
   auto k_swz = [](int kr) { return kr & (UPR < 16 ? UPR - 1 : 15); };
-  auto v_swz = [](int kr) { return UPR == 8 ? ((kr >> 1) & 3) << 1 : (kr & 7) << 1; };
+  auto v_swz = [](int kr) { return UPR == 8 ? ((kr >> 1) & 1) << 2 : (kr & 3) << 2; };
   // This lane's places in a tile. Rows are a multiple of 128 bytes and the
   // swizzle is the same for rows 16 (K: 32) apart, so units 2 c + half of K
   // are at k_at ^ 32 c, values 32 d.. of V at v_at ^ 64 d, and the row blocks
