@@ -485,8 +485,8 @@ typedef struct {
  * fixed size can be captured once and run partly filled. The visible keys of
  * all sequences and key-value heads are split evenly over the GPU, whatever
  * the lengths, and the parts of one sequence joined in a fixed order (a
- * second launch, where any is split): results do not depend on timing. No length is read on the
- * host. Limits: 0 <= n < 2^20. Workspace:
+ * second launch, left out where nothing can be split): results do not depend
+ * on timing. No length is read on the host. Limits: 0 <= n < 2^20. Workspace:
  * moe_attn_decode_workspace_size(cache, n, n_heads) bytes (0 for invalid
  * arguments). Errors: NULL, SHAPE, FORMAT (fmt), PARAM (alignment, scale,
  * window, scales of a cache that takes none), WORKSPACE, HIP. */
