@@ -436,39 +436,9 @@ __global__ __launch_bounds__(kThreads) void count_used_kernel(const int* refs, i
 __global__ __launch_bounds__(kThreads) void rank_kernel(const int* refs, int P, int segs,
                                                         CompactPlan pl, int* n_used) {
   __shared__ long s_w[kWaves];
-  __shared__ int s_cnt[kWaves];
+  __shared__ int s_cnt[kWaves], s_low[kWaves];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  long all = 0, before = 0;
-  if (segs == 1) {                       // counted here: no launch before this one
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const long p = k * kThreads + threadIdx.x;
-      all += p < P ? refs[p] > 0 : 0;
-    }
-  } else {
-    for (int i = threadIdx.x; i < segs; i += kThreads) {
-      const int c = pl.seg_used[i];
-      all += c;
-      if (i < (int)blockIdx.x) before += c;
-    }
-  }
-  long U, base;
-  block_scan(all, s_w, &U);
-  block_scan(before, s_w, &base);
-  // used(U): the segments before U's, and the used pages of its own below U
-  const int useg = (int)(U / kSeg);
-  long part = 0;
-  if (segs > 1)
-    for (int i = threadIdx.x; i < segs && i < useg; i += kThreads) part += pl.seg_used[i];
-  for (long p = (long)useg * kSeg + threadIdx.x; p < U; p += kThreads) part += refs[p] > 0;
-  long used_u;
-  block_scan(part, s_w, &used_u);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    pl.hdr[0] = (int)U;
-    pl.hdr[1] = (int)(U - used_u);
-    if (n_used) *n_used = (int)U;
-  }
-  const long first = (long)blockIdx.x * kSeg + (long)w * (64 * kPer) + lane;
+  const long wave0 = (long)blockIdx.x * kSeg + (long)w * (64 * kPer), first = wave0 + lane;
   uint64_t m[kPer];
   int mine = 0;
 #pragma unroll
@@ -478,7 +448,40 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const int* refs, int P, 
     mine += __popcll(m[k]);
   }
   if (lane == 0) s_cnt[w] = mine;
-  __syncthreads();
+  long U = 0, base = 0, used_u = 0;
+  if (segs == 1) {                       // all from the ballots, no launch before this one
+    __syncthreads();
+    for (int i = 0; i < kWaves; ++i) U += s_cnt[i];
+    int low = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const long below = U - (wave0 + 64 * k);
+      low += __popcll(below >= 64 ? m[k] : below > 0 ? m[k] & ((1ull << below) - 1) : 0);
+    }
+    if (lane == 0) s_low[w] = low;
+    __syncthreads();
+    for (int i = 0; i < kWaves; ++i) used_u += s_low[i];
+  } else {
+    long all = 0, before = 0;
+    for (int i = threadIdx.x; i < segs; i += kThreads) {
+      const int c = pl.seg_used[i];
+      all += c;
+      if (i < (int)blockIdx.x) before += c;
+    }
+    block_scan(all, s_w, &U);
+    block_scan(before, s_w, &base);
+    // used(U): the segments before U's, and the used pages of its own below U
+    const int useg = (int)(U / kSeg);
+    long part = 0;
+    for (int i = threadIdx.x; i < segs && i < useg; i += kThreads) part += pl.seg_used[i];
+    for (long p = (long)useg * kSeg + threadIdx.x; p < U; p += kThreads) part += refs[p] > 0;
+    block_scan(part, s_w, &used_u);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    pl.hdr[0] = (int)U;
+    pl.hdr[1] = (int)(U - used_u);
+    if (n_used) *n_used = (int)U;
+  }
   long u = base;
   for (int i = 0; i < w; ++i) u += s_cnt[i];
 #pragma unroll
