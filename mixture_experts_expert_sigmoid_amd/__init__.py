@@ -571,12 +571,31 @@ def moe_cache_copy_pages(caches, src, dst, err_word, stream=None):
                                       _stream(stream)), where)
 
 
+class _Workspace:
+    """A workspace that grows. Every buffer handed out is kept: a graph captured
+    with it goes on writing there, and so may work on another stream. Each is at
+    least twice the one before it, so all of them together take at most twice
+    the last."""
+
+    def __init__(self, device):
+        self.device, self.buffers = device, []
+
+    def get(self, need: int) -> torch.Tensor:
+        if not self.buffers or self.buffers[-1].numel() < need:
+            last = self.buffers[-1].numel() if self.buffers else 0
+            self.buffers.append(torch.empty(max(need, 2 * last, 16), dtype=torch.uint8,
+                                            device=self.device))
+        return self.buffers[-1]
+
+
 class KvCache:
     """A paged cache of several layers with its tables: device tensors, their
-    descriptors and one workspace. Slots are handed in as int32 device tensors.
+    descriptors and a workspace. Slots are handed in as int32 device tensors.
     Everything is enqueued on `stream` (the current one if None); calls on
     different streams have to be ordered by the caller, as they share the
-    tables and the workspace. Problems found on the device are ORed into
+    tables and the workspace. Graphs captured through the object hold its
+    addresses, so it has to outlive them; later calls, larger ones too, leave
+    what they use in place. Problems found on the device are ORed into
     err_word."""
 
     def __init__(self, *, n_layers, n_pages, page_size, n_heads, head_dim, n_slots, max_pages,
@@ -594,7 +613,19 @@ class KvCache:
                                 None if v_scale is None else v_scale[i])
                        for i in range(n_layers)]
         self.desc = kv_table(self.table, self.lens, page_size, n_pages, self.refs)
-        self._ws = None
+        self._scales = [t for t in (k_scale, v_scale) if t is not None]
+        self._ws = _Workspace(self.k.device)
+        self._streams = {}                       # those that work was enqueued on
+
+    def _on(self, stream):
+        """Tells the allocator, once per stream, that this stream uses the
+        object's tensors, so that none is given back while its work runs."""
+        raw = _stream(stream)
+        if raw not in self._streams:
+            self._streams[raw] = s = torch.cuda.current_stream() if stream is None else stream
+            for t in (self.k, self.v, self.table, self.lens, self.refs, self.err_word,
+                      *self._scales, *self._ws.buffers):
+                t.record_stream(s)
 
     def _new(self, like, stream):
         """An empty tensor like `like`, contiguous, of the stream it is used on."""
@@ -602,12 +633,15 @@ class KvCache:
             return torch.empty_like(like, memory_format=torch.contiguous_format)
 
     def workspace(self, need, stream=None):
-        if self._ws is None or self._ws.numel() < need:
-            with torch.cuda.stream(stream):
-                self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.k.device)
-        if stream is not None:
-            self._ws.record_stream(stream)
-        return self._ws
+        """At least `need` bytes for work on `stream`."""
+        self._on(stream)
+        held = len(self._ws.buffers)
+        with torch.cuda.stream(stream):
+            ws = self._ws.get(need)
+        if len(self._ws.buffers) > held:
+            for s in self._streams.values():
+                ws.record_stream(s)
+        return ws
 
     def grow(self, slots, n_new, stream=None):
         """Room for n_new more tokens of each slot; returns their first positions
@@ -618,6 +652,7 @@ class KvCache:
         return start
 
     def append(self, layer, slots, start, cu, k, v, stream=None):
+        self._on(stream)
         moe_cache_append(self.layers[layer], self.desc, start, cu, k, v, self.err_word,
                          slots=slots, stream=stream)
 
@@ -641,9 +676,11 @@ class KvCache:
         return out
 
     def free(self, slots, stream=None):
+        self._on(stream)
         moe_cache_free(self.desc, slots, self.err_word, stream)
 
     def trim(self, slots, window, n_first=0, stream=None):
+        self._on(stream)
         moe_cache_trim(self.desc, slots, window, n_first, self.err_word, stream)
 
     def fork(self, src, dst, stream=None):

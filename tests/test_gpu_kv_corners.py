@@ -1,0 +1,67 @@
+"""Corners of the cache and attention operators, each against its definition."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_expert_sigmoid_amd as M
+from tests.test_gpu_cache import _cache, _i
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU")]
+
+
+def test_graph_through_the_object_survives_larger_calls():
+    """decode captured through KvCache, then a call that needs a larger
+    workspace: replays equal the eager call and leave new tensors alone."""
+    c = _cache(4, 40, 200, 16, layers=1, hkv=2, D=64, fill=False)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    c.k.normal_(generator=gen), c.v.normal_(generator=gen)
+    slots = _i([0, 1, 2, -1])
+    c.grow(slots, _i([600, 333, 40, 0]))
+    q = torch.randn(4, 4, 64, generator=gen, device="cuda").bfloat16()
+    want = c.decode(0, slots, q, 0.125)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.decode(0, slots, q, 0.125)
+    first = c.workspace(1)
+    sizes = [first.numel()] * 4 + [1 << 16, 1 << 20]
+    for rep in range(3):
+        c.workspace(3 * c.workspace(1).numel())
+        fresh = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes]
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all((x == 0x5A).all() for x in fresh)
+        assert c.workspace(1).data_ptr() != first.data_ptr()
+        assert torch.equal(c.decode(0, slots, q, 0.125), want)
+    assert M.moe_read_device_error(c.err_word) == 0
+
+
+def test_memory_is_not_reused_under_work_on_another_stream():
+    """Calls under a stream of their own: the object's memory, given back while
+    that stream still has work, is not handed out before it is done."""
+    for how in ("current", "argument"):
+        c = _cache(2, 4, 9, 16, layers=1, hkv=1, D=64)
+        at = {t.data_ptr() for t in (c.k, c.v, c.workspace(1 << 21))}
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        q, gone = torch.randn(2, 2, 64, device="cuda").bfloat16(), _i([0])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)
+        if how == "current":
+            with torch.cuda.stream(s):
+                c.free(gone)
+                out = c.decode(0, None, q, 0.1)
+        else:
+            out = c.decode(0, None, q, 0.1, stream=s)
+        shapes = c.k.shape, c.v.shape
+        del c
+        new = [torch.empty(x, dtype=torch.bfloat16, device="cuda") for x in shapes] + \
+            [torch.empty(1 << 21, dtype=torch.uint8, device="cuda")]
+        busy = not s.query()
+        assert busy and not at & {t.data_ptr() for t in new}
+        s.synchronize()
+        assert (out == 0).all()
+        del new
