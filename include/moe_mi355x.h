@@ -499,7 +499,8 @@ size_t moe_attn_decode_workspace_size(const moe_kv_cache *cache, long n,
 /* Attention of the newest tokens of n sequences: rows cu_q[i] ..
  * cu_q[i + 1] - 1 of q (device int32 [n + 1], ascending from 0 to T) are the
  * last m = cu_q[i + 1] - cu_q[i] tokens of slot s = slots[i] (NULL: s = i),
- * row cu_q[i] + t at position len[s] - m + t. A whole prompt (m = len) or the
+ * row cu_q[i] + t at position len[s] - m + t; rows outside cu_q[0] ..
+ * cu_q[n] - 1 are not written. A whole prompt (m = len) or the
  * next chunk of one; its keys and values are in the cache already
  * (moe_cache_append). Rows with a negative slots[i] or position give 0 and
  * -infinity. T = rows of q (< 2^31 / n_heads). Workspace:

@@ -86,7 +86,8 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   t.q0 = pre_cu(a, t.seq);
   t.m = max(0, pre_cu(a, t.seq + 1) - t.q0);
   t.rows = t.m * g;
-  if (t.tile * ROWS >= t.rows) return false;
+  // (below 0 where rows of q come before the first sequence's)
+  if (t.tile < 0 || t.tile * ROWS >= t.rows) return false;
   // (uniform, told so: loads behind the error word's atomic are not taken for it)
   t.slot = __builtin_amdgcn_readfirstlane(kv_slot(a.slots, t.seq, a.t.n_slots, a.err));
   t.L = __builtin_amdgcn_readfirstlane(kv_len(a.t, t.slot));

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import mixture_experts_expert_sigmoid_amd as M
+from tests.cache_ref import Pool, check
+from tests.test_gpu_attn import _q, _reference
 from tests.test_gpu_cache import _cache, _i
 
 pytestmark = [pytest.mark.gpu,
@@ -65,3 +67,29 @@ def test_memory_is_not_reused_under_work_on_another_stream():
         s.synchronize()
         assert (out == 0).all()
         del new
+
+
+def test_prefill_rows_outside_the_list():
+    """Rows of q before the first sequence's and after the last one's: not
+    written, and no other row is touched for them."""
+    rng = np.random.default_rng(21)
+    lens, rows = [50, 90], [36, 20]
+    pool = Pool(rng, kv="bf16", hkv=2, D=128, ps=16, lens=lens)
+    q = _q(rng, 64 + 56 + 40, 8, 128, "bf16")
+    want = _reference(pool, [0, 1], rows, q[64:120], 8, 0, 0, 0.1, "bf16")
+    cache, table = pool.desc(M)
+    qd = torch.from_numpy(q).to("cuda", torch.bfloat16)
+    # heads outermost, rows of the buffer around them: all but 64..119 stay
+    buf = torch.full((10, 160, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[1:9].transpose(0, 1)
+    lse = torch.full((160, 8), 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(16, M.moe_attn_prefill_workspace_size(cache, 2, 160, 8)),
+                     dtype=torch.uint8, device="cuda")
+    M.moe_attn_prefill(cache, table, qd, _i([64, 100, 120]), out, 0.1, err, ws, lse=lse)
+    assert M.moe_read_device_error(err) == 0
+    check(out[64:120].double().cpu().numpy(), want[0], want[2], "out")
+    check(lse[64:120].double().cpu().numpy(), want[1], want[3], "lse")
+    assert (buf[0] == 7).all() and (buf[9] == 7).all()
+    assert (out[:64] == 7).all() and (out[120:] == 7).all()
+    assert (lse[:64] == 7).all() and (lse[120:] == 7).all()
