@@ -392,6 +392,13 @@ def _kv_fmt(t: torch.Tensor, where: str) -> int:
     return fmt
 
 
+def _on_gpu(where: str, *tensors: Optional[torch.Tensor]):
+    """The kernels take addresses: one of host memory would fault the GPU."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise MoeError(-5, where, f"tensor {tuple(t.shape)} is on the device {t.device}")
+
+
 def _i32(t: Optional[torch.Tensor], n: int, where: str):
     """Pointer of a contiguous int32 list of at least n entries (or None)."""
     if t is None:
@@ -399,11 +406,19 @@ def _i32(t: Optional[torch.Tensor], n: int, where: str):
     if t.dtype is not _INT32 or t.numel() < n or not t.is_contiguous():
         raise MoeError(-2, where, f"wants {n} contiguous int32, got {t.dtype} "
                                   f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        _on_gpu(where, t)
     return t.data_ptr()
 
 
-def _bytes(ws: Optional[torch.Tensor]) -> int:
-    return 0 if ws is None else ws.nbytes
+def _work(ws: Optional[torch.Tensor], where: str):
+    """Pointer and bytes of a workspace."""
+    if ws is None:
+        return None, 0
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _on_gpu(where, ws)
+        raise MoeError(-2, where, "the workspace is not contiguous")
+    return ws.data_ptr(), ws.nbytes
 
 
 def kv_cache(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
@@ -420,6 +435,7 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] =
         if sc is not None and (sc.dtype != torch.float32 or sc.numel() != k.shape[1]
                                or not sc.is_contiguous()):
             raise MoeError(-2, "kv_cache", "scales are fp32 [heads]")
+    _on_gpu("kv_cache", k, v, k_scale, v_scale)
     P, H, ps, D = k.shape
     c = MoeKvCache(_kv_fmt(k, "kv_cache"), P, ps, H, D, k.stride(0), k.stride(1), k.stride(2),
                    k.data_ptr(), v.data_ptr(),
@@ -435,6 +451,7 @@ def kv_table(table: torch.Tensor, lens: torch.Tensor, page_size: int, n_pages: i
     [slots], refs int32 [n_pages] (for grow, free, trim, fork, compact)."""
     if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
         raise MoeError(-2, "kv_table", "table is int32 [slots][max_pages], rows contiguous")
+    _on_gpu("kv_table", table)
     ld = table.stride(0) if table.shape[0] > 1 else table.shape[1]
     t = MoeKvTable(table.shape[0], table.shape[1], ld, n_pages, page_size, table.data_ptr(),
                    _i32(lens, table.shape[0], "kv_table"),
@@ -450,6 +467,8 @@ def _rows(t: torch.Tensor, where: str, shape, D: int):
     if len(st) != 3 or shape[2] != D or st[2] != 1 or t.shape != shape:
         raise MoeError(-2, where, f"wants {tuple(shape)} of [rows][heads][{D}] with contiguous "
                                   f"rows, got {tuple(t.shape)} strides {st}")
+    if not t.is_cuda:
+        _on_gpu(where, t)
     if shape[0] > 1 and shape[1] > 1:
         return st
     return (st[0] if shape[0] > 1 else shape[1] * D), (st[1] if shape[1] > 1 else D)
@@ -465,6 +484,7 @@ def _attn(where, cache: MoeKvCache, q, out, scale, window, n_first, lse) -> MoeA
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
                             or not lse.is_contiguous()):
         raise MoeError(-2, where, "lse is fp32 [rows][heads], contiguous")
+    _on_gpu(where, lse)
     return MoeAttn(fmt, shape[1], q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
                    None if lse is None else lse.data_ptr(), scale, window, n_first)
 
@@ -480,8 +500,9 @@ def moe_attn_decode(cache: MoeKvCache, table: MoeKvTable, q, out, scale, err_wor
     a = _attn(where, cache, q, out, scale, window, n_first, lse)
     n = q.shape[0]
     _check(lib().moe_attn_decode(ctypes.byref(cache), ctypes.byref(table),
-                                 _i32(slots, n, where), n, ctypes.byref(a), _p(err_word),
-                                 _p(ws), _bytes(ws), _stream(stream)), where)
+                                 _i32(slots, n, where), n, ctypes.byref(a),
+                                 _i32(err_word, 1, where), *_work(ws, where),
+                                 _stream(stream)), where)
 
 
 def moe_attn_prefill_workspace_size(cache: MoeKvCache, n: int, T: int, n_heads: int) -> int:
@@ -497,8 +518,8 @@ def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, 
     n = cu_q.numel() - 1
     _check(lib().moe_attn_prefill(ctypes.byref(cache), ctypes.byref(table),
                                   _i32(slots, n, where), n, _i32(cu_q, 1, where), q.shape[0],
-                                  ctypes.byref(a), _p(err_word), _p(ws), _bytes(ws),
-                                  _stream(stream)), where)
+                                  ctypes.byref(a), _i32(err_word, 1, where),
+                                  *_work(ws, where), _stream(stream)), where)
 
 
 def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_word, *,
@@ -515,7 +536,7 @@ def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_
     _check(lib().moe_cache_append(
         ctypes.byref(cache), ctypes.byref(table), _i32(slots, n, where),
         _i32(start, n, where), _i32(cu, 1, where), n, T, _kv_fmt(k, where), _p(k), ks[0],
-        ks[1], _p(v), vs[0], vs[1], _p(err_word), _stream(stream)), where)
+        ks[1], _p(v), vs[0], vs[1], _i32(err_word, 1, where), _stream(stream)), where)
 
 
 def moe_cache_workspace_size(table: MoeKvTable, n: int) -> int:
@@ -527,20 +548,22 @@ def moe_cache_grow(table: MoeKvTable, slots, n_new, start, err_word, ws, stream=
     n = n_new.numel()
     _check(lib().moe_cache_grow(ctypes.byref(table), _i32(slots, n, where),
                                 _i32(n_new, n, where), n, _i32(start, n, where),
-                                _p(err_word), _p(ws), _bytes(ws), _stream(stream)), where)
+                                _i32(err_word, 1, where), *_work(ws, where),
+                                _stream(stream)), where)
 
 
 def moe_cache_free(table: MoeKvTable, slots, err_word, stream=None):
+    where = "moe_cache_free"
     n = slots.numel()
-    _check(lib().moe_cache_free(ctypes.byref(table), _i32(slots, n, "moe_cache_free"), n,
-                                _p(err_word), _stream(stream)), "moe_cache_free")
+    _check(lib().moe_cache_free(ctypes.byref(table), _i32(slots, n, where), n,
+                                _i32(err_word, 1, where), _stream(stream)), where)
 
 
 def moe_cache_trim(table: MoeKvTable, slots, window, n_first, err_word, stream=None):
+    where = "moe_cache_trim"
     n = slots.numel()
-    _check(lib().moe_cache_trim(ctypes.byref(table), _i32(slots, n, "moe_cache_trim"), n,
-                                window, n_first, _p(err_word), _stream(stream)),
-           "moe_cache_trim")
+    _check(lib().moe_cache_trim(ctypes.byref(table), _i32(slots, n, where), n, window, n_first,
+                                _i32(err_word, 1, where), _stream(stream)), where)
 
 
 def _layers(caches):
@@ -552,22 +575,23 @@ def moe_cache_fork(caches, table: MoeKvTable, src, dst, err_word, ws, stream=Non
     where = "moe_cache_fork"
     n = src.numel()
     _check(lib().moe_cache_fork(_layers(caches), len(caches), ctypes.byref(table),
-                                _i32(src, n, where), _i32(dst, n, where), n, _p(err_word),
-                                _p(ws), _bytes(ws), _stream(stream)), where)
+                                _i32(src, n, where), _i32(dst, n, where), n,
+                                _i32(err_word, 1, where), *_work(ws, where),
+                                _stream(stream)), where)
 
 
 def moe_cache_compact(caches, table: MoeKvTable, n_used, err_word, ws, stream=None):
     where = "moe_cache_compact"
     _check(lib().moe_cache_compact(_layers(caches), len(caches), ctypes.byref(table),
-                                   _i32(n_used, 1, where), _p(err_word), _p(ws), _bytes(ws),
-                                   _stream(stream)), where)
+                                   _i32(n_used, 1, where), _i32(err_word, 1, where),
+                                   *_work(ws, where), _stream(stream)), where)
 
 
 def moe_cache_copy_pages(caches, src, dst, err_word, stream=None):
     where = "moe_cache_copy_pages"
     n = src.numel()
     _check(lib().moe_cache_copy_pages(_layers(caches), len(caches), _i32(src, n, where),
-                                      _i32(dst, n, where), n, _p(err_word),
+                                      _i32(dst, n, where), n, _i32(err_word, 1, where),
                                       _stream(stream)), where)
 
 
