@@ -411,6 +411,13 @@ def _i32(t: Optional[torch.Tensor], n: int, where: str):
     return t.data_ptr()
 
 
+def _err(t: Optional[torch.Tensor], where: str):
+    """Pointer of an error word."""
+    if t is not None and t.dtype is _INT32 and t.is_cuda and t.numel():
+        return t.data_ptr()
+    return _i32(t, 1, where)
+
+
 def _work(ws: Optional[torch.Tensor], where: str):
     """Pointer and bytes of a workspace."""
     if ws is None:
@@ -474,39 +481,38 @@ def _rows(t: torch.Tensor, where: str, shape, D: int):
     return (st[0] if shape[0] > 1 else shape[1] * D), (st[1] if shape[1] > 1 else D)
 
 
-def _attn(where, cache: MoeKvCache, q, out, scale, window, n_first, lse) -> MoeAttn:
-    shape, D, fmt = q.shape, cache.head_dim, _KV_FMT.get(q.dtype)
+def _attn(where, cache: MoeKvCache, shape, q, out, scale, window, n_first, lse) -> MoeAttn:
+    D, fmt = cache.head_dim, _KV_FMT.get(q.dtype)
     if out.dtype is not q.dtype:
         raise MoeError(-2, where, "out and q differ in type")
     if fmt is None:
         raise MoeError(-3, where, f"dtype {q.dtype}")
     qs, os_ = _rows(q, where, shape, D), _rows(out, where, shape, D)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
-                            or not lse.is_contiguous()):
+                            or not lse.is_contiguous() or not lse.is_cuda):
+        _on_gpu(where, lse)
         raise MoeError(-2, where, "lse is fp32 [rows][heads], contiguous")
-    _on_gpu(where, lse)
     return MoeAttn(fmt, shape[1], q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
                    None if lse is None else lse.data_ptr(), scale, window, n_first)
 
 
 def moe_attn_decode_workspace_size(cache: MoeKvCache, n: int, n_heads: int) -> int:
-    return lib().moe_attn_decode_workspace_size(ctypes.byref(cache), n, n_heads)
+    return lib().moe_attn_decode_workspace_size(cache, n, n_heads)
 
 
 def moe_attn_decode(cache: MoeKvCache, table: MoeKvTable, q, out, scale, err_word, ws, *,
                     window=0, n_first=0, slots=None, lse=None, stream=None):
     """One new token per sequence: q and out [n][heads][head_dim], lse [n][heads]."""
     where = "moe_attn_decode"
-    a = _attn(where, cache, q, out, scale, window, n_first, lse)
-    n = q.shape[0]
-    _check(lib().moe_attn_decode(ctypes.byref(cache), ctypes.byref(table),
-                                 _i32(slots, n, where), n, ctypes.byref(a),
-                                 _i32(err_word, 1, where), *_work(ws, where),
+    shape = q.shape
+    a, n = _attn(where, cache, shape, q, out, scale, window, n_first, lse), shape[0]
+    _check(lib().moe_attn_decode(cache, table, _i32(slots, n, where), n, a,
+                                 _err(err_word, where), *_work(ws, where),
                                  _stream(stream)), where)
 
 
 def moe_attn_prefill_workspace_size(cache: MoeKvCache, n: int, T: int, n_heads: int) -> int:
-    return lib().moe_attn_prefill_workspace_size(ctypes.byref(cache), n, T, n_heads)
+    return lib().moe_attn_prefill_workspace_size(cache, n, T, n_heads)
 
 
 def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, err_word, ws,
@@ -514,11 +520,11 @@ def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, 
     """The newest tokens of n = len(cu_q) - 1 sequences: q and out
     [T][heads][head_dim], lse [T][heads]."""
     where = "moe_attn_prefill"
-    a = _attn(where, cache, q, out, scale, window, n_first, lse)
+    shape = q.shape
+    a = _attn(where, cache, shape, q, out, scale, window, n_first, lse)
     n = cu_q.numel() - 1
-    _check(lib().moe_attn_prefill(ctypes.byref(cache), ctypes.byref(table),
-                                  _i32(slots, n, where), n, _i32(cu_q, 1, where), q.shape[0],
-                                  ctypes.byref(a), _i32(err_word, 1, where),
+    _check(lib().moe_attn_prefill(cache, table, _i32(slots, n, where), n,
+                                  _i32(cu_q, 1, where), shape[0], a, _err(err_word, where),
                                   *_work(ws, where), _stream(stream)), where)
 
 
@@ -527,43 +533,43 @@ def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_
     """k and v [T][heads][head_dim] to positions start[i].. of the slots; cu int32
     [n + 1], or None for one token each."""
     where = "moe_cache_append"
-    T = k.shape[0]
-    n = T if cu is None else cu.numel() - 1
     shape, D = k.shape, cache.head_dim
+    T = shape[0]
+    n = T if cu is None else cu.numel() - 1
     if v.dtype is not k.dtype or (T and shape[1] != cache.n_heads):
         raise MoeError(-2, where, "k and v differ in type, or their heads from the cache's")
     ks, vs = _rows(k, where, shape, D), _rows(v, where, shape, D)
     _check(lib().moe_cache_append(
-        ctypes.byref(cache), ctypes.byref(table), _i32(slots, n, where),
-        _i32(start, n, where), _i32(cu, 1, where), n, T, _kv_fmt(k, where), _p(k), ks[0],
-        ks[1], _p(v), vs[0], vs[1], _i32(err_word, 1, where), _stream(stream)), where)
+        cache, table, _i32(slots, n, where), _i32(start, n, where), _i32(cu, 1, where), n, T,
+        _kv_fmt(k, where), _p(k), ks[0], ks[1], _p(v), vs[0], vs[1], _err(err_word, where),
+        _stream(stream)), where)
 
 
 def moe_cache_workspace_size(table: MoeKvTable, n: int) -> int:
-    return lib().moe_cache_workspace_size(ctypes.byref(table), n)
+    return lib().moe_cache_workspace_size(table, n)
 
 
 def moe_cache_grow(table: MoeKvTable, slots, n_new, start, err_word, ws, stream=None):
     where = "moe_cache_grow"
     n = n_new.numel()
-    _check(lib().moe_cache_grow(ctypes.byref(table), _i32(slots, n, where),
+    _check(lib().moe_cache_grow(table, _i32(slots, n, where),
                                 _i32(n_new, n, where), n, _i32(start, n, where),
-                                _i32(err_word, 1, where), *_work(ws, where),
+                                _err(err_word, where), *_work(ws, where),
                                 _stream(stream)), where)
 
 
 def moe_cache_free(table: MoeKvTable, slots, err_word, stream=None):
     where = "moe_cache_free"
     n = slots.numel()
-    _check(lib().moe_cache_free(ctypes.byref(table), _i32(slots, n, where), n,
-                                _i32(err_word, 1, where), _stream(stream)), where)
+    _check(lib().moe_cache_free(table, _i32(slots, n, where), n,
+                                _err(err_word, where), _stream(stream)), where)
 
 
 def moe_cache_trim(table: MoeKvTable, slots, window, n_first, err_word, stream=None):
     where = "moe_cache_trim"
     n = slots.numel()
-    _check(lib().moe_cache_trim(ctypes.byref(table), _i32(slots, n, where), n, window, n_first,
-                                _i32(err_word, 1, where), _stream(stream)), where)
+    _check(lib().moe_cache_trim(table, _i32(slots, n, where), n, window, n_first,
+                                _err(err_word, where), _stream(stream)), where)
 
 
 def _layers(caches):
@@ -574,16 +580,16 @@ def moe_cache_fork(caches, table: MoeKvTable, src, dst, err_word, ws, stream=Non
     """caches: the MoeKvCache of every layer."""
     where = "moe_cache_fork"
     n = src.numel()
-    _check(lib().moe_cache_fork(_layers(caches), len(caches), ctypes.byref(table),
+    _check(lib().moe_cache_fork(_layers(caches), len(caches), table,
                                 _i32(src, n, where), _i32(dst, n, where), n,
-                                _i32(err_word, 1, where), *_work(ws, where),
+                                _err(err_word, where), *_work(ws, where),
                                 _stream(stream)), where)
 
 
 def moe_cache_compact(caches, table: MoeKvTable, n_used, err_word, ws, stream=None):
     where = "moe_cache_compact"
-    _check(lib().moe_cache_compact(_layers(caches), len(caches), ctypes.byref(table),
-                                   _i32(n_used, 1, where), _i32(err_word, 1, where),
+    _check(lib().moe_cache_compact(_layers(caches), len(caches), table,
+                                   _i32(n_used, 1, where), _err(err_word, where),
                                    *_work(ws, where), _stream(stream)), where)
 
 
@@ -591,7 +597,7 @@ def moe_cache_copy_pages(caches, src, dst, err_word, stream=None):
     where = "moe_cache_copy_pages"
     n = src.numel()
     _check(lib().moe_cache_copy_pages(_layers(caches), len(caches), _i32(src, n, where),
-                                      _i32(dst, n, where), n, _i32(err_word, 1, where),
+                                      _i32(dst, n, where), n, _err(err_word, where),
                                       _stream(stream)), where)
 
 
