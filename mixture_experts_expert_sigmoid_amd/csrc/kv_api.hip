@@ -112,8 +112,12 @@ int attn_args(const moe_kv_cache* cache, const moe_kv_table* table, const int* s
   a->hq = at->n_heads;
   a->g = at->n_heads / cache->n_heads;
   a->scale = at->scale * 1.44269504088896340736f;
-  a->window = at->window;
-  a->first = at->window ? at->n_first : 0;
+  // A window that no context of this table exceeds is none. What is left is at
+  // most kMaxTokens, so that position - window stays within 32 bits, for rows
+  // before a sequence's first position too.
+  const long most = (long)table->max_pages * table->page_size;
+  a->window = at->window < most ? at->window : 0;
+  a->first = a->window ? (int)(at->n_first < most ? at->n_first : most) : 0;
   a->err = err_word;
   return MOE_OK;
 }

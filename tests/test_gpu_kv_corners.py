@@ -5,7 +5,7 @@ import torch
 
 import mixture_experts_expert_sigmoid_amd as M
 from tests.cache_ref import Pool, check
-from tests.test_gpu_attn import _q, _reference
+from tests.test_gpu_attn import _q, _reference, _run
 from tests.test_gpu_cache import _cache, _i
 
 pytestmark = [pytest.mark.gpu,
@@ -93,3 +93,22 @@ def test_prefill_rows_outside_the_list():
     assert (buf[0] == 7).all() and (buf[9] == 7).all()
     assert (out[:64] == 7).all() and (out[120:] == 7).all()
     assert (lse[:64] == 7).all() and (lse[120:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("window,first", [(2**31 - 1, 2**31 - 1), (2**31 - 1, 3), (96, 2**31 - 1),
+                                          (95, 2**31 - 1), (95, 0)])
+def test_largest_windows_and_rows_before_the_first_position(kind, window, first):
+    """Windows and first tokens up to the largest int, over a table of 96
+    tokens, with rows without a sequence and rows before position 0."""
+    rng = np.random.default_rng(22)
+    pool = Pool(rng, kv="bf16", hkv=2, D=64, ps=16, lens=[96, 20, 0], max_pages=6)
+    slots = [0, -1, 1, 2]
+    rows = [1] * 4 if kind == "decode" else [70, 30, 40, 3]
+    q = _q(rng, sum(rows), 4, 64, "bf16")
+    out, lse, err = _run(kind, pool, slots, rows, q, 4, window, first, 0.1, "bf16")
+    want = _reference(pool, slots, rows, q, 4, window, first, 0.1, "bf16")
+    assert err == 0
+    check(out, want[0], want[2], "out")
+    check(lse, want[1], want[3], "lse")
+    assert np.isneginf(lse).any() and np.isfinite(lse).any()
