@@ -536,9 +536,9 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * moe_cache_grow makes room for n_new[i] >= 0 more tokens of slots[i] (NULL:
  * i) and counts them in: start[i] = len, len += n_new[i], with new pages
  * where page_size * (entries held) is short. A slot is left as it was, with
- * start[i] = -1 and MOE_DEVERR_CACHE_FULL, if its table row is too short or
- * if the slots up to it in the list whose rows suffice need more pages in all
- * than are free.
+ * start[i] = -1 and MOE_DEVERR_CACHE_FULL, if its table row is too short, or
+ * if it needs a page and the slots up to it in the list whose rows suffice
+ * need more pages in all than are free.
  *
  * moe_cache_free gives the slots' pages back (refs - 1 each, entries -1,
  * len 0). moe_cache_trim gives back the pages whose tokens j all have

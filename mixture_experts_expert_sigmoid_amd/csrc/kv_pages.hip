@@ -139,6 +139,7 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
   __shared__ long s_w[kWaves];
   __shared__ int s_cnt[kWaves];
   Scan sc{0};
+  bool spent = false;      // the list has asked for more pages than were free
   for (int base = 0; base < n; base += kThreads) {
     const int i = base + threadIdx.x, m = min(n - base, kThreads);
     int slot = -1, L = 0, add = 0;
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
       if (slot >= 0) {
         have = div_up(L, t.ps);
         const long want = div_up((long)L + add, t.ps);
-        full = want > t.max_pages;
+        full = want > t.max_pages || (spent && want > have);
         need = full ? 0 : want - have;
       }
     }
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
       if (ok && add > 0) t.len[slot] = L + add;
       if (slot >= 0 && full) atomicOr(err, kErrFull);
     }
-    if (found < total) sc.pos = 0;   // pages went back: look again from the front
+    spent |= found < total;
     __syncthreads();
   }
 }

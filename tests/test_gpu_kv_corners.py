@@ -6,7 +6,7 @@ import torch
 import mixture_experts_expert_sigmoid_amd as M
 from tests.cache_ref import Pool, check
 from tests.test_gpu_attn import _q, _reference, _run
-from tests.test_gpu_cache import _cache, _i
+from tests.test_gpu_cache import Sim, _cache, _i, _same
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU")]
@@ -112,3 +112,25 @@ def test_largest_windows_and_rows_before_the_first_position(kind, window, first)
     check(out, want[0], want[2], "out")
     check(lse, want[1], want[3], "lse")
     assert np.isneginf(lse).any() and np.isfinite(lse).any()
+
+
+@pytest.mark.parametrize("free,new", [
+    (1, [0] * 1023 + [20, 5, 0]),                # entry 1023 needs two pages, 1024 one
+    (150, [1] * 10 + [200 * 16] + [1] * 2000),
+    (3, [16] * 1024 + [0, 16, 0]),               # short within the first 1024, then no need
+])
+def test_grow_refuses_all_after_the_shortage(free, new):
+    """Once the list needs more pages than are free, no later slot that needs a
+    page gets one, wherever in the list it stands; a slot that needs none does."""
+    n, ps, mp, P = len(new), 16, 201, 3000
+    print(f"[case] grow {free} of {n}", flush=True)
+    c, sim = _cache(n, mp, P, ps, layers=1, hkv=1, fill=False), Sim(n, mp, P, ps)
+    refs = np.ones(P, np.int32)
+    refs[np.random.default_rng(free).choice(P, free, replace=False)] = 0
+    c.refs.copy_(torch.from_numpy(refs))
+    sim.refs = refs.tolist()
+    start = c.grow(None, _i(new))
+    want = sim.grow(range(n), new)
+    assert start.tolist() == want
+    _same(c, sim, "grow")
+    assert sim.err == M.MOE_DEVERR_CACHE_FULL and -1 in want and 0 in want
