@@ -125,16 +125,22 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
       const int c8 = bx[k] & (upr - 1);
       char* dst = (val ? a.c.v : a.c.k) + off + h * a.c.sh;
       if (Q) {
-        // x / s: with y = RN(1 / s), q0 = RN(x y) and the residual x - q0 s,
-        // exact by FMA, RN(q0 + residual y) is the correctly rounded quotient
-        // (Markstein's theorem) where nothing leaves the normal range or the
-        // quotient is far below the least code; other lanes divide. Three
-        // operations a value instead of the division's ten.
+        // x / s: with y = RN(1 / s), q0 = RN(x y) and the residual r = q0 s - x,
+        // exact by FMA, q = RN(q0 - r y). q0 is within 1.5 units of its last
+        // place u of x / s, so q0 - r y within 2^-23 u, and q is RN(x / s) but
+        // where x / s lies that close to a point halfway between two floats;
+        // there it may be the other of the two. The code is the quotient's all
+        // the same: it could differ only beside a tie T of the codes (5 bits,
+        // 16 <= T < 32), where x 2^a = (T 2^20 +- 1) S + d, |d| <= 8, S the 24
+        // bits of s. x has at most 11 bits, so a > 30, which asks for S = j 2^20
+        // -+ d and j = T d: but 8 <= j < 16. A zero keeps its sign: r is +0 for
+        // zeros of both signs, so q0 - r y is q0. All this in the normal range
+        // and for s > 0; other lanes divide. Three operations a value instead of
+        // the division's ten.
         const float s = (val ? a.c.vs : a.c.ks)[h];
-        const float as = fabsf(s);
         const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
         float f[8];
-        bool fast = as >= 0x1p-60f && as <= 0x1p60f;
+        bool fast = s >= 0x1p-60f && s <= 0x1p60f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           f[j] = in_f32<IN>(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFF);
@@ -145,7 +151,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float q0 = __fmul_rn(f[j], y);
-            f[j] = __builtin_fmaf(__builtin_fmaf(-q0, s, f[j]), y, q0);
+            f[j] = __builtin_fmaf(-__builtin_fmaf(q0, s, -f[j]), y, q0);
           }
         } else {
 #pragma unroll

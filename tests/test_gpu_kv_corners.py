@@ -4,9 +4,9 @@ import pytest
 import torch
 
 import mixture_experts_expert_sigmoid_amd as M
-from tests.cache_ref import Pool, check
+from tests.cache_ref import DT, Pool, check
 from tests.test_gpu_attn import _q, _reference, _run
-from tests.test_gpu_cache import Sim, _cache, _i, _same
+from tests.test_gpu_cache import Sim, _cache, _codes, _i, _same
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU")]
@@ -134,3 +134,26 @@ def test_grow_refuses_all_after_the_shortage(free, new):
     assert start.tolist() == want
     _same(c, sim, "grow")
     assert sim.err == M.MOE_DEVERR_CACHE_FULL and -1 in want and 0 in want
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_append_keeps_the_sign_of_zero(dt):
+    """Codes of zeros of both signs by scales of both signs, alone and beside
+    values that take the division."""
+    D, ps, H = 64, 16, 2
+    k, v = (torch.zeros(1, H, ps, D, dtype=torch.uint8, device="cuda").view(DT["e4m3"])
+            for _ in range(2))
+    sc = torch.tensor([0.03, -0.03], device="cuda")
+    x = torch.randn(3, H, D, generator=torch.Generator().manual_seed(1)).to("cuda", DT[dt])
+    x[:, :, ::3] = -0.0
+    x[:, :, 1::6] = 0.0
+    x[1, :, 5] = float("inf")                    # its unit of eight divides
+    x[2, :, 13] = float("nan")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    M.moe_cache_append(M.kv_cache(k, v, sc, sc), M.kv_table(_i([[0]]), _i([0]), ps, 1), _i([0]),
+                       _i([0, 3]), x, -x, err)
+    for got, new in ((k, x), (v, -x)):
+        want = _codes(new, sc).view(torch.uint8)
+        want[new.isnan()] = 0x7F
+        assert torch.equal(got.view(torch.uint8)[0, :, :3].transpose(0, 1), want)
+        assert (want == 0x80).any() and (want == 0).any()
