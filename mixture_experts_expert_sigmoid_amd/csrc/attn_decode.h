@@ -41,6 +41,13 @@ namespace {
 
 constexpr int kDecPartRow = 32;       // maxima and sums of 16 heads, before their D floats each
 
+// Probabilities are taken 2^lift times as large, at most 2^15 in f16, whose
+// numbers end at 2^-24: keys down to 2^-40 of the largest enter the product,
+// where many of them beside one strong key would otherwise count in the sum but
+// not in the product (130 k keys at 2^-26: 0.2 %). bf16 has the exponents of
+// fp32. Sums and O are as much larger; a quotient of them is not.
+template <bool BF> constexpr float kDecLift = BF ? 0.0f : 15.0f;
+
 // what a query at position L - 1 sees, as blocks of 32 keys: blocks 0..nb1-1
 // (first keys), then those from b2 on up to the length
 struct DecSpan {
@@ -347,7 +354,7 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
       float ps = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sv[j] = exp2_fast(sv[j] - mu);
+        sv[j] = exp2_fast(BF ? sv[j] - mu : sv[j] - mu + kDecLift<BF>);
         ps += sv[j];
       }
       l = l * alpha + ps;
@@ -469,7 +476,7 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
             slot_p[lc] = m;
             slot_p[16 + lc] = l;
           } else if (a.lse) {
-            a.lse[(long)seq * a.hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+            a.lse[(long)seq * a.hq + head] = (m + (__builtin_amdgcn_logf(l) - kDecLift<BF>)) * kLn2;
           }
         }
       }
@@ -527,7 +534,8 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
             *(u32x2*)(dst + 2 * t) = y;
           }
           if (a.lse && (tid & 15) == 0)
-            a.lse[(long)seq * a.hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+            a.lse[(long)seq * a.hq + head] =
+                (mm + (__builtin_amdgcn_logf(ll) - kDecLift<BF>)) * kLn2;
         } else {
           if ((tid & 15) == 0) {
             slot_p[hh] = mm;
@@ -610,7 +618,7 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
         *(uint32_t*)(dst + 2 * (lane * E + e)) = pack16<BF>(s.o[e] * inv, s.o[e + 1] * inv);
     }
     if (a.lse && lane == 0)
-      a.lse[(long)seq * a.hq + head] = (s.m + __builtin_amdgcn_logf(s.l)) * kLn2;
+      a.lse[(long)seq * a.hq + head] = (s.m + (__builtin_amdgcn_logf(s.l) - kDecLift<BF>)) * kLn2;
   };
   const State none{kNegInf, 0.0f, {}};
 

@@ -16,8 +16,8 @@
 // transposed (ds_read_b64_tr_b16), in that key order.
 //
 // Rescaling. O and the sum follow the maximum only when it has grown by more
-// than 8 (a factor of 2^8 of P, which neither type nor sum minds): rare after
-// the first tiles, and exact all the same.
+// than a factor of 2^8 of P (f16: 2^3.9), which neither type nor sum minds: rare
+// after the first tiles, and exact all the same.
 //
 // Masked places. Scores are replaced, not added to. V rows that no row of the
 // tile sees are staged as zeros; in tiles where some rows see a key and some
@@ -114,6 +114,21 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
   return max(1, min(min(a.n_split, nb >> 2), (int)sqrtf((float)nb * a.split_gain)));
 }
 
+// A maximum is followed when it has grown by more than 2^kDefer. In f16, whose
+// numbers end at 2^-24 and have all their bits from 2^-14 on, probabilities are
+// taken 2^kLift times as large, so that many weak keys beside a strong one are
+// not lost from the product while they count in the sum; both together stay
+// below 2^16. bf16 has the exponents of fp32. Following so much sooner costs
+// f16 prompts of 6000 tokens 1 % at head_dim 64 and 128, 5 % at 256 (8 % over
+// e4m3), whose O takes three instructions a register to rescale. No lift for a
+// maximum (of scores in base 2) whose own rounding could take them past 2^16.
+template <bool BF> constexpr float kDefer = BF ? 8.0f : 3.9f;
+constexpr float kLift = 12.0f;
+template <bool BF>
+__device__ __forceinline__ float pre_lift(float m) {
+  return !BF && fabsf(m) < 0x1p18f ? kLift : 0.0f;
+}
+
 template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_prefill_kernel(AttnArgs a) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
@@ -159,7 +174,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const uint32_t flip = sc < 0.0f ? 0x80008000u : 0u;
   const bool flat = sc == 0.0f;
   sc = flat ? 1.0f : fabsf(sc);
-  const float thr = fminf(8.0f / sc, 1e30f);
+  const float thr = fminf(kDefer<BF> / sc, 1e30f);
 
   // this lane's row
   struct Row {
@@ -423,7 +438,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     bm = xor32_reduce(bm, OpMax{});
     if (__any(bm > m + thr)) {
       const float mn = fmaxf(m, bm);
-      const float f = exp2_fast((m - (mn == kNegInf ? 0.0f : mn)) * sc);
+      float df = (m - (mn == kNegInf ? 0.0f : mn)) * sc;
+      if constexpr (!BF) df += pre_lift<BF>(mn * sc) - pre_lift<BF>(m * sc);
+      const float f = exp2_fast(df);
       m = mn;
       l *= f;
 #pragma unroll
@@ -431,6 +448,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
+  };
+  // the exponent of P less s sc
+  auto neg_of = [&] {
+    const float ms = m * sc;
+    return m == kNegInf ? 0.0f : BF ? -ms : pre_lift<BF>(ms) - ms;
   };
   // P of a tile (s), its sum and its product with V (vx), and beside them, if
   // NEXT, S^T of the next tile (sn) from its K (kn). One matrix instruction
@@ -451,7 +473,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     constexpr bool NEXT = decltype(next)::value;
     constexpr int MQ = NEXT ? NA * NC : 0, MV = 2 * NA * ND, NE = 16 * NA;
     asm volatile("" : "+v"(k_at), "+v"(v_at));   // not 2 x NC addresses kept in registers
-    const float neg = m == kNegInf ? 0.0f : -m * sc;
+    const float neg = neg_of();
     u32x4 op[MQ + MV], pb[2 * NA];
     float pend[kLag + 1], p0 = 0.0f;
     auto read = [&](int i) {
@@ -598,7 +620,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
           }
         dot = xor32_reduce(dot, OpSum{});
         const bool sees = j <= pos && (j >= lo || j < a.first);
-        const float pv = exp2_fast(__builtin_fmaf(dot, sc, m == kNegInf ? 0.0f : -m * sc));
+        const float pv = exp2_fast(__builtin_fmaf(dot, sc, neg_of()));
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -641,7 +663,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
                   (kvh * a.g + row_of + rr - tk * a.g) * a.o_head + 16 * u) = y;
     }
     if (a.lse && half == 0 && me.have)
-      a.lse[me.q * a.hq + me.head] = (m * sc + __builtin_amdgcn_logf(l)) * kLn2;
+      a.lse[me.q * a.hq + me.head] =
+          (m * sc + (__builtin_amdgcn_logf(l) - pre_lift<BF>(m * sc))) * kLn2;
   } else if (me.have) {
     const long rows = a.T * a.hq, ri = me.q * a.hq + me.head;
     float* dst = a.part + ((long)blockIdx.y * rows + ri) * D;
@@ -653,7 +676,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
             f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
     if (half == 0) {
       float* ml = a.part + (long)a.n_split * rows * D + ((long)blockIdx.y * rows + ri) * 2;
-      ml[0] = m * sc;
+      ml[0] = m * sc - pre_lift<BF>(m * sc);
       ml[1] = l;
     }
   }

@@ -157,3 +157,52 @@ def test_append_keeps_the_sign_of_zero(dt):
         want[new.isnan()] = 0x7F
         assert torch.equal(got.view(torch.uint8)[0, :, :3].transpose(0, 1), want)
         assert (want == 0x80).any() and (want == 0).any()
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("dt,kv,D", [("f16", "f16", 64), ("f16", "e4m3", 128), ("f16", "f16", 256),
+                                     ("bf16", "bf16", 128)])
+def test_many_weak_keys_beside_a_strong_one(kind, dt, kv, D):
+    """A page of one strong key (score 18, V = 0) and 1023 weak ones (score 0,
+    V = 64), named 128 times: all of out comes from probabilities of e^-18 =
+    2^-25.97 of the largest. Bar: a score of 26 in base 2 is rounded twice
+    (under 2^-17 of the probability, the exponential and the division with it),
+    each probability and the result are rounded to the type (u each), and one
+    fp32 sum takes a step for every 16 keys at most (2^-24 each)."""
+    n, hq, T, ps, entries = 2, 4, 70, 1024, 128
+    k, v = torch.zeros(1, 1, ps, D), torch.full((1, 1, ps, D), 64.0)
+    k[..., 3, 0] = 18.0
+    v[..., 3, :] = 0.0
+    k, v = (x.to(DT[kv]).cuda() for x in (k, v))
+    one = torch.ones(1, device="cuda") if kv == "e4m3" else None
+    cache = M.kv_cache(k, v, one, one)
+    table = M.kv_table(torch.zeros(n, entries, dtype=torch.int32, device="cuda"),
+                       _i([ps * entries] * n), ps, 1)
+    rows = n if kind == "decode" else n * T
+    q = torch.zeros(rows, hq, D, dtype=DT[dt], device="cuda")
+    q[..., 0] = 1.0
+    out, lse = torch.empty_like(q), torch.empty(rows, hq, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    print(f"[case] weak keys {kind} {dt} {kv} {D}", flush=True)
+    if kind == "decode":
+        ws = torch.empty(M.moe_attn_decode_workspace_size(cache, n, hq), dtype=torch.uint8,
+                         device="cuda")
+        M.moe_attn_decode(cache, table, q, out, 1.0, err, ws, lse=lse)
+    else:
+        ws = torch.empty(max(16, M.moe_attn_prefill_workspace_size(cache, n, rows, hq)),
+                         dtype=torch.uint8, device="cuda")
+        M.moe_attn_prefill(cache, table, q, _i([0, T, 2 * T]), out, 1.0, err, ws, lse=lse)
+    # keys seen: of the prompts' earlier rows the last ones are missing
+    end = ps * entries
+    L = np.full((n, 1), end) if kind == "decode" else \
+        np.arange(end - T + 1, end + 1)[None].repeat(n, 0)
+    strong = L // ps + (L % ps > 3)
+    z = strong + (L - strong) * np.exp(-18.0)
+    want = (64.0 * (L - strong) * np.exp(-18.0) / z).reshape(-1, 1, 1)
+    u = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dt]
+    bar = (2 * u + 2.0 ** -17 + end / 16 * 2.0 ** -24) * want
+    check(out.double().cpu().numpy(), np.broadcast_to(want, out.shape),
+          np.broadcast_to(bar, out.shape), "out")
+    want = np.broadcast_to((18.0 + np.log(z)).reshape(-1, 1), lse.shape)
+    check(lse.double().cpu().numpy(), want, np.full(lse.shape, 2.0 ** -21 * 60), "lse")
+    assert M.moe_read_device_error(err) == 0
