@@ -542,7 +542,9 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * need more pages in all than are free.
  *
  * moe_cache_free gives the slots' pages back (refs - 1 each, entries -1,
- * len 0). moe_cache_trim gives back the pages whose tokens j all have
+ * len 0), those in entries past the tokens too. (Grow and fork expect none
+ * there: grow writes over such entries, fork leaves them out.)
+ * moe_cache_trim gives back the pages whose tokens j all have
  * n_first <= j < len - window (no query from position len - 1 on sees them),
  * entries -1, len unchanged.
  *

@@ -192,18 +192,27 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
   }
 }
 
+// the whole row, kFreePer entries a thread: a caller may have put pages there
+// ahead of the slot's tokens
+constexpr int kFreePer = 4;
+
 __global__ __launch_bounds__(256) void free_kernel(KvTable t, const int* slots, int* err) {
   const int slot = kv_slot(slots, blockIdx.x, t.n_slots, err);
   if (slot < 0) return;
-  const int used = (int)div_up(kv_len(t, slot), t.ps);
   int* row = t.table + slot * t.ld;
-  for (int j = threadIdx.x; j < used; j += 256) {
-    const int e = row[j];
-    row[j] = -1;
-    if (e >= 0 && e < t.n_pages) atomicSub(&t.refs[e], 1);
+  int e[kFreePer];
+#pragma unroll
+  for (int k = 0; k < kFreePer; ++k) {
+    const int j = ((int)blockIdx.y * kFreePer + k) * 256 + threadIdx.x;
+    e[k] = j < t.max_pages ? row[j] : -1;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) t.len[slot] = 0;
+#pragma unroll
+  for (int k = 0; k < kFreePer; ++k) {
+    if (e[k] == -1) continue;
+    row[((int)blockIdx.y * kFreePer + k) * 256 + threadIdx.x] = -1;
+    if (e[k] >= 0 && e[k] < t.n_pages) atomicSub(&t.refs[e[k]], 1);
+  }
+  if (blockIdx.y == 0 && threadIdx.x == 0) t.len[slot] = 0;
 }
 
 __global__ __launch_bounds__(256) void trim_kernel(KvTable t, const int* slots, int window,
@@ -562,7 +571,8 @@ hipError_t launch_cache_grow(const KvTable& t, const int* slots, const int* n_ne
 
 hipError_t launch_cache_free(const KvTable& t, const int* slots, long n, int* err,
                              hipStream_t s) {
-  free_kernel<<<(int)n, 256, 0, s>>>(t, slots, err);
+  const unsigned parts = (unsigned)((t.max_pages + 256 * kFreePer - 1) / (256 * kFreePer));
+  free_kernel<<<dim3((unsigned)n, parts), 256, 0, s>>>(t, slots, err);
   return hipGetLastError();
 }
 

@@ -206,3 +206,25 @@ def test_many_weak_keys_beside_a_strong_one(kind, dt, kv, D):
     want = np.broadcast_to((18.0 + np.log(z)).reshape(-1, 1), lse.shape)
     check(lse.double().cpu().numpy(), want, np.full(lse.shape, 2.0 ** -21 * 60), "lse")
     assert M.moe_read_device_error(err) == 0
+
+
+def test_free_gives_back_pages_past_the_length():
+    """Pages that a caller has put into a slot's row ahead of its tokens are the
+    slot's pages too."""
+    S, mp, P, ps = 3, 5000, 40, 16
+    c = _cache(S, mp, P, ps, layers=1, fill=False)
+    tab = torch.full((S, mp), -1, dtype=torch.int32)
+    tab[0, :3] = torch.tensor([4, 9, 30])
+    tab[1, :2] = torch.tensor([5, 6])
+    tab[1, 4000], tab[1, 4999] = 7, 9            # 9 is shared
+    tab[2, 0] = 11
+    refs = torch.zeros(P, dtype=torch.int32)
+    for p in tab[tab >= 0].tolist():
+        refs[p] += 1
+    c.table.copy_(tab), c.refs.copy_(refs), c.lens.copy_(torch.tensor([20, 17, 1]))
+    c.free(_i([1, -1, 0]))
+    torch.cuda.synchronize()
+    assert c.lens.tolist() == [0, 0, 1]
+    assert (c.table[:2] == -1).all() and c.table[2, 0].item() == 11
+    assert c.refs.nonzero().flatten().tolist() == [11] and c.refs[11].item() == 1
+    assert M.moe_read_device_error(c.err_word) == 0
