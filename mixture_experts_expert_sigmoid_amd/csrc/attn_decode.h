@@ -449,15 +449,16 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
     if constexpr (TS == 1) {
       if (lc < heads) {
         const int head = kvh * a.g + hbase + lc;
-        const float inv = l == 0.0f ? 0.0f : vs / l;     // no visible key: 0
+        const float inv = vs / l;
         char* dst = a.out + seq * a.o_row + head * a.o_head;
         float* part = slot_p + kDecPartRow + lc * D;
         // four values of the head from d on; e4m3: row 4 lg + i of tile t is
         // value (D / 16) row + t
         auto put = [&](int d, f32x4 y) {
           if (whole_pair)
-            *(u32x2*)(dst + 2 * d) = u32x2{pack16<BF>(y[0] * inv, y[1] * inv),
-                                           pack16<BF>(y[2] * inv, y[3] * inv)};
+            *(u32x2*)(dst + 2 * d) =
+                u32x2{pack16<BF>(of_sum(y[0], inv, l), of_sum(y[1], inv, l)),
+                      pack16<BF>(of_sum(y[2], inv, l), of_sum(y[3], inv, l))};
           else
             *(f32x4*)(part + d) = y;
         };
@@ -525,12 +526,12 @@ __global__ __launch_bounds__(256, dec_waves(D, F8)) void attn_decode_kernel(Attn
         }
         const int head = kvh * a.g + hbase + hh;
         if (whole_pair) {
-          const float inv = ll == 0.0f ? 0.0f : vs / ll;       // no visible key: 0
+          const float inv = vs / ll;
           char* dst = a.out + seq * a.o_row + head * a.o_head + 2 * d0;
 #pragma unroll
           for (int t = 0; t < VE; t += 4) {
-            u32x2 y = {pack16<BF>(acc[t] * inv, acc[t + 1] * inv),
-                       pack16<BF>(acc[t + 2] * inv, acc[t + 3] * inv)};
+            u32x2 y = {pack16<BF>(of_sum(acc[t], inv, ll), of_sum(acc[t + 1], inv, ll)),
+                       pack16<BF>(of_sum(acc[t + 2], inv, ll), of_sum(acc[t + 3], inv, ll))};
             *(u32x2*)(dst + 2 * t) = y;
           }
           if (a.lse && (tid & 15) == 0)
@@ -606,16 +607,16 @@ __global__ __launch_bounds__(256) void decode_join_kernel(AttnArgs a) {
     s.m = mn;
   };
   auto write = [&](const State& s, int hh) {
-    float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
-    if (F8 && s.l != 0.0f) inv *= a.c.vs[kvh];
+    const float inv = (F8 ? a.c.vs[kvh] : 1.0f) / s.l;
     const int head = kvh * a.g + hbase + hh;
     char* dst = a.out + seq * a.o_row + head * a.o_head;
     if constexpr (E == 1) {
-      *(uint16_t*)(dst + 2 * lane) = (uint16_t)pack16<BF>(s.o[0] * inv, 0.0f);
+      *(uint16_t*)(dst + 2 * lane) = (uint16_t)pack16<BF>(of_sum(s.o[0], inv, s.l), 0.0f);
     } else {
 #pragma unroll
       for (int e = 0; e < E; e += 2)
-        *(uint32_t*)(dst + 2 * (lane * E + e)) = pack16<BF>(s.o[e] * inv, s.o[e + 1] * inv);
+        *(uint32_t*)(dst + 2 * (lane * E + e)) =
+            pack16<BF>(of_sum(s.o[e], inv, s.l), of_sum(s.o[e + 1], inv, s.l));
     }
     if (a.lse && lane == 0)
       a.lse[(long)seq * a.hq + head] = (s.m + (__builtin_amdgcn_logf(s.l) - kDecLift<BF>)) * kLn2;

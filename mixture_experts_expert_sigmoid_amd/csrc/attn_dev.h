@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A value of the result, of the sum l of its row's probabilities: 0 without one,
+// whatever infinities the values of keys that score -infinity left in y.
+__device__ __forceinline__ float of_sum(float y, float inv, float l) {
+  return l == 0.0f ? 0.0f : y * inv;
+}
+
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994530942f;
 

@@ -638,8 +638,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   if (parts == 1) {
     // turned round through the wave's share of LDS, so that stores take whole
     // rows; the 16-byte units of a row are swizzled by its number
-    float inv = l == 0.0f ? 0.0f : 1.0f / l;     // no visible key: 0
-    if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
+    const float inv = (F8 ? a.c.vs[kvh] : 1.0f) / l;
     constexpr int RB = 2 * D, WB = 32 * RB;
     static_assert(TB >= WB && TB <= 2 * WB, "a buffer holds one or two waves' rows");
     char* const mine =
@@ -649,8 +648,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        const u32x2 y = {pack16<BF>(o[d][i] * inv, o[d][i + 1] * inv),
-                         pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        const u32x2 y = {
+            pack16<BF>(of_sum(o[d][i], inv, l), of_sum(o[d][i + 1], inv, l)),
+            pack16<BF>(of_sum(o[d][i + 2], inv, l), of_sum(o[d][i + 3], inv, l))};
         *(u32x2*)(mine + l31 * RB + 16 * ((4 * d + (i >> 2)) ^ (l31 & (UPR - 1))) + 8 * half) = y;
       }
 #pragma unroll
@@ -736,13 +736,12 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
       }
     }
   }
-  float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (F8 && l != 0.0f) inv *= a.c.vs[kvh];
+  const float inv = (F8 ? a.c.vs[kvh] : 1.0f) / l;
   char* dst = a.out + ((long)t.q0 + tok) * a.o_row + head * a.o_head + 2 * d0;
 #pragma unroll
   for (int e = 0; e < V; e += 4) {
-    const u32x2 y = {pack16<BF>(acc[e] * inv, acc[e + 1] * inv),
-                     pack16<BF>(acc[e + 2] * inv, acc[e + 3] * inv)};
+    const u32x2 y = {pack16<BF>(of_sum(acc[e], inv, l), of_sum(acc[e + 1], inv, l)),
+                     pack16<BF>(of_sum(acc[e + 2], inv, l), of_sum(acc[e + 3], inv, l))};
     *(u32x2*)(dst + 2 * e) = y;
   }
   if (a.lse && d0 == 0) a.lse[ri] = (m + __builtin_amdgcn_logf(l)) * kLn2;

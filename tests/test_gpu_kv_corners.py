@@ -228,3 +228,28 @@ def test_free_gives_back_pages_past_the_length():
     assert (c.table[:2] == -1).all() and c.table[2, 0].item() == 11
     assert c.refs.nonzero().flatten().tolist() == [11] and c.refs[11].item() == 1
     assert M.moe_read_device_error(c.err_word) == 0
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("L,entries", [(20, 2), (3000, 200), (3000, 2100)])
+def test_only_scores_of_minus_infinity(kind, dt, L, entries):
+    """A row whose keys all score -infinity gives 0 and -infinity, whatever its
+    values are, over short and long contexts (split and joined)."""
+    D, hq = 64, 2
+    k = torch.zeros(1, 1, 16, D, dtype=DT[dt], device="cuda")
+    v = torch.ones_like(k)
+    k[..., 0] = -float("inf")
+    v[..., 5, ::2], v[..., 7, ::3] = float("inf"), float("nan")
+    cache = M.kv_cache(k, v)
+    table = M.kv_table(torch.zeros(1, entries, dtype=torch.int32, device="cuda"), _i([L]), 16, 1)
+    q = torch.ones(1 if kind == "decode" else 9, hq, D, dtype=DT[dt], device="cuda")
+    out, lse = torch.full_like(q, 3.0), torch.zeros(q.shape[:2], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    if kind == "decode":
+        M.moe_attn_decode(cache, table, q, out, 1.0, err, ws, lse=lse)
+    else:
+        M.moe_attn_prefill(cache, table, q, _i([0, 9]), out, 1.0, err, ws, lse=lse)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    assert M.moe_read_device_error(err) == 0
