@@ -152,9 +152,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const int half = lane >> 5, l31 = lane & 31;
 
   PreTile t;
-  const int kvh = blockIdx.x % a.c.hkv;
+  const int block = a.block0 + (int)blockIdx.x, kvh = block % a.c.hkv;
   // longest tiles first; sequence i's tiles start at cu[i] g / ROWS + i
-  const int tt = (int)(gridDim.x / a.c.hkv) - 1 - (int)(blockIdx.x / a.c.hkv);
+  const int tt = a.n_tiles - 1 - block / a.c.hkv;
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
   if (!pre_span<D>(a, t)) return;
@@ -688,7 +688,8 @@ template <bool BF, bool F8, int D>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   constexpr int ROWS = PreShape<D>::ROWS, V = D / 16;
   PreTile t;
-  const int kvh = blockIdx.x % a.c.hkv, tt = (int)(blockIdx.x / a.c.hkv);
+  const int block = a.block0 + (int)blockIdx.x;
+  const int kvh = block % a.c.hkv, tt = block / a.c.hkv;
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
   if (!pre_span<D>(a, t)) return;
@@ -748,14 +749,21 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
 }
 
 template <bool BF, bool F8, int D>
-hipError_t run_prefill(const AttnArgs& a, hipStream_t s) {
-  const long tiles = prefill_tiles(a.n, a.T, a.g);
-  attn_prefill_kernel<BF, F8, D>
-      <<<dim3((unsigned)(tiles * a.c.hkv), a.n_split), 256, 0, s>>>(a);
-  if (a.n_split > 1)
-    prefill_join_kernel<BF, F8, D>
-        <<<dim3((unsigned)(tiles * a.c.hkv), PreShape<D>::ROWS / 16), 256, 0, s>>>(a);
-  return hipGetLastError();
+hipError_t run_prefill(const AttnArgs& all, hipStream_t s) {
+  AttnArgs a = all;
+  a.n_tiles = (int)prefill_tiles(a.n, a.T, a.g);
+  const long blocks = (long)a.n_tiles * a.c.hkv;
+  for (long b = 0; b < blocks; b += kMaxGrid) {
+    const unsigned grid = (unsigned)(blocks - b < kMaxGrid ? blocks - b : kMaxGrid);
+    a.block0 = (int)b;
+    attn_prefill_kernel<BF, F8, D><<<dim3(grid, a.n_split), 256, 0, s>>>(a);
+    if (a.n_split > 1)
+      prefill_join_kernel<BF, F8, D>
+          <<<dim3(grid, PreShape<D>::ROWS / 16), 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int D>

@@ -50,6 +50,8 @@ struct AttnArgs {
   long T;
   int n_split;
   float split_gain;      // see pre_parts
+  int n_tiles;           // of a key-value head
+  int block0;            // first of all workgroups that this launch runs
   // decode: every pair is one team's
   int whole;
   // partial results of split rows
@@ -105,6 +107,11 @@ int prefill_splits(long n, long T, int hq, int hkv);
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 
+// Workgroups of 256 threads in one launch: a grid has fewer than 2^32 threads.
+// Calls that need more (a list of a million sequences and many heads, rows by
+// the hundred million) take several launches.
+constexpr long kMaxGrid = 1L << 23;
+
 struct AppendArgs {
   KvCache c;
   KvTable t;
@@ -117,6 +124,7 @@ struct AppendArgs {
   const char* v;
   long k_row, k_head, v_row, v_head;    // bytes
   int* err;
+  long row0;             // first row that this launch takes
 };
 hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s);
 

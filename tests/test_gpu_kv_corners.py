@@ -253,3 +253,30 @@ def test_only_scores_of_minus_infinity(kind, dt, L, entries):
         M.moe_attn_prefill(cache, table, q, _i([0, 9]), out, 1.0, err, ws, lse=lse)
     assert (out == 0).all() and (lse == -float("inf")).all()
     assert M.moe_read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("first", [0, 1 << 19, (1 << 20) - 4])
+def test_prefill_over_a_list_of_a_million(first):
+    """More workgroups than one launch takes: 2^20 - 1 list entries, all but
+    three of them empty, over 16 key-value heads."""
+    n, hkv, D = (1 << 20) - 1, 16, 64
+    rng = np.random.default_rng(23)
+    pool = Pool(rng, kv="bf16", hkv=hkv, D=D, ps=16, lens=[40, 7, 100])
+    rows = [20, 7, 30]
+    q = _q(rng, sum(rows), hkv, D, "bf16")
+    want = _reference(pool, [0, 1, 2], rows, q, hkv, 0, 0, 0.125, "bf16")
+    slots = torch.full((n,), -1, dtype=torch.int32)
+    slots[first:first + 3] = torch.tensor([0, 1, 2])
+    m = torch.zeros(n, dtype=torch.int64)
+    m[first:first + 3] = torch.tensor(rows)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), m.cumsum(0)]).int().cuda()
+    cache, table = pool.desc(M)
+    qd = torch.from_numpy(q).to("cuda", torch.bfloat16)
+    out, lse = torch.full_like(qd, 7.0), torch.full(qd.shape[:2], 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(16, M.moe_attn_prefill_workspace_size(cache, n, sum(rows), hkv)),
+                     dtype=torch.uint8, device="cuda")
+    M.moe_attn_prefill(cache, table, qd, cu, out, 0.125, err, ws, slots=slots.cuda(), lse=lse)
+    assert M.moe_read_device_error(err) == 0
+    check(out.double().cpu().numpy(), want[0], want[2], "out")
+    check(lse.double().cpu().numpy(), want[1], want[3], "lse")
