@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
   const int lg = __builtin_ctz(upr);
   const int per = 2 * a.c.hkv * upr;              // units per token
   const int tid = threadIdx.x;
-  const long r0 = (long)blockIdx.x * rows;
+  const long r0 = a.row0 + (long)blockIdx.x * rows;
   const int nr = (int)min((long)rows, a.T - r0);
 
   // unit x of row `row`, 256 units on a time
@@ -177,15 +177,21 @@ hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s) {
   // a row a workgroup as long as there are few, so that single tokens spread
   // over the CUs; more of them share one lookup's latency for prompts
   const int rows = (int)(a.T >= 1024 * kMaxRows ? kMaxRows : a.T < 2048 ? 1 : a.T / 1024);
-  const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
   const bool q = a.c.fmt == KV_E4M3;
-  if (!q)
-    append_kernel<KV_BF16, false><<<grid, 256, 0, s>>>(a, rows);   // bits only, either type
-  else if (fmt == KV_BF16)
-    append_kernel<KV_BF16, true><<<grid, 256, 0, s>>>(a, rows);
-  else
-    append_kernel<KV_F16, true><<<grid, 256, 0, s>>>(a, rows);
-  return hipGetLastError();
+  AppendArgs p = a;
+  for (p.row0 = 0; p.row0 < a.T; p.row0 += kMaxGrid * rows) {
+    const long left = (a.T - p.row0 + rows - 1) / rows;
+    const unsigned grid = (unsigned)(left < kMaxGrid ? left : kMaxGrid);
+    if (!q)
+      append_kernel<KV_BF16, false><<<grid, 256, 0, s>>>(p, rows);   // bits only, either type
+    else if (fmt == KV_BF16)
+      append_kernel<KV_BF16, true><<<grid, 256, 0, s>>>(p, rows);
+    else
+      append_kernel<KV_F16, true><<<grid, 256, 0, s>>>(p, rows);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

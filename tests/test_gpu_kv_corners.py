@@ -280,3 +280,32 @@ def test_prefill_over_a_list_of_a_million(first):
     assert M.moe_read_device_error(err) == 0
     check(out.double().cpu().numpy(), want[0], want[2], "out")
     check(lse.double().cpu().numpy(), want[1], want[3], "lse")
+
+
+def test_append_of_more_rows_than_one_launch_takes():
+    """2^27 + 5 rows of 64 values, of which the last three and three around each
+    multiple of 2^26 have a place; the others' start is negative."""
+    T, D, ps = (1 << 27) + 5, 64, 16
+    if torch.cuda.mem_get_info()[0] < 3 * T * D * 2:
+        pytest.skip("needs 52 GB of free memory")
+    x = torch.empty(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    at = [(1 << 26) - 2, (1 << 27) - 2, T - 3]
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    new = torch.randn(9, 1, D, generator=gen, device="cuda").bfloat16()
+    cu, start = [0], []
+    for i, a in enumerate(at):
+        x[a:a + 3] = new[3 * i:3 * i + 3]
+        cu += [a, a + 3]
+        start += [-1, 2 * i]
+    if cu[-1] < T:
+        cu.append(T), start.append(-1)
+    k, v = (torch.zeros(6, 1, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = [0, 1, 2, 3, 4, 5][:len(start)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    M.moe_cache_append(M.kv_cache(k, v), M.kv_table(_i([[s] for s in range(6)]), _i([0] * 6), ps, 6),
+                       _i(start), _i(cu), x, x, err, slots=_i(slots))
+    want = torch.zeros_like(k)
+    for i in range(3):
+        want[2 * i + 1, 0, 2 * i:2 * i + 3] = new[3 * i:3 * i + 3, 0]
+    assert M.moe_read_device_error(err) == 0
+    assert torch.equal(k, want) and torch.equal(v, want)
