@@ -564,8 +564,9 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * MOE_DEVERR_CACHE_PAGE. No dst occurs twice or is also a src.
  *
  * layers: host array of n_layers (1..1024) caches alike in all but their
- * pointers and scales. Workspace: moe_cache_workspace_size(table, n) bytes
- * serves grow, fork and compact for up to n slots. */
+ * pointers and scales. Limits: 0 <= n < 2^20, for fork 0 <= n <= 65535, for
+ * copy_pages 0 <= n < 2^31. Workspace: moe_cache_workspace_size(table, n)
+ * bytes, 16-byte aligned, serve grow, fork and compact for up to n slots. */
 int moe_cache_grow(const moe_kv_table *table, const int *slots,
                    const int *n_new, long n, int *start, int *err_word,
                    void *ws, size_t ws_bytes, void *stream);

@@ -268,7 +268,8 @@ int moe_cache_grow(const moe_kv_table* table, const int* slots, const int* n_new
   if (!err_word) return MOE_ERR_NULL;
   if (n == 0) return MOE_OK;
   if (!n_new || !start) return MOE_ERR_NULL;
-  if (!ws || ws_bytes < moe::cache_ws_bytes(table->n_pages, n)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < moe::cache_ws_bytes(table->n_pages, n) || ((uintptr_t)ws & 15))
+    return MOE_ERR_WORKSPACE;
   return done(moe::launch_cache_grow(dev_table(table), slots, n_new, n, start, err_word, ws,
                                      (hipStream_t)stream),
               "moe_cache_grow");

@@ -90,3 +90,12 @@ def test_error_words_and_workspaces_of_a_wrong_kind():
             with pytest.raises(M.MoeError) as e:
                 call(**kw)
             assert e.value.status == -2, (i, bad)
+
+
+@needs_lib
+def test_upkeep_workspaces_are_aligned():
+    L, t, c = M.lib(), _t(), _c()
+    big, at = 1 << 40, 264                       # not a multiple of 16
+    assert L.moe_cache_grow(t, 256, 256, 4, 256, 256, at, big, None) == -6
+    assert L.moe_cache_fork((M.MoeKvCache * 1)(c), 1, t, 256, 256, 4, 256, at, big, None) == -6
+    assert L.moe_cache_compact((M.MoeKvCache * 1)(c), 1, t, None, 256, at, big, None) == -6
