@@ -434,19 +434,24 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] =
     of bfloat16, float16 or float8_e4m3fn (with scales [heads] fp32), of any
     strides alike in both but with rows of head_dim contiguous; a cache laid
     out [pages][page_size][heads][head_dim] is passed as its transpose(1, 2)."""
-    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4:
-        raise MoeError(-2, "kv_cache", "k and v differ in shape, strides or type")
-    if k.stride(3) != 1:
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4:
+        raise MoeError(-2, "kv_cache", "k and v differ in shape or type")
+    P, H, ps, D = k.shape
+    # a dimension of one entry has no stride of its own: one that a dense cache
+    # would have stands for it
+    strides = [(x.stride(0) if P > 1 else H * ps * D, x.stride(1) if H > 1 else D, x.stride(2),
+                x.stride(3)) for x in (k, v)]
+    if strides[0] != strides[1]:
+        raise MoeError(-2, "kv_cache", "k and v differ in strides")
+    if strides[0][3] != 1:
         raise MoeError(-2, "kv_cache", "rows of head_dim are not contiguous")
     for sc in (k_scale, v_scale):
         if sc is not None and (sc.dtype != torch.float32 or sc.numel() != k.shape[1]
                                or not sc.is_contiguous()):
             raise MoeError(-2, "kv_cache", "scales are fp32 [heads]")
     _on_gpu("kv_cache", k, v, k_scale, v_scale)
-    P, H, ps, D = k.shape
-    c = MoeKvCache(_kv_fmt(k, "kv_cache"), P, ps, H, D, k.stride(0), k.stride(1), k.stride(2),
-                   k.data_ptr(), v.data_ptr(),
-                   None if k_scale is None else k_scale.data_ptr(),
+    c = MoeKvCache(_kv_fmt(k, "kv_cache"), P, ps, H, D, *strides[0][:3], k.data_ptr(),
+                   v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
                    None if v_scale is None else v_scale.data_ptr())
     c._keep = (k, v, k_scale, v_scale)
     return c

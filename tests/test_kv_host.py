@@ -99,3 +99,26 @@ def test_upkeep_workspaces_are_aligned():
     assert L.moe_cache_grow(t, 256, 256, 4, 256, 256, at, big, None) == -6
     assert L.moe_cache_fork((M.MoeKvCache * 1)(c), 1, t, 256, 256, 4, 256, at, big, None) == -6
     assert L.moe_cache_compact((M.MoeKvCache * 1)(c), 1, t, None, 256, at, big, None) == -6
+
+
+def test_dimensions_of_one_entry_have_no_stride():
+    """One head, or one page, of a cache: k and v that differ only in strides
+    that address nothing, or have such below head_dim, are the same layout."""
+    b = torch.bfloat16
+    k = torch.zeros(6, 16, 64, dtype=b).unsqueeze(1)                # stride(1) = 1024
+    v = torch.zeros(6, 16, 1, 64, dtype=b).transpose(1, 2)          # stride(1) = 64
+    assert k.stride() != v.stride()
+    small = torch.zeros(6 * 1024, dtype=b).as_strided((6, 1, 16, 64), (1024, 1, 64, 1))
+    for pair in ((k, v), (v, k), (small, v)):
+        c = M.kv_cache(*(x.as_subclass(_OnGpu) for x in pair))
+        assert (c.stride_page, c.stride_tok, c.n_heads) == (1024, 64, 1)
+        assert c.stride_head >= 64 and c.stride_head % 8 == 0
+    one = torch.zeros(2 * 1024, dtype=b).as_strided((1, 2, 16, 64), (1, 1024, 64, 1))
+    c = M.kv_cache(one.as_subclass(_OnGpu), torch.zeros(1, 2, 16, 64, dtype=b).as_subclass(_OnGpu))
+    assert c.stride_page >= 64 and c.stride_page % 8 == 0
+    assert (c.stride_head, c.stride_tok) == (1024, 64)
+    k = torch.zeros(6, 2, 16, 64, dtype=b)
+    for v in (torch.zeros(6, 2, 17, 64, dtype=b)[:, :, :16],
+              torch.zeros(6, 16, 2, 64, dtype=b).transpose(1, 2)):
+        with pytest.raises(M.MoeError):
+            M.kv_cache(k, v)
