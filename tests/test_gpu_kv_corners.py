@@ -302,8 +302,8 @@ def test_append_of_more_rows_than_one_launch_takes():
     k, v = (torch.zeros(6, 1, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     slots = [0, 1, 2, 3, 4, 5][:len(start)]
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    M.moe_cache_append(M.kv_cache(k, v), M.kv_table(_i([[s] for s in range(6)]), _i([0] * 6), ps, 6),
-                       _i(start), _i(cu), x, x, err, slots=_i(slots))
+    table = M.kv_table(_i([[s] for s in range(6)]), _i([0] * 6), ps, 6)
+    M.moe_cache_append(M.kv_cache(k, v), table, _i(start), _i(cu), x, x, err, slots=_i(slots))
     want = torch.zeros_like(k)
     for i in range(3):
         want[2 * i + 1, 0, 2 * i:2 * i + 3] = new[3 * i:3 * i + 3, 0]
