@@ -465,7 +465,8 @@ typedef struct {
  * lse = -infinity. What lies in masked places, infinities and NaN included,
  * does not enter. Products accumulate in fp32, the softmax statistics are
  * fp32; the probabilities enter the second product in the type of q, all
- * those from 2^-26 of the largest on with its full precision. */
+ * those from 2^-26 of the largest on with its full precision (prompts in f16:
+ * for scores up to 1.8e5). */
 typedef struct {
   int fmt;             /* MOE_KV_BF16 or MOE_KV_F16: q and out; a cache that
                           is not MOE_KV_E4M3 has the same fmt */

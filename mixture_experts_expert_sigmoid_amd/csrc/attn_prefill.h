@@ -3,9 +3,12 @@
 //
 // Mathematics. One pass over the keys with the running maximum and sum of a
 // softmax: S^T = K Q^T, P = 2^(S - m), O^T = V^T P^T, all in fp32 but the
-// 16-bit operands. The rows of a tile are (token, query head) pairs of one
-// key-value head, token-major, so the heads that share keys share the tile:
-// a tile spans few positions, and a short chunk still fills it.
+// 16-bit operands. P is one of them (the matrix instructions take no wider one
+// at their rate): that rounding is of the size of the result's own, and results
+// stand 13-35 % further from the 64-bit values than with P of 32 bits. The rows
+// of a tile are (token, query head) pairs of one key-value head, token-major, so
+// the heads that share keys share the tile: a tile spans few positions, and a
+// short chunk still fills it.
 //
 // Layout. Four waves of 32 rows, v_mfma_*_32x32x16. A row lies in a lane's
 // column of S^T (lane l: row l % 32, 16 of 32 keys), so the softmax
@@ -27,11 +30,11 @@
 // Bound: the matrix cores and the exponentials for long prompts; latency for
 // short ones. Few tiles: the keys of each are split over workgroups and the
 // parts joined in order. Measured: a causal prompt of 11999 tokens, 32 heads
-// of 128 over 8 (bf16) 1.09-1.13 ms, 1.05-1.08 PFLOP/s (a large library
+// of 128 over 8 (bf16) 1.07-1.10 ms, 1.08-1.10 PFLOP/s (a large library
 // product: 1.25); 6000 tokens of head_dim 64 860, of 256 760 TFLOP/s; two
-// chunks of 500 tokens over 16..24 k e4m3 keys 410-418 us, 0.9 PFLOP/s; seven
-// prompts of 130..3001 tokens, window 512, head_dim 64 (f16) 84 us; a prompt of
-// 37 tokens 8.1 us. A wave by itself on its SIMD takes 1.15 us for 64 keys of
+// chunks of 500 tokens over 16..24 k e4m3 keys 406-411 us, 0.9 PFLOP/s; seven
+// prompts of 130..3001 tokens, window 512, head_dim 64 (f16) 85 us; a prompt of
+// 37 tokens 8.2 us. A wave by itself on its SIMD takes 1.15 us for 64 keys of
 // head_dim 128, two 1.1 us for both: loads further ahead (four buffers) gained
 // nothing, so that is the wave's own chain of reads, products and softmax.
 #pragma once

@@ -4,8 +4,9 @@
 // are on their way, then all quantise (e4m3 caches) and store. Bound by HBM
 // for prompts (input read once, codes written once), by latency and launch for
 // single tokens. Measured: 8 prompts of 500..8001 tokens, 8 heads of 128, into
-// e4m3 (223 MB) 61 us, 3.6 TB/s (a large copy: 4.8); a token of each of 64
-// sequences 6.9 us a call, 4.1 us of it the kernel. 8 rows a workgroup and 4
+// e4m3 (223 MB) 62 us, 3.6 TB/s (a large copy: 4.8), into bf16 (297 MB) 65 us,
+// 4.6 TB/s; a token of each of 64 sequences 6.8 us a call, 4.2 us of it the
+// kernel. 8 rows a workgroup and 4
 // loads in flight: 16 rows, 4 rows, 8 or 2 loads were all slower (8: 67 us).
 #include "common.h"
 #include "kv.h"
