@@ -34,7 +34,7 @@
 // product: 1.25); 6000 tokens of head_dim 64 860, of 256 760 TFLOP/s; two
 // chunks of 500 tokens over 16..24 k e4m3 keys 406-411 us, 0.9 PFLOP/s; seven
 // prompts of 130..3001 tokens, window 512, head_dim 64 (f16) 85 us; a prompt of
-// 37 tokens 8.2 us. A wave by itself on its SIMD takes 1.15 us for 64 keys of
+// 37 tokens 8.1 us. A wave by itself on its SIMD takes 1.15 us for 64 keys of
 // head_dim 128, two 1.1 us for both: loads further ahead (four buffers) gained
 // nothing, so that is the wave's own chain of reads, products and softmax.
 #pragma once
@@ -641,7 +641,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   if (parts == 1) {
     // turned round through the wave's share of LDS, so that stores take whole
     // rows; the 16-byte units of a row are swizzled by its number
-    const float inv = (F8 ? a.c.vs[kvh] : 1.0f) / l;
+    const float inv = l == 0.0f ? 0.0f : (F8 ? a.c.vs[kvh] : 1.0f) / l;
+    if (__any(me.have && l == 0.0f)) {           // see of_sum; rare, so not a select in all rows
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = of_sum(o[d][i], 1.0f, l);
+    }
     constexpr int RB = 2 * D, WB = 32 * RB;
     static_assert(TB >= WB && TB <= 2 * WB, "a buffer holds one or two waves' rows");
     char* const mine =
@@ -651,9 +657,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        const u32x2 y = {
-            pack16<BF>(of_sum(o[d][i], inv, l), of_sum(o[d][i + 1], inv, l)),
-            pack16<BF>(of_sum(o[d][i + 2], inv, l), of_sum(o[d][i + 3], inv, l))};
+        const u32x2 y = {pack16<BF>(o[d][i] * inv, o[d][i + 1] * inv),
+                         pack16<BF>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
         *(u32x2*)(mine + l31 * RB + 16 * ((4 * d + (i >> 2)) ^ (l31 & (UPR - 1))) + 8 * half) = y;
       }
 #pragma unroll
