@@ -450,8 +450,15 @@ typedef struct {
                                       that slot as empty) */
 #define MOE_DEVERR_CACHE_FULL 0x10 /* grow or fork: not enough free pages or
                                       table entries for a slot, left as it was */
-#define MOE_DEVERR_CACHE_BUSY 0x20 /* fork into a slot that holds tokens, left
-                                      as it was */
+#define MOE_DEVERR_CACHE_BUSY 0x20 /* fork into a slot that holds tokens, keep
+                                      in a page of several slots: left as it
+                                      was */
+#define MOE_DEVERR_TREE 0x40       /* a drafted token whose parent does not come
+                                      before it (taken as a child of the
+                                      context), a tree of more than
+                                      MOE_TREE_MAX tokens (its rows give 0 and
+                                      -infinity), or an accepted path that is
+                                      none (that slot left as it was) */
 
 /* Queries, outputs and mask of an attention call. Row r of q belongs to
  * position p of its sequence (see the entry points), query head h to
@@ -515,6 +522,27 @@ int moe_attn_prefill(const moe_kv_cache *cache, const moe_kv_table *table,
 size_t moe_attn_prefill_workspace_size(const moe_kv_cache *cache, long n,
                                        long T, int n_heads);
 
+/* Attention of drafted tokens that form a tree behind the context of each
+ * sequence. As moe_attn_prefill: rows cu_q[i] .. cu_q[i + 1] - 1 of q are the
+ * last m tokens of slot s = slots[i], at most MOE_TREE_MAX of them, their keys
+ * and values in the cache already. parent[r] (device int32 [T]) is row r's
+ * parent as an index among its sequence's rows, before its own (0 .. t - 1 for
+ * the t-th row), or -1: a child of the context. Row t sees, of the C = len[s] -
+ * m tokens before, all, and of the drafted ones itself and its ancestors. The
+ * position of a drafted token is C + the number of its ancestors: with a
+ * window the key at position p is visible to the row at position p' iff
+ * p' - p < window or p < n_first. A sequence with len[s] < m gives 0 and
+ * -infinity. After the verdict over the tree: moe_cache_keep. Workspace:
+ * moe_attn_tree_workspace_size(cache, n, T, n_heads) bytes. Errors as for
+ * moe_attn_decode. */
+#define MOE_TREE_MAX 256
+int moe_attn_tree(const moe_kv_cache *cache, const moe_kv_table *table,
+                  const int *slots, long n, const int *cu_q, long T,
+                  const int *parent, const moe_attn *attn, int *err_word,
+                  void *ws, size_t ws_bytes, void *stream);
+size_t moe_attn_tree_workspace_size(const moe_kv_cache *cache, long n, long T,
+                                    int n_heads);
+
 /* Writes new keys and values: rows cu[i] .. cu[i + 1] - 1 of k and v (device
  * int32 [n + 1]; NULL: one row each, T = n) go to positions start[i],
  * start[i] + 1, ... of slot slots[i] (NULL: i). Nothing is written for a
@@ -560,12 +588,22 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * moves to the i-th free page below U; refs and every table entry follow.
  * n_used[0] = U (device int32, NULL allowed).
  *
+ * moe_cache_keep keeps the accepted path of each tree of drafted tokens
+ * (moe_attn_tree): of the n_draft[i] newest tokens of slots[i] (NULL: i), those
+ * at path[cu[i]] .. path[cu[i + 1] - 1] among them (device int32 [n_path];
+ * ascending, as a path from the context down is) become the next ones behind
+ * the context, in every layer; the slot's length follows, and pages left
+ * without tokens go back. An entry that is no such path leaves its slot as it
+ * was, with MOE_DEVERR_TREE; so does one that would write into a page of
+ * another slot too, with MOE_DEVERR_CACHE_BUSY. cu: device int32 [n + 1],
+ * within 0..n_path.
+ *
  * moe_cache_copy_pages copies page src[i] to page dst[i], in every layer;
  * entries < 0 are skipped, entries >= n_pages too, with
  * MOE_DEVERR_CACHE_PAGE. No dst occurs twice or is also a src.
  *
  * layers: host array of n_layers (1..1024) caches alike in all but their
- * pointers and scales. Limits: 0 <= n < 2^20, for fork 0 <= n <= 65535, for
+ * pointers and scales; a cache whose v is its k has one array. Limits: 0 <= n < 2^20, for fork 0 <= n <= 65535, for
  * copy_pages 0 <= n < 2^31. Workspace: moe_cache_workspace_size(table, n)
  * bytes, 16-byte aligned, serve grow, fork and compact for up to n slots. */
 int moe_cache_grow(const moe_kv_table *table, const int *slots,
@@ -582,10 +620,50 @@ int moe_cache_fork(const moe_kv_cache *layers, int n_layers,
 int moe_cache_compact(const moe_kv_cache *layers, int n_layers,
                       const moe_kv_table *table, int *n_used, int *err_word,
                       void *ws, size_t ws_bytes, void *stream);
+int moe_cache_keep(const moe_kv_cache *layers, int n_layers,
+                   const moe_kv_table *table, const int *slots,
+                   const int *n_draft, const int *cu, const int *path,
+                   long n_path, long n, int *err_word, void *stream);
 int moe_cache_copy_pages(const moe_kv_cache *layers, int n_layers,
                          const int *src, const int *dst, long n, int *err_word,
                          void *stream);
 size_t moe_cache_workspace_size(const moe_kv_table *table, long n);
+
+/* ------------------------------------------------------- latent attention -- */
+/* Attention whose keys and values are one latent vector a token, shared by all
+ * query heads: with c_j the latent vector of token j (latent_dim values) and
+ * r_j its rotary key (rope_dim values), head h's key is [Wk_h c_j, r_j] and its
+ * value Wv_h c_j. A cache keeps c_j and r_j alone, in one array of pages: value
+ * d of token i of page p lies at element p * stride_page + i * stride_tok + d,
+ * the rotary values behind the latent ones. Its tables are moe_kv_table; grow,
+ * free and trim take them as they are, fork, compact, keep and copy_pages
+ * take the array as moe_latent_pages describes it. */
+typedef struct {
+  int fmt;             /* moe_kv_fmt */
+  int n_pages;         /* >= 1 */
+  int page_size;       /* a multiple of 16, 16..4096 */
+  int latent_dim;      /* 256 or 512 */
+  int rope_dim;        /* 64 */
+  long stride_page, stride_tok;   /* elements; multiples of 16 bytes, at least
+                          latent_dim + rope_dim; stride_tok * 16 elements under
+                          2^30 bytes */
+  void *c;             /* 16-byte aligned */
+  const float *scale;  /* device fp32 [1], value = code * scale; MOE_KV_E4M3
+                          only (NULL otherwise) */
+} moe_latent_cache;
+
+/* The cache as the calls that move pages take it: heads of 64 values and no
+ * second array (v = k). Not for attention or append. */
+int moe_latent_pages(const moe_latent_cache *cache, moe_kv_cache *pages);
+
+/* Writes new tokens, as moe_cache_append: rows of c [T][latent_dim] and of rope
+ * [T][rope_dim], of type fmt, strides of their rows in elements, multiples of
+ * 8. */
+int moe_latent_append(const moe_latent_cache *cache, const moe_kv_table *table,
+                      const int *slots, const int *start, const int *cu, long n,
+                      long T, int fmt, const void *c, long c_stride_row,
+                      const void *rope, long rope_stride_row, int *err_word,
+                      void *stream);
 
 /* --------------------------------------------------------------- misc -- */
 /* Synchronises `stream`, then copies *err_word (device) to *host_bits. */

@@ -33,6 +33,8 @@ MOE_DEVERR_W4_SCALE = 0x4
 MOE_DEVERR_CACHE_PAGE = 0x8
 MOE_DEVERR_CACHE_FULL = 0x10
 MOE_DEVERR_CACHE_BUSY = 0x20
+MOE_DEVERR_TREE = 0x40
+MOE_TREE_MAX = 256
 MOE_KV_BF16, MOE_KV_F16, MOE_KV_E4M3 = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE",
           -3: "MOE_ERR_FORMAT", -4: "MOE_ERR_LOCAL_RANGE", -5: "MOE_ERR_PARAM",
@@ -76,6 +78,12 @@ class MoeKvCache(ctypes.Structure):
                 ("n_heads", c_int), ("head_dim", c_int), ("stride_page", c_long),
                 ("stride_head", c_long), ("stride_tok", c_long), ("k", c_void_p),
                 ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class MoeLatentCache(ctypes.Structure):
+    _fields_ = [("fmt", c_int), ("n_pages", c_int), ("page_size", c_int),
+                ("latent_dim", c_int), ("rope_dim", c_int), ("stride_page", c_long),
+                ("stride_tok", c_long), ("c", c_void_p), ("scale", c_void_p)]
 
 
 class MoeKvTable(ctypes.Structure):
@@ -143,6 +151,10 @@ _SIGS = {
                                  c_size_t, c_void_p]),
     "moe_attn_prefill_workspace_size": (c_size_t, [POINTER(MoeKvCache), c_long, c_long,
                                                    c_int]),
+    "moe_attn_tree": (c_int, [POINTER(MoeKvCache), POINTER(MoeKvTable), c_void_p, c_long,
+                              c_void_p, c_long, c_void_p, POINTER(MoeAttn), c_void_p, c_void_p,
+                              c_size_t, c_void_p]),
+    "moe_attn_tree_workspace_size": (c_size_t, [POINTER(MoeKvCache), c_long, c_long, c_int]),
     "moe_cache_append": (c_int, [POINTER(MoeKvCache), POINTER(MoeKvTable), c_void_p,
                                  c_void_p, c_void_p, c_long, c_long, c_int, c_void_p,
                                  c_long, c_long, c_void_p, c_long, c_long, c_void_p,
@@ -158,7 +170,14 @@ _SIGS = {
                                   c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_cache_copy_pages": (c_int, [POINTER(MoeKvCache), c_int, c_void_p, c_void_p, c_long,
                                      c_void_p, c_void_p]),
+    "moe_cache_keep": (c_int, [POINTER(MoeKvCache), c_int, POINTER(MoeKvTable), c_void_p,
+                               c_void_p, c_void_p, c_void_p, c_long, c_long, c_void_p,
+                               c_void_p]),
     "moe_cache_workspace_size": (c_size_t, [POINTER(MoeKvTable), c_long]),
+    "moe_latent_pages": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvCache)]),
+    "moe_latent_append": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvTable), c_void_p,
+                                  c_void_p, c_void_p, c_long, c_long, c_int, c_void_p, c_long,
+                                  c_void_p, c_long, c_void_p, c_void_p]),
     "moe_read_device_error": (c_int, [c_void_p, POINTER(c_int), c_void_p]),
     "moe_status_string": (ctypes.c_char_p, [c_int]),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -533,6 +552,25 @@ def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, 
                                   *_work(ws, where), _stream(stream)), where)
 
 
+def moe_attn_tree_workspace_size(cache: MoeKvCache, n: int, T: int, n_heads: int) -> int:
+    return lib().moe_attn_tree_workspace_size(cache, n, T, n_heads)
+
+
+def moe_attn_tree(cache: MoeKvCache, table: MoeKvTable, q, cu_q, parent, out, scale, err_word,
+                  ws, *, window=0, n_first=0, slots=None, lse=None, stream=None):
+    """Drafted tokens that form a tree behind the context of each of n =
+    len(cu_q) - 1 sequences: q and out [T][heads][head_dim], lse [T][heads],
+    parent int32 [T], among the sequence's own rows, -1 for a child of the
+    context."""
+    where = "moe_attn_tree"
+    shape = q.shape
+    a = _attn(where, cache, shape, q, out, scale, window, n_first, lse)
+    n = cu_q.numel() - 1
+    _check(lib().moe_attn_tree(cache, table, _i32(slots, n, where), n, _i32(cu_q, 1, where),
+                               shape[0], _i32(parent, shape[0], where), a,
+                               _err(err_word, where), *_work(ws, where), _stream(stream)), where)
+
+
 def moe_cache_append(cache: MoeKvCache, table: MoeKvTable, start, cu, k, v, err_word, *,
                      slots=None, stream=None):
     """k and v [T][heads][head_dim] to positions start[i].. of the slots; cu int32
@@ -604,6 +642,72 @@ def moe_cache_copy_pages(caches, src, dst, err_word, stream=None):
     _check(lib().moe_cache_copy_pages(_layers(caches), len(caches), _i32(src, n, where),
                                       _i32(dst, n, where), n, _err(err_word, where),
                                       _stream(stream)), where)
+
+
+def moe_cache_keep(caches, table: MoeKvTable, n_draft, cu, path, err_word, *, slots=None,
+                   stream=None):
+    """The accepted path of each tree: entries cu[i] .. cu[i + 1] - 1 of path, among
+    the n_draft[i] newest tokens of the slot."""
+    where = "moe_cache_keep"
+    n = n_draft.numel()
+    _check(lib().moe_cache_keep(_layers(caches), len(caches), table, _i32(slots, n, where),
+                                _i32(n_draft, n, where), _i32(cu, n + 1, where),
+                                _i32(path, 0, where), path.numel(), n, _err(err_word, where),
+                                _stream(stream)), where)
+
+
+# -------------------------------------------------------- latent attention
+
+def latent_cache(c: torch.Tensor, latent_dim: int,
+                 scale: Optional[torch.Tensor] = None) -> MoeLatentCache:
+    """Descriptor of one layer's latent cache: c [pages][page_size][latent_dim +
+    rope_dim] of bfloat16, float16 or float8_e4m3fn (with scale [1] fp32), rows
+    contiguous."""
+    where = "latent_cache"
+    if c.dim() != 3 or c.stride(2) != 1 or latent_dim > c.shape[2]:
+        raise MoeError(-2, where, "c is [pages][page_size][latent + rotary], rows contiguous")
+    if scale is not None and (scale.dtype != torch.float32 or scale.numel() != 1):
+        raise MoeError(-2, where, "the scale is fp32 [1]")
+    _on_gpu(where, c, scale)
+    P, ps, D = c.shape
+    d = MoeLatentCache(_kv_fmt(c, where), P, ps, latent_dim, D - latent_dim,
+                       c.stride(0) if P > 1 else ps * D, c.stride(1), c.data_ptr(),
+                       None if scale is None else scale.data_ptr())
+    d._keep = (c, scale)
+    return d
+
+
+def moe_latent_pages(cache: MoeLatentCache) -> MoeKvCache:
+    """The cache as moe_cache_fork, compact, keep and copy_pages take it."""
+    pages = MoeKvCache()
+    _check(lib().moe_latent_pages(cache, pages), "moe_latent_pages")
+    pages._keep = getattr(cache, "_keep", None)
+    return pages
+
+
+def _flat(t: torch.Tensor, where: str, T: int, D: int):
+    """Stride of the rows of a [T][D] tensor."""
+    if t.dim() != 2 or t.shape != (T, D) or t.stride(1) != 1:
+        raise MoeError(-2, where, f"wants {(T, D)} with contiguous rows, got {tuple(t.shape)} "
+                                  f"strides {t.stride()}")
+    if not t.is_cuda:
+        _on_gpu(where, t)
+    return t.stride(0) if T > 1 else D
+
+
+def moe_latent_append(cache: MoeLatentCache, table: MoeKvTable, start, cu, c, rope, err_word, *,
+                      slots=None, stream=None):
+    """c [T][latent_dim] and rope [T][rope_dim] to positions start[i].. of the slots;
+    cu int32 [n + 1], or None for one token each."""
+    where = "moe_latent_append"
+    T = c.shape[0]
+    n = T if cu is None else cu.numel() - 1
+    if rope.dtype is not c.dtype:
+        raise MoeError(-2, where, "c and rope differ in type")
+    cs, rs = _flat(c, where, T, cache.latent_dim), _flat(rope, where, T, cache.rope_dim)
+    _check(lib().moe_latent_append(
+        cache, table, _i32(slots, n, where), _i32(start, n, where), _i32(cu, 1, where), n, T,
+        _kv_fmt(c, where), _p(c), cs, _p(rope), rs, _err(err_word, where), _stream(stream)), where)
 
 
 class _Workspace:
@@ -725,6 +829,23 @@ class KvCache:
     def compact(self, n_used=None, stream=None):
         ws = self.workspace(moe_cache_workspace_size(self.desc, 0), stream)
         moe_cache_compact(self.layers, self.desc, n_used, self.err_word, ws, stream)
+
+    def tree(self, layer, slots, q, cu_q, parent, scale, out=None, window=0, n_first=0, lse=None,
+             stream=None):
+        """The newest tokens as drafted trees: parent int32 [T]."""
+        out = self._new(q, stream) if out is None else out
+        c = self.layers[layer]
+        ws = self.workspace(moe_attn_tree_workspace_size(c, cu_q.numel() - 1, q.shape[0],
+                                                         q.shape[1]), stream)
+        moe_attn_tree(c, self.desc, q, cu_q, parent, out, scale, self.err_word, ws,
+                      window=window, n_first=n_first, slots=slots, lse=lse, stream=stream)
+        return out
+
+    def keep(self, slots, n_draft, cu, path, stream=None):
+        """The accepted paths of the trees; the rest of them is given back."""
+        self._on(stream)
+        moe_cache_keep(self.layers, self.desc, n_draft, cu, path, self.err_word, slots=slots,
+                       stream=stream)
 
 
 # ------------------------------------------------------------ layer object

@@ -10,6 +10,9 @@ hipError_t launch_decode_256(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_64(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_tree_64(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_tree_128(const AttnArgs& a, int fmt, hipStream_t s);
+hipError_t launch_tree_256(const AttnArgs& a, int fmt, hipStream_t s);
 
 namespace {
 inline size_t al16(size_t b) { return (b + 15) & ~(size_t)15; }
@@ -71,7 +74,8 @@ size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
   return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
 }
 
-hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
+namespace {
+AttnArgs split_prefill(const AttnArgs& all) {
   AttnArgs a = all;
   // no more parts than the most keys that a tile can see pay for, so that calls
   // over short tables, or of many rows, need no join
@@ -84,9 +88,22 @@ hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
   if (most > nb / 4) most = nb / 4;
   if (most > pay) most = (long)pay;
   a.n_split = most < 1 ? 1 : (int)most;
+  return a;
+}
+}  // namespace
+
+hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
+  const AttnArgs a = split_prefill(all);
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);
+}
+
+hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
+  const AttnArgs a = split_prefill(all);
+  return a.c.D == 64    ? launch_tree_64(a, fmt, s)
+         : a.c.D == 128 ? launch_tree_128(a, fmt, s)
+                        : launch_tree_256(a, fmt, s);
 }
 
 }  // namespace moe

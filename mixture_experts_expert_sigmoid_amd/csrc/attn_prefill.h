@@ -41,9 +41,14 @@
 #include <type_traits>
 
 #include "attn_dev.h"
+#include "attn_tree.h"
 
 namespace moe {
 namespace {
+
+// what the newest tokens of a sequence see of each other: those before them, or
+// their ancestors in a tree
+enum { kCausal, kTree };
 
 // keys of a tile, rows of a workgroup's tile
 template <int D>
@@ -82,7 +87,7 @@ __device__ __forceinline__ int pre_last(const AttnArgs& a, Ok ok) {
   }
 }
 
-template <int D>
+template <int D, int MODE>
 __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   const int g = a.g;
@@ -95,9 +100,22 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   t.slot = __builtin_amdgcn_readfirstlane(kv_slot(a.slots, t.seq, a.t.n_slots, a.err));
   t.L = __builtin_amdgcn_readfirstlane(kv_len(a.t, t.slot));
   const int r1 = min(t.rows, (t.tile + 1) * ROWS) - 1;
-  t.p_min = t.L - t.m + t.tile * ROWS / g;
-  t.p_max = t.L - t.m + r1 / g;
-  t.lo_min = a.window ? max(0, t.p_min - a.window + 1) : 0;
+  if constexpr (MODE == kTree) {
+    // any row may see any drafted token; all see those before (p_min), from the
+    // shallowest one's window on
+    if (t.m > kTreeMax) {
+      atomicOr(a.err, kErrTree);
+      t.L = 0;
+    }
+    if (t.L < t.m) t.L = 0;
+    t.p_min = max(0, t.L - t.m) - 1;
+    t.p_max = t.L - 1;
+    t.lo_min = a.window ? max(0, t.p_min - a.window + 2) : 0;
+  } else {
+    t.p_min = t.L - t.m + t.tile * ROWS / g;
+    t.p_max = t.L - t.m + r1 / g;
+    t.lo_min = a.window ? max(0, t.p_min - a.window + 1) : 0;
+  }
   t.lo_max = a.window ? max(0, t.p_max - a.window + 1) : 0;
   // the groups of the first keys and those of the window lie end to end, so
   // that the few first keys do not take a tile of their own
@@ -132,7 +150,7 @@ __device__ __forceinline__ float pre_lift(float m) {
   return !BF && fabsf(m) < 0x1p18f ? kLift : 0.0f;
 }
 
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_prefill_kernel(AttnArgs a) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   constexpr int NA = BN / 32;                    // 32-key score tiles
@@ -149,6 +167,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   __shared__ int s_gone;                         // last tile with a group that has no page
   __shared__ int s_miss[2][4];                   // the same for each wave's group, by buffer
   __shared__ int s_bad;                          // values of V not finite were taken out
+  __shared__ TreeRows<MODE == kTree ? ROWS : 0> s_tree;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -160,7 +179,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const int tt = a.n_tiles - 1 - block / a.c.hkv;
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
-  if (!pre_span<D>(a, t)) return;
+  if (!pre_span<D, MODE>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
@@ -179,6 +198,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   sc = flat ? 1.0f : fabsf(sc);
   const float thr = fminf(kDefer<BF> / sc, 1e30f);
 
+  constexpr int GT = BN / 16;                    // groups of a tile
+  auto group_key = [&](int i) { return 16 * (i < t.ng1 ? i : t.b2 + i - t.ng1); };
+  // tiles of which every row sees every key (the first keys' may be such too,
+  // and are treated as if not)
+  const int whole0 =
+      (t.ng1 + max(0, (t.lo_max + 15) / 16 - t.b2) + GT - 1) / GT;
+  const int whole1 = (t.ng1 - t.b2 + (t.p_min + 1) / 16) / GT;
+  auto whole = [&](int x) { return x >= whole0 && x < whole1; };
+  // the rows' ancestors, for the parts that have tiles that are not whole
+  const bool masked = MODE == kTree && (x0 < whole0 || x1 > whole1);
+  if constexpr (MODE == kTree)
+    if (masked) s_tree.fetch(a.parent + t.q0, t.m);
+
   // this lane's row
   struct Row {
     bool have;
@@ -192,8 +224,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     const int k = max(tok, 0);
     return Row{tok >= 0, kvh * a.g + (tok >= 0 ? row_of + l31 - k * a.g : 0), (long)t.q0 + k};
   };
+  const int tok0 = t.tile * ROWS / a.g;          // the tile's first token
   auto pos_of = [&] {
     asm volatile("" : "+v"(tok));
+    if constexpr (MODE == kTree)
+      return tok >= 0 ? t.L - t.m + (masked ? s_tree.depth(tok - tok0) : 0) : -1;
     return tok >= 0 ? t.L - t.m + tok : -1;
   };
   u32x4 q[NC];
@@ -219,15 +254,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   const char* kb = a.c.k + kvh * a.c.sh;
   const char* vb = a.c.v + kvh * a.c.sh;
   const int grp = w * WR / 16;                   // 16-key group that this wave brings from
-
-  constexpr int GT = BN / 16;                    // groups of a tile
-  auto group_key = [&](int i) { return 16 * (i < t.ng1 ? i : t.b2 + i - t.ng1); };
-  // tiles of which every row sees every key (the first keys' may be such too,
-  // and are treated as if not)
-  const int whole0 =
-      (t.ng1 + max(0, (t.lo_max + 15) / 16 - t.b2) + GT - 1) / GT;
-  const int whole1 = (t.ng1 - t.b2 + (t.p_min + 1) / 16) / GT;
-  auto whole = [&](int x) { return x >= whole0 && x < whole1; };
 
   // Byte offset in the cache of the wave's group of the next 64 tiles, a tile
   // a lane; kMissing: no page, kUnseen: nothing of it is visible. One lookup a
@@ -418,11 +444,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
         return (uint32_t)((1ull << cnt) - 1);
       };
       const int pos = pos_of(), lo = a.window ? pos - a.window + 1 : 0;
+      const int end = MODE == kTree ? (tok >= 0 ? t.L - t.m : 0) : pos + 1;
       const int at = 16 * (t.b2 - t.ng1 + GT * x) + 4 * half;
-      uint32_t see = below(pos + 1 - at) & (~below(lo - at) | below(a.first - at));
+      uint32_t see = below(end - at) & (~below(lo - at) | below(a.first - at));
+      if constexpr (MODE == kTree) {
+        // the row's own key and its ancestors': 64 keys from `at` on, of which
+        // the lane has four of each eight
+        if (masked && tok >= 0) {
+          uint64_t f = s_tree.bits(tok - tok0, at - (t.L - t.m)) & 0x0F0F0F0F0F0F0F0Full;
+          f = (f | f >> 4) & 0x00FF00FF00FF00FFull;
+          f = (f | f >> 8) & 0x0000FFFF0000FFFFull;
+          see |= (uint32_t)(f | f >> 16);
+        }
+      }
       if (GT * x < t.ng1) {                      // groups of the first keys
         const uint32_t own = below(16 * (t.ng1 - GT * x));
-        see = (see & ~own) | (own & below(min(pos + 1, a.first) - 16 * GT * x - 4 * half));
+        see = (see & ~own) | (own & below(min(end, a.first) - 16 * GT * x - 4 * half));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) see &= (gone >> i) & 1 ? ~(0xFFu << (8 * i)) : ~0u;
@@ -563,6 +600,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     __syncthreads();                             // s_gone and s_miss are set
     issue_k(x0, g0, s_k0, s_miss[0]);
     issue_v(g0, s_v0);
+    if constexpr (MODE == kTree)
+      if (masked)
+        s_tree.build(tok0, min(t.m, (t.tile * ROWS + ROWS - 1) / a.g + 1), t.L - t.m, a.window,
+                     a.first, a.err);
     if (x0 + 1 < x1) g1 = group_of(x0 + 1);
     arrived();
     finish_k(s_k0);
@@ -622,7 +663,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
                        : (float)__builtin_bit_cast(_Float16, (uint16_t)q16));
           }
         dot = xor32_reduce(dot, OpSum{});
-        const bool sees = j <= pos && (j >= lo || j < a.first);
+        bool sees = j <= pos && (j >= lo || j < a.first);
+        if constexpr (MODE == kTree) {
+          const int b = j - (t.L - t.m);         // a drafted token
+          if (b >= 0) sees = tok >= 0 && (s_tree.bits(tok - tok0, b) & 1);
+        }
         const float pv = exp2_fast(__builtin_fmaf(dot, sc, neg_of()));
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -692,7 +737,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
 
 // Joins the parts of split tiles: a workgroup for each 16 rows of a tile, 16
 // lanes a row, the parts in order.
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   constexpr int ROWS = PreShape<D>::ROWS, V = D / 16;
   PreTile t;
@@ -700,7 +745,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   const int kvh = block % a.c.hkv, tt = block / a.c.hkv;
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
-  if (!pre_span<D>(a, t)) return;
+  if (!pre_span<D, MODE>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if (parts == 1) return;
   const int r = t.tile * ROWS + (int)blockIdx.y * 16 + (threadIdx.x >> 4);
@@ -756,7 +801,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   if (a.lse && d0 == 0) a.lse[ri] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <bool BF, bool F8, int D>
+template <bool BF, bool F8, int D, int MODE>
 hipError_t run_prefill(const AttnArgs& all, hipStream_t s) {
   AttnArgs a = all;
   a.n_tiles = (int)prefill_tiles(a.n, a.T, a.g);
@@ -764,9 +809,9 @@ hipError_t run_prefill(const AttnArgs& all, hipStream_t s) {
   for (long b = 0; b < blocks; b += kMaxGrid) {
     const unsigned grid = (unsigned)(blocks - b < kMaxGrid ? blocks - b : kMaxGrid);
     a.block0 = (int)b;
-    attn_prefill_kernel<BF, F8, D><<<dim3(grid, a.n_split), 256, 0, s>>>(a);
+    attn_prefill_kernel<BF, F8, D, MODE><<<dim3(grid, a.n_split), 256, 0, s>>>(a);
     if (a.n_split > 1)
-      prefill_join_kernel<BF, F8, D>
+      prefill_join_kernel<BF, F8, D, MODE>
           <<<dim3(grid, PreShape<D>::ROWS / 16), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -774,12 +819,12 @@ hipError_t run_prefill(const AttnArgs& all, hipStream_t s) {
   return hipSuccess;
 }
 
-template <int D>
+template <int D, int MODE>
 hipError_t run_prefill_d(const AttnArgs& a, int fmt, hipStream_t s) {
   const bool f8 = a.c.fmt == KV_E4M3;
   if (fmt == KV_BF16)
-    return f8 ? run_prefill<true, true, D>(a, s) : run_prefill<true, false, D>(a, s);
-  return f8 ? run_prefill<false, true, D>(a, s) : run_prefill<false, false, D>(a, s);
+    return f8 ? run_prefill<true, true, D, MODE>(a, s) : run_prefill<true, false, D, MODE>(a, s);
+  return f8 ? run_prefill<false, true, D, MODE>(a, s) : run_prefill<false, false, D, MODE>(a, s);
 }
 
 }  // namespace

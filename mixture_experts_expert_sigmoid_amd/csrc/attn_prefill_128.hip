@@ -3,6 +3,6 @@
 
 namespace moe {
 hipError_t launch_prefill_128(const AttnArgs& a, int fmt, hipStream_t s) {
-  return run_prefill_d<128>(a, fmt, s);
+  return run_prefill_d<128, kCausal>(a, fmt, s);
 }
 }  // namespace moe

@@ -9,7 +9,7 @@
 namespace moe {
 
 // err_word bits, equal to the public header's MOE_DEVERR_CACHE_*
-constexpr int kErrPage = 0x8, kErrFull = 0x10, kErrBusy = 0x20;
+constexpr int kErrPage = 0x8, kErrFull = 0x10, kErrBusy = 0x20, kErrTree = 0x40;
 
 enum { KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2 };
 inline int kv_esize(int fmt) { return fmt == KV_E4M3 ? 1 : 2; }
@@ -52,6 +52,7 @@ struct AttnArgs {
   float split_gain;      // see pre_parts
   int n_tiles;           // of a key-value head
   int block0;            // first of all workgroups that this launch runs
+  const int* parent;     // of each row, trees only
   // decode: every pair is one team's
   int whole;
   // partial results of split rows
@@ -107,6 +108,11 @@ int prefill_splits(long n, long T, int hq, int hkv);
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 
+// Drafted tokens that form a tree behind the context run through the prompt
+// kernels, with ancestors in place of the tokens before.
+constexpr int kTreeMax = 256;           // tokens of one tree
+hipError_t launch_attn_tree(const AttnArgs& a, int fmt, hipStream_t s);
+
 // Workgroups of 256 threads in one launch: a grid has fewer than 2^32 threads.
 // Calls that need more (a list of a million sequences and many heads, rows by
 // the hundred million) take several launches.
@@ -127,6 +133,8 @@ struct AppendArgs {
   long row0;             // first row that this launch takes
 };
 hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s);
+constexpr int kLatRope = 64;            // rotary values behind a latent vector
+hipError_t launch_latent_append(const AppendArgs& a, int fmt, hipStream_t s);
 
 // K and V of up to kCopyLayers layers by pointer; more take more launches
 constexpr int kCopyLayers = 32;
@@ -151,6 +159,18 @@ hipError_t launch_cache_compact(const CopyLayers* cl, int n_cl, const KvTable& t
                                 int* n_used, void* ws, hipStream_t s);
 hipError_t launch_cache_copy(const CopyLayers* cl, int n_cl, const int* src,
                              const int* dst, long n, int n_pages, int* err,
+                             hipStream_t s);
+struct KeepArgs {
+  KvTable t;
+  const int* slots;      // nullable
+  const int* n_draft;
+  const int* cu;
+  const int* path;
+  long n_path;
+  long i0;               // first list entry of this launch
+  int* err;
+};
+hipError_t launch_cache_keep(const CopyLayers* cl, int n_cl, const KeepArgs& a, long n,
                              hipStream_t s);
 size_t cache_ws_bytes(int n_pages, long n);
 

@@ -12,6 +12,8 @@
 static_assert(MOE_DEVERR_CACHE_PAGE == moe::kErrPage, "err bit");
 static_assert(MOE_DEVERR_CACHE_FULL == moe::kErrFull, "err bit");
 static_assert(MOE_DEVERR_CACHE_BUSY == moe::kErrBusy, "err bit");
+static_assert(MOE_DEVERR_TREE == moe::kErrTree, "err bit");
+static_assert(MOE_TREE_MAX == moe::kTreeMax, "limit");
 static_assert(MOE_KV_BF16 == moe::KV_BF16 && MOE_KV_F16 == moe::KV_F16 &&
                   MOE_KV_E4M3 == moe::KV_E4M3,
               "formats");
@@ -164,9 +166,38 @@ int copy_layers(const moe_kv_cache* layers, int n_layers, const moe_kv_table* ta
       ++*n_out;
     }
     cl.p[cl.n++] = (char*)c->k;
-    cl.p[cl.n++] = (char*)c->v;
+    if (c->v != c->k) cl.p[cl.n++] = (char*)c->v;     // (a latent cache has one array)
   }
   return MOE_OK;
+}
+
+int check_latent(const moe_latent_cache* c) {
+  if (!c) return MOE_ERR_NULL;
+  if (c->fmt < MOE_KV_BF16 || c->fmt > MOE_KV_E4M3) return MOE_ERR_FORMAT;
+  if (c->n_pages < 1 || c->page_size < 16 || c->page_size > 4096 || c->page_size % 16 ||
+      (c->latent_dim != 256 && c->latent_dim != 512) || c->rope_dim != moe::kLatRope)
+    return MOE_ERR_SHAPE;
+  const long es = moe::kv_esize(c->fmt), unit = 16 / es;
+  for (long s : {c->stride_page, c->stride_tok})
+    if (s < c->latent_dim + c->rope_dim || s > (1L << 46) || s % unit) return MOE_ERR_SHAPE;
+  if (c->stride_tok >= (1L << 30) / (16 * es)) return MOE_ERR_SHAPE;
+  if (!c->c) return MOE_ERR_NULL;
+  if (((uintptr_t)c->c) & 15) return MOE_ERR_PARAM;
+  const bool scaled = c->fmt == MOE_KV_E4M3;
+  if (scaled && !c->scale) return MOE_ERR_NULL;
+  if (!scaled && c->scale) return MOE_ERR_PARAM;
+  return MOE_OK;
+}
+
+int check_latent_pair(const moe_latent_cache* c, const moe_kv_table* t) {
+  return c->page_size == t->page_size && c->n_pages == t->n_pages ? MOE_OK : MOE_ERR_SHAPE;
+}
+
+// D: the latent vector's; one head, keys and values in one array
+moe::KvCache dev_latent(const moe_latent_cache* c) {
+  const long es = moe::kv_esize(c->fmt);
+  return {(char*)c->c, (char*)c->c, c->stride_page * es, 0, c->stride_tok * es, c->scale,
+          c->scale, c->fmt, c->n_pages, c->page_size, 1, c->latent_dim};
 }
 
 constexpr int kMaxGroups = (kMaxLayers + moe::kCopyLayers - 1) / moe::kCopyLayers;
@@ -224,6 +255,29 @@ int moe_attn_prefill(const moe_kv_cache* cache, const moe_kv_table* table, const
   a.part = (float*)ws;
   return done(moe::launch_attn_prefill(a, attn->fmt, (hipStream_t)stream),
               "moe_attn_prefill");
+}
+
+size_t moe_attn_tree_workspace_size(const moe_kv_cache* cache, long n, long T, int n_heads) {
+  return moe_attn_prefill_workspace_size(cache, n, T, n_heads);
+}
+
+int moe_attn_tree(const moe_kv_cache* cache, const moe_kv_table* table, const int* slots, long n,
+                  const int* cu_q, long T, const int* parent, const moe_attn* attn, int* err_word,
+                  void* ws, size_t ws_bytes, void* stream) {
+  moe::AttnArgs a;
+  int st = attn_args(cache, table, slots, n, T, attn, err_word, &a);
+  if (st) return st;
+  if (!slots && n > table->n_slots) return MOE_ERR_SHAPE;
+  if (n == 0 && T > 0) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!cu_q || !parent) return MOE_ERR_NULL;
+  const size_t need = moe::prefill_ws_bytes(n, T, a.hq, a.c.hkv, a.c.D);
+  if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return MOE_ERR_WORKSPACE;
+  a.cu = cu_q;
+  a.T = T;
+  a.parent = parent;
+  a.part = (float*)ws;
+  return done(moe::launch_attn_tree(a, attn->fmt, (hipStream_t)stream), "moe_attn_tree");
 }
 
 int moe_cache_append(const moe_kv_cache* cache, const moe_kv_table* table, const int* slots,
@@ -318,6 +372,63 @@ int moe_cache_fork(const moe_kv_cache* layers, int n_layers, const moe_kv_table*
   return done(moe::launch_cache_fork(cl, n_cl, dev_table(table), src, dst, n, err_word, ws,
                                      (hipStream_t)stream),
               "moe_cache_fork");
+}
+
+int moe_cache_keep(const moe_kv_cache* layers, int n_layers, const moe_kv_table* table,
+                   const int* slots, const int* n_draft, const int* cu, const int* path,
+                   long n_path, long n, int* err_word, void* stream) {
+  int st = check_table(table, true);
+  if (st) return st;
+  moe::CopyLayers cl[kMaxGroups];
+  int n_cl = 0;
+  st = copy_layers(layers, n_layers, table, cl, &n_cl);
+  if (st) return st;
+  if (n < 0 || n >= (1L << 20) || n_path < 0 || n_path >= (1L << 31) ||
+      (!slots && n > table->n_slots))
+    return MOE_ERR_SHAPE;
+  if (!err_word) return MOE_ERR_NULL;
+  if (n == 0) return MOE_OK;
+  if (!n_draft || !cu || (!path && n_path > 0)) return MOE_ERR_NULL;
+  const moe::KeepArgs a{dev_table(table), slots, n_draft, cu, path, n_path, 0, err_word};
+  return done(moe::launch_cache_keep(cl, n_cl, a, n, (hipStream_t)stream), "moe_cache_keep");
+}
+
+int moe_latent_pages(const moe_latent_cache* cache, moe_kv_cache* pages) {
+  const int st = check_latent(cache);
+  if (st) return st;
+  if (!pages) return MOE_ERR_NULL;
+  *pages = {cache->fmt, cache->n_pages, cache->page_size,
+            (cache->latent_dim + cache->rope_dim) / 64, 64, cache->stride_page, 64,
+            cache->stride_tok, cache->c, cache->c, cache->scale, cache->scale};
+  return MOE_OK;
+}
+
+int moe_latent_append(const moe_latent_cache* cache, const moe_kv_table* table, const int* slots,
+                      const int* start, const int* cu, long n, long T, int fmt, const void* c,
+                      long c_stride_row, const void* rope, long rope_stride_row, int* err_word,
+                      void* stream) {
+  int st = check_latent(cache);
+  if (st) return st;
+  st = check_table(table, false);
+  if (st) return st;
+  st = check_latent_pair(cache, table);
+  if (st) return st;
+  if (fmt != MOE_KV_BF16 && fmt != MOE_KV_F16) return MOE_ERR_FORMAT;
+  if (cache->fmt != MOE_KV_E4M3 && cache->fmt != fmt) return MOE_ERR_FORMAT;
+  if (n < 0 || n >= (1L << 20) || T < 0 || T >= (1L << 31) || (!cu && T != n) ||
+      (n == 0 && T > 0) || (!slots && n > table->n_slots))
+    return MOE_ERR_SHAPE;
+  if (!err_word) return MOE_ERR_NULL;
+  if (T == 0) return MOE_OK;
+  if (!start || !c || !rope) return MOE_ERR_NULL;
+  if (!row_strides_ok(c_stride_row, cache->latent_dim, cache->latent_dim) ||
+      !row_strides_ok(rope_stride_row, cache->rope_dim, cache->rope_dim))
+    return MOE_ERR_SHAPE;
+  if ((((uintptr_t)c) | ((uintptr_t)rope)) & 15) return MOE_ERR_PARAM;
+  moe::AppendArgs a{dev_latent(cache), dev_table(table), slots, start, cu, (int)n, T,
+                    (const char*)c, (const char*)rope, c_stride_row * 2, 0,
+                    rope_stride_row * 2, 0, err_word};
+  return done(moe::launch_latent_append(a, fmt, (hipStream_t)stream), "moe_latent_append");
 }
 
 int moe_cache_compact(const moe_kv_cache* layers, int n_layers, const moe_kv_table* table,

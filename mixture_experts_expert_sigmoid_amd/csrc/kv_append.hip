@@ -40,13 +40,14 @@ __device__ __forceinline__ uint32_t pack4(const float (&q)[4], bool finite) {
 constexpr int kMaxRows = 8;      // rows of a workgroup
 constexpr int kBatch = 4;        // 16-byte loads of a thread in flight
 
-// IN: type of the rows; Q: into an e4m3 cache
-template <int IN, bool Q>
+// IN: type of the rows; Q: into an e4m3 cache; LAT: a latent cache, whose
+// tokens are D values of k and then kLatRope of v, in one array with one scale
+template <int IN, bool Q, bool LAT>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
   __shared__ long s_off[kMaxRows];                // place of the row's token; -1: none
   const int upr = a.c.D >> 3;                     // 16-byte units per head, a power of two
   const int lg = __builtin_ctz(upr);
-  const int per = 2 * a.c.hkv * upr;              // units per token
+  const int per = LAT ? upr + kLatRope / 8 : 2 * a.c.hkv * upr;      // units per token
   const int tid = threadIdx.x;
   const long r0 = a.row0 + (long)blockIdx.x * rows;
   const int nr = (int)min((long)rows, a.T - r0);
@@ -65,7 +66,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
       bx[k] = x;
       in[k] = make_uint4(0, 0, 0, 0);
       if (row < nr) {
-        const int kvh = x >> lg, val = kvh >= a.c.hkv, h = kvh - val * a.c.hkv;
+        const int kvh = x >> lg, val = LAT ? kvh > 0 : kvh >= a.c.hkv;
+        const int h = LAT ? 0 : kvh - val * a.c.hkv;
         const long r = r0 + row;
         in[k] = *(const uint4*)((val ? a.v + r * a.v_row + h * a.v_head
                                      : a.k + r * a.k_row + h * a.k_head) +
@@ -122,8 +124,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
       if (br[k] >= nr) continue;
       const long off = s_off[br[k]];
       if (off < 0) continue;
-      const int kvh = bx[k] >> lg, val = kvh >= a.c.hkv, h = kvh - val * a.c.hkv;
-      const int c8 = bx[k] & (upr - 1);
+      const int kvh = bx[k] >> lg, val = LAT ? 0 : kvh >= a.c.hkv;
+      const int h = LAT ? 0 : kvh - val * a.c.hkv;
+      const int c8 = LAT ? bx[k] : bx[k] & (upr - 1);
       char* dst = (val ? a.c.v : a.c.k) + off + h * a.c.sh;
       if (Q) {
         // x / s: with y = RN(1 / s), q0 = RN(x y) and the residual r = q0 s - x,
@@ -172,9 +175,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int rows) {
   }
 }
 
-}  // namespace
-
-hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s) {
+template <bool LAT>
+hipError_t run_append(const AppendArgs& a, int fmt, hipStream_t s) {
   // a row a workgroup as long as there are few, so that single tokens spread
   // over the CUs; more of them share one lookup's latency for prompts
   const int rows = (int)(a.T >= 1024 * kMaxRows ? kMaxRows : a.T < 2048 ? 1 : a.T / 1024);
@@ -184,15 +186,25 @@ hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s) {
     const long left = (a.T - p.row0 + rows - 1) / rows;
     const unsigned grid = (unsigned)(left < kMaxGrid ? left : kMaxGrid);
     if (!q)
-      append_kernel<KV_BF16, false><<<grid, 256, 0, s>>>(p, rows);   // bits only, either type
+      append_kernel<KV_BF16, false, LAT><<<grid, 256, 0, s>>>(p, rows);   // bits only, any type
     else if (fmt == KV_BF16)
-      append_kernel<KV_BF16, true><<<grid, 256, 0, s>>>(p, rows);
+      append_kernel<KV_BF16, true, LAT><<<grid, 256, 0, s>>>(p, rows);
     else
-      append_kernel<KV_F16, true><<<grid, 256, 0, s>>>(p, rows);
+      append_kernel<KV_F16, true, LAT><<<grid, 256, 0, s>>>(p, rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_append(const AppendArgs& a, int fmt, hipStream_t s) {
+  return run_append<false>(a, fmt, s);
+}
+
+hipError_t launch_latent_append(const AppendArgs& a, int fmt, hipStream_t s) {
+  return run_append<true>(a, fmt, s);
 }
 
 }  // namespace moe

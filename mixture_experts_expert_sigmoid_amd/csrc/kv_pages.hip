@@ -1,6 +1,6 @@
 // Upkeep of the pages of a key-value cache: taking free pages (grow, fork),
-// giving them back (free, trim), and moving or copying their contents
-// (fork, compact, copy_pages).
+// giving them back (free, trim, keep), and moving or copying their contents
+// (fork, compact, copy_pages, keep).
 //
 // A page is free when no table entry names it (refs 0), so there is no free
 // list: the lowest free pages are found by ranking the zeros of refs. One
@@ -29,7 +29,7 @@ constexpr int kSeg = kThreads * kPer;   // pages per step
 // without any.
 constexpr int kCountedPool = 65536;
 
-__device__ __forceinline__ long div_up(long a, long b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ long div_up(long a, long b) { return (a + b - 1) / b; }
 
 // inclusive prefix sum over the workgroup; s_w holds one long per wave
 __device__ __forceinline__ long block_scan(long v, long* s_w, long* total) {
@@ -409,6 +409,136 @@ hipError_t copy_all(const CopyLayers* cl, int n_cl, const int* from, const int* 
   return hipGetLastError();
 }
 
+// -------------------------------------------------------------------- keep
+// The accepted path of a tree of drafted tokens: its j-th token, the a_j-th
+// drafted one, goes to place j behind the C tokens of context. a is ascending,
+// so a_j >= j: no token goes to the place of a later one of the path, and a
+// thread that has read a batch of tokens before it writes them, in the path's
+// order, has read every place before it is written. A thread keeps to its 16
+// bytes of a token, so nothing else is to be ordered.
+//
+// A slot that is to be kept gets its new length with the sign bit set from the
+// copy's first workgroup for it, and without from the launch after the copies:
+// that one gives pages back, after which refs no longer tell who was to be left.
+struct Path {
+  int slot, L, C, k;     // tokens now, those before the tree, accepted ones
+  const int* at;
+  bool marked;           // found right by another workgroup
+};
+constexpr uint32_t kKeptBit = 0x80000000u;
+
+// entry i's path, read and checked by the whole workgroup alike; false: none,
+// or one that the slot is to be left for
+__device__ bool path_of(const KeepArgs& a, long i, bool tell, Path& p) {
+  p.slot = kv_slot(a.slots, (int)i, a.t.n_slots, a.err);
+  if (p.slot < 0) return false;
+  const int m = a.n_draft[i], c0 = a.cu[i], c1 = a.cu[i + 1];
+  // one read for all: the length may be marked meanwhile
+  __shared__ int s_len;
+  if (threadIdx.x == 0) s_len = a.t.len[p.slot];
+  __syncthreads();
+  const int len = s_len, cap = a.t.max_pages * a.t.ps;
+  const int now = (int)((uint32_t)len & ~kKeptBit);
+  p.k = c1 - c0;
+  p.at = a.path + c0;
+  p.marked = len < 0 && now <= cap;
+  if (p.marked) {
+    p.C = now - p.k;
+    p.L = p.C + m;
+    return true;
+  }
+  p.L = max(0, min(len, cap));
+  p.C = p.L - m;
+  int bad = 0;
+  if (c0 < 0 || c1 < c0 || c1 > a.n_path || m < 0 || m > p.L || p.k > m) {
+    bad = kErrTree;
+  } else {
+    const int* row = a.t.table + p.slot * a.t.ld;
+    for (int j = threadIdx.x; j < p.k; j += blockDim.x) {
+      const int x = p.at[j];
+      if (x <= (j ? p.at[j - 1] : -1) || x >= m) {
+        bad |= kErrTree;
+      } else if (x != j) {
+        const int e = row[kv_entry(a.t, p.C + j)];
+        if (e >= 0 && e < a.t.n_pages && a.t.refs[e] > 1) bad |= kErrBusy;
+      }
+    }
+  }
+  const int tree = __syncthreads_or(bad & kErrTree), busy = __syncthreads_or(bad & kErrBusy);
+  if (!(tree | busy)) return true;
+  if (tell && threadIdx.x == 0) atomicOr(a.err, tree ? kErrTree : kErrBusy);
+  return false;
+}
+
+constexpr int kKeepTokens = 64;         // of a path, found at a time
+constexpr int kKeepBatch = 8;           // loads of a thread in flight
+
+// Workgroup (i, y): 256 of the 16-byte columns that all arrays' tokens have, of
+// entry i. Bound by the latency of finding the places (slot -> length, path ->
+// entries) for a step's few tokens.
+__global__ __launch_bounds__(256) void keep_copy_kernel(CopyLayers cl, KeepArgs a) {
+  __shared__ long s_from[kKeepTokens], s_to[kKeepTokens];
+  Path p;
+  if (!path_of(a, a.i0 + blockIdx.x, blockIdx.y == 0, p)) return;
+  if (blockIdx.y == 0 && !p.marked && threadIdx.x == 0)
+    a.t.len[p.slot] = (int)((uint32_t)(p.C + p.k) | kKeptBit);
+  const int upr = cl.row_bytes >> 4, lg = __builtin_ctz(upr);
+  const int per = cl.hkv * upr, col = (int)blockIdx.y * 256 + threadIdx.x;
+  const int arr = col / per, u = col - arr * per;
+  const bool mine = arr < cl.n;
+  char* const base = cl.p[mine ? arr : 0] + (u >> lg) * cl.sh + ((u & (upr - 1)) << 4);
+  const int* row = a.t.table + p.slot * a.t.ld;
+  auto place = [&](int pos) {
+    const int i = kv_entry(a.t, pos), e = row[i];
+    return e >= 0 && e < a.t.n_pages ? e * cl.sp + (pos - i * a.t.ps) * cl.st : -1L;
+  };
+  for (int j0 = 0; j0 < p.k; j0 += kKeepTokens) {
+    const int cnt = min(kKeepTokens, p.k - j0);
+    if (j0) __syncthreads();
+    if ((int)threadIdx.x < cnt) {
+      const int j = j0 + threadIdx.x, x = p.at[j];
+      long from = -1, to = -1;
+      if (x != j) {
+        from = place(p.C + x);
+        to = place(p.C + j);
+        if ((from | to) < 0) {
+          atomicOr(a.err, kErrPage);
+          from = -1;
+        }
+      }
+      s_from[threadIdx.x] = from;
+      s_to[threadIdx.x] = to;
+    }
+    __syncthreads();
+    if (!mine) continue;
+    for (int t = 0; t < cnt; t += kKeepBatch) {
+      uint4 v[kKeepBatch];
+#pragma unroll
+      for (int b = 0; b < kKeepBatch; ++b)
+        if (t + b < cnt && s_from[t + b] >= 0) v[b] = *(const uint4*)(base + s_from[t + b]);
+#pragma unroll
+      for (int b = 0; b < kKeepBatch; ++b)
+        if (t + b < cnt && s_from[t + b] >= 0) *(uint4*)(base + s_to[t + b]) = v[b];
+    }
+  }
+}
+
+// the lengths, and the pages of rejected tokens given back, once every layer
+// has been moved
+__global__ __launch_bounds__(256) void keep_kernel(KeepArgs a) {
+  Path p;
+  if (!path_of(a, blockIdx.x, false, p) || !p.marked) return;
+  int* row = a.t.table + p.slot * a.t.ld;
+  const int end = (int)div_up(p.L, a.t.ps);
+  for (int j = (int)div_up(p.C + p.k, a.t.ps) + threadIdx.x; j < end; j += 256) {
+    const int e = row[j];
+    if (e == -1) continue;
+    row[j] = -1;
+    if (e >= 0 && e < a.t.n_pages) atomicSub(&a.t.refs[e], 1);
+  }
+  if (threadIdx.x == 0) a.t.len[p.slot] = p.C + p.k;
+}
+
 // ----------------------------------------------------------------- compact
 // ws: hdr {U, pairs}, used pages per segment, holes, movers, rank of each
 // page among the movers
@@ -595,6 +725,24 @@ hipError_t launch_cache_fork(const CopyLayers* cl, int n_cl, const KvTable& t, c
   else
     fork_kernel<kFew><<<grid, 256, 0, s>>>(cl[0], t, src, dst, (int)n, p);
   return copy_all(cl + 1, n_cl - 1, p.from, p.to, n, nullptr, t.n_pages, nullptr, s);
+}
+
+hipError_t launch_cache_keep(const CopyLayers* cl, int n_cl, const KeepArgs& all, long n,
+                             hipStream_t s) {
+  KeepArgs a = all;
+  for (int i = 0; i < n_cl; ++i) {
+    const long cols = (long)cl[i].n * cl[i].hkv * (cl[i].row_bytes >> 4);
+    const unsigned wgs = (unsigned)div_up(cols, 256);
+    const long most = kMaxGrid / wgs;             // entries of one launch
+    for (a.i0 = 0; a.i0 < n; a.i0 += most) {
+      const unsigned m = (unsigned)(n - a.i0 < most ? n - a.i0 : most);
+      keep_copy_kernel<<<dim3(m, wgs), 256, 0, s>>>(cl[i], a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  keep_kernel<<<(unsigned)n, 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_cache_compact(const CopyLayers* cl, int n_cl, const KvTable& t, int* n_used,
