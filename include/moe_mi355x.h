@@ -665,6 +665,24 @@ int moe_latent_append(const moe_latent_cache *cache, const moe_kv_table *table,
                       const void *rope, long rope_stride_row, int *err_word,
                       void *stream);
 
+/* Absorbed attention over the cache: with q'_h = [Wk_h^T q_h, q_rope_h] the
+ * scores are those of the keys [c_j, r_j], and the result is sum_j p_j c_j, from
+ * which the caller takes Wv_h times it. attn: q [rows][n_heads][latent_dim +
+ * rope_dim], out [rows][n_heads][latent_dim], n_heads 1..1024, the rest as for
+ * moe_attn_prefill. Rows cu_q[i] .. cu_q[i + 1] - 1 (device int32 [n + 1]; NULL:
+ * one row each, T = n) are the newest tokens of slots[i] (NULL: i): what they
+ * see of each other goes by parent as in moe_attn_tree, or, without (NULL), by
+ * their order as in moe_attn_prefill. The keys of all rows are dealt out evenly
+ * over the GPU and the parts joined in a fixed order. Limits: 0 <= n < 2^20,
+ * T < 2^31 / n_heads. Workspace: moe_attn_latent_workspace_size(cache, n, T,
+ * n_heads) bytes. Errors as for moe_attn_decode. */
+int moe_attn_latent(const moe_latent_cache *cache, const moe_kv_table *table,
+                    const int *slots, long n, const int *cu_q, long T,
+                    const int *parent, const moe_attn *attn, int *err_word,
+                    void *ws, size_t ws_bytes, void *stream);
+size_t moe_attn_latent_workspace_size(const moe_latent_cache *cache, long n,
+                                      long T, int n_heads);
+
 /* --------------------------------------------------------------- misc -- */
 /* Synchronises `stream`, then copies *err_word (device) to *host_bits. */
 int moe_read_device_error(const int *err_word, int *host_bits, void *stream);

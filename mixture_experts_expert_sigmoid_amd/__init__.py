@@ -174,6 +174,11 @@ _SIGS = {
                                c_void_p, c_void_p, c_void_p, c_long, c_long, c_void_p,
                                c_void_p]),
     "moe_cache_workspace_size": (c_size_t, [POINTER(MoeKvTable), c_long]),
+    "moe_attn_latent": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvTable), c_void_p, c_long,
+                                c_void_p, c_long, c_void_p, POINTER(MoeAttn), c_void_p, c_void_p,
+                                c_size_t, c_void_p]),
+    "moe_attn_latent_workspace_size": (c_size_t, [POINTER(MoeLatentCache), c_long, c_long,
+                                                  c_int]),
     "moe_latent_pages": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvCache)]),
     "moe_latent_append": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvTable), c_void_p,
                                   c_void_p, c_void_p, c_long, c_long, c_int, c_void_p, c_long,
@@ -505,13 +510,15 @@ def _rows(t: torch.Tensor, where: str, shape, D: int):
     return (st[0] if shape[0] > 1 else shape[1] * D), (st[1] if shape[1] > 1 else D)
 
 
-def _attn(where, cache: MoeKvCache, shape, q, out, scale, window, n_first, lse) -> MoeAttn:
-    D, fmt = cache.head_dim, _KV_FMT.get(q.dtype)
+def _attn(where, shape, dk, dv, q, out, scale, window, n_first, lse) -> MoeAttn:
+    """q of keys of dk, out of values of dv."""
+    fmt = _KV_FMT.get(q.dtype)
     if out.dtype is not q.dtype:
         raise MoeError(-2, where, "out and q differ in type")
     if fmt is None:
         raise MoeError(-3, where, f"dtype {q.dtype}")
-    qs, os_ = _rows(q, where, shape, D), _rows(out, where, shape, D)
+    qs = _rows(q, where, shape, dk)
+    os_ = _rows(out, where, shape if dk == dv else (*shape[:2], dv), dv)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
                             or not lse.is_contiguous() or not lse.is_cuda):
         _on_gpu(where, lse)
@@ -529,7 +536,8 @@ def moe_attn_decode(cache: MoeKvCache, table: MoeKvTable, q, out, scale, err_wor
     """One new token per sequence: q and out [n][heads][head_dim], lse [n][heads]."""
     where = "moe_attn_decode"
     shape = q.shape
-    a, n = _attn(where, cache, shape, q, out, scale, window, n_first, lse), shape[0]
+    D, n = cache.head_dim, shape[0]
+    a = _attn(where, shape, D, D, q, out, scale, window, n_first, lse)
     _check(lib().moe_attn_decode(cache, table, _i32(slots, n, where), n, a,
                                  _err(err_word, where), *_work(ws, where),
                                  _stream(stream)), where)
@@ -545,7 +553,8 @@ def moe_attn_prefill(cache: MoeKvCache, table: MoeKvTable, q, cu_q, out, scale, 
     [T][heads][head_dim], lse [T][heads]."""
     where = "moe_attn_prefill"
     shape = q.shape
-    a = _attn(where, cache, shape, q, out, scale, window, n_first, lse)
+    D = cache.head_dim
+    a = _attn(where, shape, D, D, q, out, scale, window, n_first, lse)
     n = cu_q.numel() - 1
     _check(lib().moe_attn_prefill(cache, table, _i32(slots, n, where), n,
                                   _i32(cu_q, 1, where), shape[0], a, _err(err_word, where),
@@ -564,7 +573,8 @@ def moe_attn_tree(cache: MoeKvCache, table: MoeKvTable, q, cu_q, parent, out, sc
     context."""
     where = "moe_attn_tree"
     shape = q.shape
-    a = _attn(where, cache, shape, q, out, scale, window, n_first, lse)
+    D = cache.head_dim
+    a = _attn(where, shape, D, D, q, out, scale, window, n_first, lse)
     n = cu_q.numel() - 1
     _check(lib().moe_attn_tree(cache, table, _i32(slots, n, where), n, _i32(cu_q, 1, where),
                                shape[0], _i32(parent, shape[0], where), a,
@@ -708,6 +718,25 @@ def moe_latent_append(cache: MoeLatentCache, table: MoeKvTable, start, cu, c, ro
     _check(lib().moe_latent_append(
         cache, table, _i32(slots, n, where), _i32(start, n, where), _i32(cu, 1, where), n, T,
         _kv_fmt(c, where), _p(c), cs, _p(rope), rs, _err(err_word, where), _stream(stream)), where)
+
+
+def moe_attn_latent_workspace_size(cache: MoeLatentCache, n: int, T: int, n_heads: int) -> int:
+    return lib().moe_attn_latent_workspace_size(cache, n, T, n_heads)
+
+
+def moe_attn_latent(cache: MoeLatentCache, table: MoeKvTable, q, cu_q, out, scale, err_word, ws,
+                    *, parent=None, window=0, n_first=0, slots=None, lse=None, stream=None):
+    """Absorbed attention of the newest tokens of n = len(cu_q) - 1 sequences, or of
+    one token each (cu_q None): q [T][heads][latent_dim + rope_dim], out
+    [T][heads][latent_dim], lse [T][heads]; parent int32 [T] for drafted trees."""
+    where = "moe_attn_latent"
+    shape, dc = q.shape, cache.latent_dim
+    a = _attn(where, shape, dc + cache.rope_dim, dc, q, out, scale, window, n_first, lse)
+    T = shape[0]
+    n = T if cu_q is None else cu_q.numel() - 1
+    _check(lib().moe_attn_latent(cache, table, _i32(slots, n, where), n, _i32(cu_q, 1, where), T,
+                                 _i32(parent, T, where), a, _err(err_word, where),
+                                 *_work(ws, where), _stream(stream)), where)
 
 
 class _Workspace:

@@ -9,6 +9,7 @@ namespace moe {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -73,5 +74,20 @@ __device__ __forceinline__ float of_sum(float y, float inv, float l) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// A maximum is followed when it has grown by more than 2^kDefer. In f16, whose
+// numbers end at 2^-24 and have all their bits from 2^-14 on, probabilities are
+// taken 2^kLift times as large, so that many weak keys beside a strong one are
+// not lost from the product while they count in the sum; both together stay
+// below 2^16. bf16 has the exponents of fp32. Following so much sooner costs
+// f16 prompts of 6000 tokens 1 % at head_dim 64 and 128, 5 % at 256 (8 % over
+// e4m3), whose O takes three instructions a register to rescale. No lift for a
+// maximum (of scores in base 2) whose own rounding could take them past 2^16.
+template <bool BF> constexpr float kDefer = BF ? 8.0f : 3.9f;
+constexpr float kLift = 12.0f;
+template <bool BF>
+__device__ __forceinline__ float pre_lift(float m) {
+  return !BF && fabsf(m) < 0x1p18f ? kLift : 0.0f;
+}
 
 }  // namespace moe

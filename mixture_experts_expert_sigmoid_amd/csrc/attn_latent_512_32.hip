@@ -1,0 +1,8 @@
+// Latent attention for vectors of 512 values, 32 rows a workgroup.
+#include "attn_latent.h"
+
+namespace moe {
+hipError_t launch_latent_512_32(const AttnArgs& a, int fmt, int grid, hipStream_t s) {
+  return run_latent_d<512, 32>(a, fmt, grid, s);
+}
+}  // namespace moe

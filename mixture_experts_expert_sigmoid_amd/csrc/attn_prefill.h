@@ -135,21 +135,6 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
   return max(1, min(min(a.n_split, nb >> 2), (int)sqrtf((float)nb * a.split_gain)));
 }
 
-// A maximum is followed when it has grown by more than 2^kDefer. In f16, whose
-// numbers end at 2^-24 and have all their bits from 2^-14 on, probabilities are
-// taken 2^kLift times as large, so that many weak keys beside a strong one are
-// not lost from the product while they count in the sum; both together stay
-// below 2^16. bf16 has the exponents of fp32. Following so much sooner costs
-// f16 prompts of 6000 tokens 1 % at head_dim 64 and 128, 5 % at 256 (8 % over
-// e4m3), whose O takes three instructions a register to rescale. No lift for a
-// maximum (of scores in base 2) whose own rounding could take them past 2^16.
-template <bool BF> constexpr float kDefer = BF ? 8.0f : 3.9f;
-constexpr float kLift = 12.0f;
-template <bool BF>
-__device__ __forceinline__ float pre_lift(float m) {
-  return !BF && fabsf(m) < 0x1p18f ? kLift : 0.0f;
-}
-
 template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_prefill_kernel(AttnArgs a) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;

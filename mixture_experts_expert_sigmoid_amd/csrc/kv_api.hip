@@ -74,8 +74,39 @@ bool row_strides_ok(long row, long head, int D) {
          head < (1L << 46);
 }
 
-// what both attention calls ask of their arguments, and the arguments of the
-// kernels; rows of q > 0
+// the queries, outputs and scale of an attention call with keys of dk and values
+// of dv; rows of q >= 0
+int attn_rows(const moe_attn* at, int dk, int dv, long rows, moe::AttnArgs* a) {
+  if (!isfinite(at->scale) || at->window < 0 || at->n_first < 0) return MOE_ERR_PARAM;
+  if (rows > 0) {
+    if (!at->q || !at->out) return MOE_ERR_NULL;
+    if (!row_strides_ok(at->q_stride_row, at->q_stride_head, dk) ||
+        !row_strides_ok(at->out_stride_row, at->out_stride_head, dv))
+      return MOE_ERR_SHAPE;
+    if ((((uintptr_t)at->q) | ((uintptr_t)at->out)) & 15) return MOE_ERR_PARAM;
+  }
+  a->q = (const char*)at->q;
+  a->out = (char*)at->out;
+  a->q_row = at->q_stride_row * 2;
+  a->q_head = at->q_stride_head * 2;
+  a->o_row = at->out_stride_row * 2;
+  a->o_head = at->out_stride_head * 2;
+  a->lse = at->lse;
+  a->hq = at->n_heads;
+  a->scale = at->scale * 1.44269504088896340736f;
+  return MOE_OK;
+}
+
+// A window that no context of at most `most` tokens exceeds is none. What is left
+// is at most kMaxTokens, so that position - window stays within 32 bits, for rows
+// before a sequence's first position too.
+void attn_window(const moe_attn* at, long most, moe::AttnArgs* a) {
+  a->window = at->window < most ? at->window : 0;
+  a->first = a->window ? (int)(at->n_first < most ? at->n_first : most) : 0;
+}
+
+// what the calls over a key-value cache ask of their arguments, and the arguments
+// of the kernels
 int attn_args(const moe_kv_cache* cache, const moe_kv_table* table, const int* slots, long n,
               long rows, const moe_attn* at, int* err_word, moe::AttnArgs* a) {
   int st = check_cache(cache);
@@ -91,35 +122,15 @@ int attn_args(const moe_kv_cache* cache, const moe_kv_table* table, const int* s
       at->n_heads % cache->n_heads || at->n_heads / cache->n_heads > 64)
     return MOE_ERR_SHAPE;
   if (rows > 0x7FFFFFFFL / at->n_heads) return MOE_ERR_SHAPE;
-  if (!isfinite(at->scale) || at->window < 0 || at->n_first < 0) return MOE_ERR_PARAM;
-  if (rows > 0) {
-    if (!at->q || !at->out) return MOE_ERR_NULL;
-    if (!row_strides_ok(at->q_stride_row, at->q_stride_head, cache->head_dim) ||
-        !row_strides_ok(at->out_stride_row, at->out_stride_head, cache->head_dim))
-      return MOE_ERR_SHAPE;
-    if ((((uintptr_t)at->q) | ((uintptr_t)at->out)) & 15) return MOE_ERR_PARAM;
-  }
   *a = moe::AttnArgs{};
+  st = attn_rows(at, cache->head_dim, cache->head_dim, rows, a);
+  if (st) return st;
   a->c = dev_cache(cache);
   a->t = dev_table(table);
   a->slots = slots;
   a->n = (int)n;
-  a->q = (const char*)at->q;
-  a->out = (char*)at->out;
-  a->q_row = at->q_stride_row * 2;
-  a->q_head = at->q_stride_head * 2;
-  a->o_row = at->out_stride_row * 2;
-  a->o_head = at->out_stride_head * 2;
-  a->lse = at->lse;
-  a->hq = at->n_heads;
   a->g = at->n_heads / cache->n_heads;
-  a->scale = at->scale * 1.44269504088896340736f;
-  // A window that no context of this table exceeds is none. What is left is at
-  // most kMaxTokens, so that position - window stays within 32 bits, for rows
-  // before a sequence's first position too.
-  const long most = (long)table->max_pages * table->page_size;
-  a->window = at->window < most ? at->window : 0;
-  a->first = a->window ? (int)(at->n_first < most ? at->n_first : most) : 0;
+  attn_window(at, (long)table->max_pages * table->page_size, a);
   a->err = err_word;
   return MOE_OK;
 }
@@ -429,6 +440,50 @@ int moe_latent_append(const moe_latent_cache* cache, const moe_kv_table* table, 
                     (const char*)c, (const char*)rope, c_stride_row * 2, 0,
                     rope_stride_row * 2, 0, err_word};
   return done(moe::launch_latent_append(a, fmt, (hipStream_t)stream), "moe_latent_append");
+}
+
+size_t moe_attn_latent_workspace_size(const moe_latent_cache* cache, long n, long T,
+                                      int n_heads) {
+  if (!cache || (cache->latent_dim != 256 && cache->latent_dim != 512) || n < 0 ||
+      n >= (1L << 20) || n_heads < 1 || n_heads > 1024 || T < 0 || T > 0x7FFFFFFFL / n_heads)
+    return 0;
+  return moe::latent_ws_bytes(n, T, n_heads, cache->latent_dim);
+}
+
+int moe_attn_latent(const moe_latent_cache* cache, const moe_kv_table* table, const int* slots,
+                    long n, const int* cu_q, long T, const int* parent, const moe_attn* at,
+                    int* err_word, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_latent(cache);
+  if (st) return st;
+  st = check_table(table, false);
+  if (st) return st;
+  st = check_latent_pair(cache, table);
+  if (st) return st;
+  if (!at || !err_word) return MOE_ERR_NULL;
+  if (at->fmt != MOE_KV_BF16 && at->fmt != MOE_KV_F16) return MOE_ERR_FORMAT;
+  if (cache->fmt != MOE_KV_E4M3 && cache->fmt != at->fmt) return MOE_ERR_FORMAT;
+  if (n < 0 || n >= (1L << 20) || T < 0 || at->n_heads < 1 || at->n_heads > 1024 ||
+      T > 0x7FFFFFFFL / at->n_heads || (!cu_q && T != n) || (n == 0 && T > 0) ||
+      (!slots && n > table->n_slots))
+    return MOE_ERR_SHAPE;
+  moe::AttnArgs a{};
+  st = attn_rows(at, cache->latent_dim + cache->rope_dim, cache->latent_dim, T, &a);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  const size_t need = moe::latent_ws_bytes(n, T, at->n_heads, cache->latent_dim);
+  if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return MOE_ERR_WORKSPACE;
+  a.c = dev_latent(cache);
+  a.t = dev_table(table);
+  attn_window(at, (long)table->max_pages * table->page_size, &a);
+  a.slots = slots;
+  a.n = (int)n;
+  a.g = at->n_heads;
+  a.err = err_word;
+  a.cu = cu_q;
+  a.T = T;
+  a.parent = parent;
+  a.part = (float*)ws;
+  return done(moe::launch_attn_latent(a, at->fmt, (hipStream_t)stream), "moe_attn_latent");
 }
 
 int moe_cache_compact(const moe_kv_cache* layers, int n_layers, const moe_kv_table* table,
