@@ -10,10 +10,8 @@ hipError_t launch_decode_256(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_64(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
-hipError_t launch_latent_256_32(const AttnArgs& a, int fmt, int grid, hipStream_t s);
-hipError_t launch_latent_256_64(const AttnArgs& a, int fmt, int grid, hipStream_t s);
-hipError_t launch_latent_512_32(const AttnArgs& a, int fmt, int grid, hipStream_t s);
-hipError_t launch_latent_512_64(const AttnArgs& a, int fmt, int grid, hipStream_t s);
+hipError_t launch_latent_256(const AttnArgs& a, int fmt, int grid, hipStream_t s);
+hipError_t launch_latent_512(const AttnArgs& a, int fmt, int grid, hipStream_t s);
 hipError_t launch_tree_64(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_tree_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_tree_256(const AttnArgs& a, int fmt, hipStream_t s);
@@ -110,12 +108,12 @@ hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
                         : launch_tree_256(a, fmt, s);
 }
 
-size_t latent_ws_bytes(long n, long T, int hq, int D) {
-  return (size_t)kLatGrid * (2 * lat_part_floats(D, lat_rows(n, T, hq)) * 4 + 16);
+size_t latent_ws_bytes(int D) {
+  return (size_t)kLatGrid * (2 * lat_part_floats(D) * 4 + 16);
 }
 
 hipError_t launch_attn_latent(const AttnArgs& all, int fmt, hipStream_t s) {
-  const int R = lat_rows(all.n, all.T, all.hq), D = all.c.D;
+  const int D = all.c.D;
   // a workgroup keeps the prefix sums of its launch's sequences in LDS
   for (long b = 0; b < all.n; b += kLatSeqs) {
     AttnArgs a = all;
@@ -135,15 +133,15 @@ hipError_t launch_attn_latent(const AttnArgs& all, int fmt, hipStream_t s) {
       if (a.lse) a.lse += b * a.hq;
       if (a.parent) a.parent += b;
     }
-    a.meta = (int*)(a.part + kLatGrid * 2 * lat_part_floats(D, R));
+    a.meta = (int*)(a.part + kLatGrid * 2 * lat_part_floats(D));
     // no more workgroups than the table's longest contexts can keep busy
-    const long tiles = a.cu ? a.T * a.hq / R + a.n : a.n * (((long)a.hq + R - 1) / R);
+    const long tiles = a.cu ? a.T * a.hq / kLatRows + a.n
+                            : a.n * (((long)a.hq + kLatRows - 1) / kLatRows);
     const long units = tiles * ((long)a.t.max_pages * a.t.ps / 32 + 1);
     const long want = (units + kLatMinUnits - 1) / kLatMinUnits;
     const int grid = (int)(want < kLatGrid ? want : kLatGrid);
-    const auto run = D == 256 ? (R == 32 ? launch_latent_256_32 : launch_latent_256_64)
-                              : (R == 32 ? launch_latent_512_32 : launch_latent_512_64);
-    const hipError_t e = run(a, fmt, grid, s);
+    const hipError_t e = D == 256 ? launch_latent_256(a, fmt, grid, s)
+                                  : launch_latent_512(a, fmt, grid, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -64,6 +64,34 @@ __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
+// Loads of 16 bytes a lane from base + off + at straight into LDS, lane l's to LDS
+// address `to` + 16 l (base, off and to alike in the wave; the offsets below 2^31). In
+// assembly, since the compiler takes loads into one array of LDS for loads into
+// any, and would wait for those in flight wherever LDS is read; they are to be
+// waited for by count (wait_counts), before a barrier if other waves read them. A
+// buffer load: global ones count as flat, and wait_counts would not do.
+__device__ __forceinline__ uint32_t lds_of(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// Those at offsets from `bytes` on read nothing and write zeros.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t bytes, int at, int off,
+                                            uint32_t to) {
+  const uint64_t b = (uint64_t)base;
+  const u32x4 rsrc = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, bytes, 0x00020000u};
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(rsrc), "s"(off)
+               : "memory", "m0");
+}
+
+// The same from an address of each lane's own.
+__device__ __forceinline__ void load_lanes_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
+               : "memory", "m0");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // A value of the result, of the sum l of its row's probabilities: 0 without one,

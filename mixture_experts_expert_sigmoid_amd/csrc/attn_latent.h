@@ -13,7 +13,7 @@ namespace {
 struct LatSeq {
   int q0, m, slot, L, C;       // first row of q, new tokens; slot, tokens, those before
   int ng1, b2, nb;             // 16-key groups 0..ng1-1, then b2 and on; 32-key tiles of them
-  int tiles;                   // of R rows
+  int tiles;                   // of kLatRows rows
   int lo_min;
 };
 
@@ -23,7 +23,6 @@ __device__ __forceinline__ int lat_cu(const AttnArgs& a, int i) {
   return c < 0 ? 0 : (c > a.T ? (int)a.T : c);
 }
 
-template <int R>
 __device__ __forceinline__ LatSeq lat_seq(const AttnArgs& a, int i) {
   LatSeq s;
   s.q0 = lat_cu(a, i);
@@ -42,7 +41,7 @@ __device__ __forceinline__ LatSeq lat_seq(const AttnArgs& a, int i) {
   s.b2 = s.lo_min / 16;
   s.ng1 = min(s.b2, (min(a.first, s.lo_min) + 15) / 16);
   s.nb = max(1, (s.ng1 + max(0, (s.L + 15) / 16 - s.b2) + 1) / 2);
-  s.tiles = (int)(((long)s.m * a.hq + R - 1) / R);
+  s.tiles = (int)(((long)s.m * a.hq + kLatRows - 1) / kLatRows);
   return s;
 }
 
@@ -59,32 +58,53 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
-template <bool BF, bool F8, int DC, int R>
-__global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
+// Waits until at most VM of the wave's vector memory operations and LGKM of its
+// reads and writes of LDS are in flight (63 and 15: however many).
+template <int VM, int LGKM>
+__device__ __forceinline__ void wait_counts() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | LGKM << 8 | (VM >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
+// A barrier for LDS alone: loads stay in flight (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() {
+  wait_counts<63, 0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <bool BF, bool F8, int DC>
+__global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs a) {
+  constexpr int R = kLatRows, NW = kLatWaves;
   constexpr int ES = F8 ? 1 : 2;
   constexpr int RB = DC * ES, UPR = RB / 16;              // bytes and units of a latent row
   constexpr int RRB = kLatRope * ES, URR = RRB / 16;      // of a rotary one
   constexpr int TB = 32 * (RB + RRB);                     // a tile of 32 keys
-  constexpr int RPL = 64 / UPR, NLD = 8 / RPL;            // rows of a load; loads of 8 rows
-  constexpr int NK = (DC + kLatRope) / 32;                // steps of the first product
-  constexpr int RQ = R / 32;                              // a wave's 16-row tiles in it
-  constexpr int RT = R / 32;                              // 32-row tiles in the second
-  constexpr int ND = DC / 128;                            // a wave's 32-row tiles of O^T
+  constexpr int RPW = 32 / NW;                            // rows of it that a wave brings
+  constexpr int RPL = 64 / UPR, NLD = RPW / RPL;          // rows of a load; loads
   constexpr int LOADS = NLD + 1;
+  constexpr int NK = (DC + kLatRope) / 32;                // steps of the first product
+  constexpr int QR = 2 * R / NW;                          // a wave's rows in it
+  constexpr int RT = R / 32;                              // 32-row tiles in the second
+  constexpr int ND = DC / 32 / NW;                        // a wave's 32-row tiles of O^T
+  constexpr int QB = R * (DC + kLatRope) * 2;             // the queries
+  static_assert(QR == 16 && ND >= 1 && NLD >= 1, "a wave's shares");
 
-  __shared__ __align__(16) char s_t0[TB], s_t1[TB], s_t2[TB], s_t3[TB];
-  __shared__ __align__(16) char s_p0[R * 64], s_p1[R * 64];
+  __shared__ __align__(16) char s_t[4][TB];               // tile x in (x - first) % 4
+  __shared__ __align__(16) char s_q[F8 ? QB : 16];        // the queries, or in the last two tiles
+  __shared__ __align__(16) char s_p[2][R * 64];           // P of tile x in x % 2
+  static_assert(F8 || 2 * TB == QB, "two tiles hold the queries");
   __shared__ long s_pref[kLatSeqs + 1];
   __shared__ TreeRows<R> s_tree;
   __shared__ float s_m[R], s_f[R], s_lm[2][R], s_l[2][R];
-  __shared__ long s_scan[4];
-  __shared__ int s_flag[2];                      // the tile whose P is to be done again
-  __shared__ int s_bad;                          // values that are not finite were taken out
-  __shared__ int s_gone[4];                      // tile x with a group that has no page, by x % 4
+  __shared__ long s_scan[NW];
+  // by x % 8: tile x if its P is to be done again; if a group of it has no page
+  __shared__ __align__(8) int s_tell[8][2];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kq = w >> 1, rq = w & 1;
+  const int kq = w / (NW / 2), rq = w % (NW / 2);         // its 16 keys, its 16 rows
   const int lc = lane & 15, g4 = lane >> 4, half = lane >> 5, l31 = lane & 31;
   const int H = a.hq;
 
@@ -92,7 +112,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
   {
     long v = 0;
     if (tid < a.n) {
-      const LatSeq s = lat_seq<R>(a, tid);
+      const LatSeq s = lat_seq(a, tid);
       v = (long)s.tiles * s.nb;
     }
     for (int d = 1; d < 64; d <<= 1) {
@@ -114,8 +134,13 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
   int* const meta = a.meta + 4 * wg;
   if (tid == 0) meta[2] = 0;
   if (wg >= W) return;
-  long u = wg * U / W;
-  const long u_end = (wg + 1) * U / W;
+  // workgroup v starts at unit v U / W, whole and rest by themselves
+  const uint32_t w32 = (uint32_t)W;
+  const long each = U >> 32 ? U / W : (uint32_t)U / w32;
+  const uint32_t rest = (uint32_t)(U - each * W);
+  auto start_of = [&](int v) { return v * each + v * rest / w32; };
+  long u = start_of(wg);
+  const long u_end = start_of(wg + 1);
   int seq = 0;
   for (int hi = a.n - 1; seq < hi;) {
     const int mid = (seq + hi + 1) >> 1;
@@ -125,26 +150,47 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
 
   const float sc = F8 ? a.scale * a.c.ks[0] : a.scale;
 
-  // Swizzles: the 16-byte units of a row lie turned by its number, so that the
-  // reads of 8 rows' same unit (K), and those of four rows' next two units, or
-  // eight rows' one (V, transposed), fall into different banks.
-  auto swz = [](int r) { return F8 ? r & 7 : (r & 3) << 1 | (r >> 2 & 1); };
-  auto swz_r = [&](int r) { return F8 ? r >> 1 & 3 : swz(r); };
-  const int k_row = 16 * kq + lc;
-  int k_at = k_row * RB + 16 * (g4 ^ swz(k_row));
+  // Swizzles: the 16-byte units of a row lie turned by its number, so that what is
+  // read at a time -- the same unit of 16 rows (K, P), the next four units of four
+  // rows or the next two of eight (V, transposed) -- lies in different banks.
+  auto swz = [](int r) {
+    return F8 ? (r & 7) << 1 | (r >> 3 & 1) : (r & 3) << 2 | (r >> 2 & 3);
+  };
+  auto swz_r = [](int r) { return F8 ? r >> 2 & 3 : r >> 1 & 7; };
+  auto p_swz = [](int r) { return r >> 2 & 3; };
+  // Operands' places in a tile, of which one turn of the swizzle takes 256 bytes:
+  // a register for each place within those, the rest by constant distances
+  const int k_row = 16 * kq + lc, v_row = 8 * half + (F8 ? lc >> 1 : lc >> 2);
+  int k_at[4], v_at[ND][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k_at[j] = k_row * RB + 16 * ((4 * j + g4) ^ swz(k_row));
   int kr_at = 32 * RB + k_row * RRB + 16 * (g4 ^ swz_r(k_row));
-  const int v_row = 8 * half + (F8 ? lc >> 1 : lc >> 2);
-  const int v_u = F8 ? g4 & 1 : 2 * (g4 & 1) + (lc >> 1 & 1);
-  int v_at = (v_row * RB + 16 * (v_u ^ swz(v_row)) + 8 * (lc & 1)) ^ (w * ND * 32 * ES);
-  auto p_swz = [](int r) { return r >> 1 & 3; };
-  const int p_to = (rq * (R / 2) + lc) * 64 + 16 * ((2 * kq + (g4 >> 1)) ^ p_swz(lc)) + 8 * (g4 & 1);
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = (w * ND + d) * 32 * ES;
+      const int un = F8 ? g4 & 1 : 2 * (g4 & 1) + (lc >> 1 & 1);
+      const int r = v_row + 4 * h;
+      v_at[d][h] = r * RB + at / 256 * 256 + 16 * ((at % 256 / 16 + un) ^ swz(r)) + 8 * (lc & 1);
+    }
+  // this lane's unit in a wave's loads of RPW rows: load i takes RPL of them (the
+  // swizzles are exclusive ors of row bits)
+  const int l_from = w % (NW / 2) * RPW;                  // row of the group
+  const int l_row = lane / UPR * (int)a.c.st;
+  const int l_unit = 16 * (lane % UPR ^ swz(l_from + lane / UPR));
+  const int l_rope = lane / URR * (int)a.c.st + RB + 16 * (lane % URR ^ swz_r(l_from + lane / URR));
+  const int p_to = (rq * QR + lc) * 64 + 16 * ((2 * kq + (g4 >> 1)) ^ p_swz(lc)) + 8 * (g4 & 1);
   const int p_from = l31 * 64 + 16 * (half ^ p_swz(l31));
 
   while (u < u_end) {
     while (s_pref[seq + 1] <= u) ++seq;
-    const LatSeq s = lat_seq<R>(a, seq);
+    seq = __builtin_amdgcn_readfirstlane(seq);   // (alike in all lanes: told so)
+    const LatSeq s = lat_seq(a, seq);
     const long rel = u - s_pref[seq];
-    const int tile = (int)(rel / s.nb), b0 = (int)(rel - (long)tile * s.nb);
+    const int tile = __builtin_amdgcn_readfirstlane(
+        rel >> 32 ? (int)(rel / s.nb) : (int)((uint32_t)rel / (uint32_t)s.nb));
+    const int b0 = __builtin_amdgcn_readfirstlane((int)(rel - (long)tile * s.nb));
     const int b1 = (int)min((long)s.nb, b0 + (u_end - u));
     const int rows = s.m * H, r0 = tile * R;
     const int tok0 = r0 / H, tok1 = (min(rows, r0 + R) - 1) / H;
@@ -163,30 +209,11 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
     __syncthreads();                             // of the piece before
     if (masked) s_tree.fetch(a.parent + s.q0, s.m);
     if (tid < R) s_m[tid] = kNegInf;
-    if (tid < 2) s_flag[tid] = -1;
-    if (tid < 4) s_gone[tid] = -1;
-    if (tid == 0) s_bad = 0;
+    if (tid < 16) s_tell[tid >> 1][tid & 1] = -1;
 
-    // this lane's rows in the first product
-    int tok[RQ];
-    u32x4 q[RQ][NK];
-#pragma unroll
-    for (int t = 0; t < RQ; ++t) {
-      const int r = r0 + rq * (R / 2) + 16 * t + lc;
-      tok[t] = r < rows ? r / H : -1;
-    }
-    auto read_q = [&](int t, auto put) __attribute__((always_inline)) {
-      const int r = here(r0 + rq * (R / 2) + 16 * t + lc);
-      const char* src = a.q + (long)(s.q0 + max(0, tok[t])) * a.q_row +
-                        (r < rows ? r - tok[t] * H : 0) * a.q_head;
-#pragma unroll
-      for (int c = 0; c < NK; ++c) {
-        const int d = F8 ? 64 * (c >> 1) + 16 * g4 + 8 * (c & 1) : 32 * c + 8 * g4;
-        put(c, *(const u32x4*)(src + 2 * d));
-      }
-    };
-#pragma unroll
-    for (int t = 0; t < RQ; ++t) read_q(t, [&](int c, const u32x4& y) { q[t][c] = y; });
+    // this lane's row in the first product
+    const int my_row = r0 + rq * QR + lc;
+    const int tok = my_row < rows ? my_row / H : -1;
     f32x16 o[ND][RT];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -194,12 +221,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][t][i] = 0.0f;
-    float m[RQ], l[RQ], pend[RQ];
-#pragma unroll
-    for (int t = 0; t < RQ; ++t) {
-      m[t] = kNegInf;
-      l[t] = pend[t] = 0.0f;
-    }
+    float m = kNegInf, l = 0.0f, pend = 0.0f;
 
     // Byte offset in the cache of the wave's group (the one it brings rows of
     // and has the scores of) in the next 64 tiles, a tile a lane
@@ -213,9 +235,12 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       return e >= 0 && e < a.t.n_pages ? e * a.c.sp + (key - i * a.t.ps) * a.c.st : kMissing;
     };
     long offs = lookup(b0 + lane);
-    int state1 = 0, state2 = 0;                  // of tiles x + 1, x + 2: < 0 without a page
+    int state1 = 0, state2 = 0, state3 = 0;      // of tiles x + 1 and on: < 0 without a page
 
-    auto issue = [&](int x, char* to) __attribute__((always_inline)) {          // x ascending
+    // The place of tile x (ascending) and its state; load i of LOADS of it
+    const char* src = a.c.k;
+    uint32_t bytes = 0;
+    auto place = [&](int x) __attribute__((always_inline)) {
       if (x - at0 >= 64) {
         at0 = x;
         offs = lookup(x + lane);
@@ -223,108 +248,123 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       const uint32_t lo32 = __builtin_amdgcn_readlane((int)offs, x - at0);
       const int hi32 = __builtin_amdgcn_readlane((int)(offs >> 32), x - at0);
       const long off = (long)(((uint64_t)(uint32_t)max(hi32, 0) << 32) | lo32);
-      const char* src = a.c.k + (hi32 < 0 ? 0L : off) + (w & 1) * 8 * a.c.st;
+      src = a.c.k + (hi32 < 0 ? 0L : off) + l_from * a.c.st;
+      bytes = hi32 < 0 ? 0 : 0x7FFFFFFF;         // (nothing is read without a place)
       if (hi32 == (int)(kMissing >> 32) && lane == 0) {
         atomicOr(a.err, kErrPage);
-        s_gone[x & 3] = x;
-      }
-      const int ln = here(lane);
-#pragma unroll
-      for (int i = 0; i < NLD; ++i) {
-        const int r = i * RPL + ln / UPR;
-        const uint32_t f = (uint32_t)(ln / UPR) * (uint32_t)a.c.st + 16 * (ln % UPR ^ swz(r));
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(src + i * RPL * a.c.st + f),
-            (__attribute__((address_space(3))) void*)(to + (8 * w + i * RPL) * RB), 16, 0, 0);
-      }
-      if (lane < 8 * URR) {
-        const int r = ln / URR;
-        const uint32_t f = (uint32_t)r * (uint32_t)a.c.st + RB + 16 * (ln % URR ^ swz_r(r));
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(src + f),
-            (__attribute__((address_space(3))) void*)(to + 32 * RB + 8 * w * RRB), 16, 0, 0);
+        s_tell[x & 7][1] = x;
       }
       return hi32;
     };
+    auto load = [&](int x, int i) __attribute__((always_inline)) {
+      const uint32_t to = lds_of(s_t) + ((x - b0) & 3) * TB;
+      if (i < NLD)
+        load_to_lds(src, bytes, here(l_row + (l_unit ^ 16 * swz(i * RPL))), i * RPL * (int)a.c.st,
+                    to + (RPW * w + i * RPL) * RB);
+      else if (lane < RPW * URR)
+        load_to_lds(src, bytes, l_rope, 0, to + 32 * RB + RPW * w * RRB);
+    };
+    auto issue = [&](int x) __attribute__((always_inline)) {
+      const int state = place(x);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) load(x, i);
+      return state;
+    };
     auto arrived = [&](auto left) __attribute__((always_inline)) {              // all but the newest `left` tiles
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(left)::value * LOADS) : "memory");
+      wait_counts<decltype(left)::value * LOADS, 15>();
+    };
+
+    // The queries, loaded as rows into LDS, turned as keys are in a 16-bit tile
+    auto q_swz = [](int r) { return (r & 3) << 2 | (r >> 2 & 3); };
+    char* const qa = F8 ? s_q : s_t[2];
+    auto issue_q = [&] {
+      const int lane = here(tid & 63);
+      constexpr int QU = DC / 8, QL = 64 / QU, QW = R / NW;        // units, rows of a load, of a wave
+      auto from = [&](int r, int un) {
+        const int g = min(r0 + r, rows - 1), tk = g / H;
+        return a.q + (long)(s.q0 + tk) * a.q_row + (g - tk * H) * a.q_head + 16 * un;
+      };
+#pragma unroll
+      for (int i = 0; i < QW / QL; ++i) {
+        const int r = w * QW + i * QL + lane / QU;
+        load_lanes_to_lds(from(r, lane % QU ^ q_swz(r)), lds_of(qa) + (w * QW + i * QL) * DC * 2);
+      }
+      const int r = w * QW + lane / 8;
+      static_assert(QW == 8, "a load for a wave's rotary rows");
+      load_lanes_to_lds(from(r, QU + (lane % 8 ^ (r >> 1 & 7))),
+                        lds_of(qa) + R * DC * 2 + w * QW * 128);
+    };
+    u32x4 q[NK];
+    auto take_q = [&] {
+      const int ln = here(lane), lc = ln & 15, g4 = ln >> 4, r = rq * QR + lc;
+#pragma unroll
+      for (int c = 0; c < NK; ++c) {
+        // values from 32 c + 8 g4 on; e4m3: as a unit of 16 keeps them for two steps
+        const int un = F8 ? 8 * (c >> 1) + 2 * g4 + (c & 1) : 4 * c + g4;
+        q[c] = *(const u32x4*)(qa + (32 * c < DC
+                                         ? r * DC * 2 + 16 * (un ^ q_swz(r))
+                                         : R * DC * 2 + r * 128 + 16 * ((un & 7) ^ (r >> 1 & 7))));
+      }
     };
 
     // Operands of S^T = K Q^T: this wave's 16 keys. Read i is step i, or for e4m3
     // steps 2 i and 2 i + 1.
     constexpr int KS = F8 ? 2 : 1, MK = NK / KS, ML = DC / 32 / KS;
     auto read_k = [&](const char* kt, int i) __attribute__((always_inline)) {
-      return *(const u32x4*)(kt + (i < ML ? k_at ^ (64 * i) : kr_at ^ (64 * (i - ML))));
+      return *(const u32x4*)(i < ML ? kt + k_at[i & 3] + 256 * (i >> 2)
+                             : i == ML ? kt + kr_at : kt + (kr_at ^ 64));
     };
-    auto step_k = [&](const u32x4& raw, int e) __attribute__((always_inline)) {
-      if constexpr (F8)
-        return u32x4{from_e4m3<BF, false>(raw[2 * e]), from_e4m3<BF, true>(raw[2 * e]),
-                     from_e4m3<BF, false>(raw[2 * e + 1]), from_e4m3<BF, true>(raw[2 * e + 1])};
-      else
-        return raw;
-    };
-    auto use_k = [&](f32x4 (&sv)[RQ], const u32x4& raw, int i) __attribute__((always_inline)) {
+    auto use_k = [&](f32x4 (&sv)[2], const u32x4& raw, int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < KS; ++e) {
-        const u32x4 ka = step_k(raw, e);
-#pragma unroll
-        for (int t = 0; t < RQ; ++t)
-          sv[t] = mfma16<BF>(ka, q[t][KS * i + e], i + e == 0 ? f32x4{0, 0, 0, 0} : sv[t]);
+        u32x4 ka = raw;
+        if constexpr (F8)
+          ka = u32x4{from_e4m3<BF, false>(raw[2 * e]), from_e4m3<BF, true>(raw[2 * e]),
+                     from_e4m3<BF, false>(raw[2 * e + 1]), from_e4m3<BF, true>(raw[2 * e + 1])};
+        const int c = KS * i + e;                // two sums, of the even and the odd steps
+        sv[c & 1] = mfma16<BF>(ka, q[c], c < 2 ? f32x4{0, 0, 0, 0} : sv[c & 1]);
       }
     };
-    // scales and masks them
-    auto mask = [&](f32x4 (&sv)[RQ], int x, int state) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < RQ; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sv[t][i] *= sc;
-      if (whole(x) && state >= 0) return;
+    // masks the scores of a tile that is not whole
+    auto mask = [&](f32x4& sv, int x, int state) __attribute__((always_inline)) {
       const int key = group_key(2 * x + kq) + 4 * g4;
-#pragma unroll
-      for (int t = 0; t < RQ; ++t) {
-        uint32_t bits = 0;                       // the lane's four keys among the drafted tokens
-        int end = s.C + tok[t] + 1, pos = end - 1;
-        if (tree) {
-          end = s.C;
-          pos = end;
-          if (masked && tok[t] >= 0) {
-            pos += s_tree.depth(tok[t] - tok0);
-            bits = (uint32_t)s_tree.bits(tok[t] - tok0, key - s.C) & 15;
-          }
-        }
-        const int lo = a.window ? pos - a.window + 1 : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = key + i;
-          const bool ok = ((j < end) & ((j >= lo) | (j < a.first))) | (bits >> i & 1);
-          sv[t][i] = ok & (tok[t] >= 0) & (state >= 0) ? sv[t][i] : kNegInf;
+      uint32_t bits = 0;                         // the lane's four keys among the drafted tokens
+      int end = s.C + tok + 1, pos = end - 1;
+      if (tree) {
+        end = s.C;
+        pos = end;
+        if (masked && tok >= 0) {
+          pos += s_tree.depth(tok - tok0);
+          bits = (uint32_t)s_tree.bits(tok - tok0, key - s.C) & 15;
         }
       }
+      const int lo = a.window ? pos - a.window + 1 : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = key + i;
+        const bool ok = ((j < end) & ((j >= lo) | (j < a.first))) | (bits >> i & 1);
+        sv[i] = ok & (tok >= 0) & (state >= 0) ? sv[i] : kNegInf;
+      }
     };
-    auto tops = [&](const f32x4& sv) {
+    auto top_of = [&](const f32x4& sv) {
       return max_across_rows(fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])));
     };
-    // P from the scores and the row's maximum m, and its sum
-    auto probs = [&](const f32x4 (&sv)[RQ], char* to) __attribute__((always_inline)) {
+    // P of tile x from the scores and the row's maximum m, and its sum
+    auto probs = [&](const f32x4& sv, int x) __attribute__((always_inline)) {
+      const float neg = m == kNegInf ? 0.0f : pre_lift<BF>(m) - m;
+      float p[4];
 #pragma unroll
-      for (int t = 0; t < RQ; ++t) {
-        const float neg = m[t] == kNegInf ? 0.0f : pre_lift<BF>(m[t]) - m[t];
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = exp2_fast(sv[t][i] + neg);
-        pend[t] = (p[0] + p[1]) + (p[2] + p[3]);
-        *(u32x2*)(to + (p_to + 16 * 64 * t)) = u32x2{pack16<BF>(p[0], p[1]), pack16<BF>(p[2], p[3])};
-      }
+      for (int i = 0; i < 4; ++i) p[i] = exp2_fast(sv[i] + neg);
+      pend = (p[0] + p[1]) + (p[2] + p[3]);
+      *(u32x2*)(s_p[x & 1] + p_to) = u32x2{pack16<BF>(p[0], p[1]), pack16<BF>(p[2], p[3])};
     };
     // lets m, l and O follow the maximum, after a barrier behind soft(); ends in
     // a barrier
-    auto follow = [&](const f32x4 (&sv)[RQ], char* to) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < RQ; ++t) {
-        const float top = tops(sv[t]);
-        if (g4 == 0) s_lm[kq][rq * (R / 2) + 16 * t + lc] = top;
-      }
-      __syncthreads();
+    auto follow = [&](const f32x4& sv, int x) __attribute__((always_inline)) {
+      const int r = rq * QR + lc;
+      const float top = top_of(sv);
+      if (g4 == 0) s_lm[kq][r] = top;
+      lds_barrier();
       if (tid < R) {
         const float old = s_m[tid], now = fmaxf(old, fmaxf(s_lm[0][tid], s_lm[1][tid]));
         float df = old - (now == kNegInf ? 0.0f : now);
@@ -332,13 +372,9 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
         s_f[tid] = exp2_fast(df);
         s_m[tid] = now;
       }
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < RQ; ++t) {
-        const int r = rq * (R / 2) + 16 * t + lc;
-        m[t] = s_m[r];
-        l[t] *= s_f[r];
-      }
+      lds_barrier();
+      m = s_m[r];
+      l *= s_f[r];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const float f = s_f[32 * t + l31];
@@ -347,8 +383,8 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[d][t][i] *= f;
       }
-      probs(sv, to);
-      __syncthreads();
+      probs(sv, x);
+      lds_barrier();
     };
     // Operand of O^T += V^T P^T: 16 keys (ks) of 32 values
     auto read_v = [&](const char* vt, int ks, int d) __attribute__((always_inline)) {
@@ -356,15 +392,14 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       u32x4 va = {0, 0, 0, 0};
       if constexpr (F8) {
         const auto y = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(p + (v_at ^ (32 * d))));
+            (__attribute__((address_space(3))) i32x2*)(p + v_at[d][0]));
         va[0] = y[0];
         va[1] = y[1];
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(p + 4 * h * RB +
-                                                         ((v_at ^ (64 * d)) ^ (16 * h))));
+              (__attribute__((address_space(3))) s16x4*)(p + v_at[d][h]));
           const u32x2 z = __builtin_bit_cast(u32x2, y);
           va[2 * h] = z[0];
           va[2 * h + 1] = z[1];
@@ -372,30 +407,20 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       }
       return va;
     };
-    // S^T of tile x (sn, from kt) if QK, the product of the tile before (vt) with
-    // its P (pt) if PV, and then P of tile x (to pn), computed with the rows'
-    // maxima of before: if one has grown too much the flag is set, and follow()
-    // does it again. One operand after another, each with the read of the one that
-    // is due kAhead later and a share of the softmax; the order is kept as written.
-    constexpr int kAhead = 4;
-    auto products = [&](auto qk, auto pv, f32x4 (&sn)[RQ], int x, int state, const char* kt,
-                        const char* vt, const char* pt, char* pn, int* flag)
+    // S^T of tile x if QK, the product of the tile before with its P if PV. One
+    // operand after another, each with the read of the one that is due kAhead
+    // later and a share of the rest: beside(i) behind the first product's operand
+    // i, the steps of soft() behind those of the second. The order is kept as
+    // written. False if beside() was: nothing but scores has changed.
+    constexpr int kAhead = 4, kSoft = 3;
+    auto products = [&](auto qk, auto pv, f32x4& sum, int x, auto beside, auto soft)
         __attribute__((always_inline)) {
       constexpr int MQ = decltype(qk)::value ? MK : 0, MV = decltype(pv)::value ? 2 * ND : 0;
-      asm volatile("" : "+v"(k_at), "+v"(kr_at), "+v"(v_at));   // not kept for every step
+      const char *kt = s_t[(x - b0) & 3], *vt = s_t[(x - b0 - 1) & 3], *pt = s_p[(x - 1) & 1];
       u32x4 op[MQ + MV], pb[2][RT];
+      f32x4 sn[2];
       auto read = [&](int i) __attribute__((always_inline)) {
         op[i] = i < MQ ? read_k(kt, i) : read_v(vt, (i - MQ) / ND, (i - MQ) % ND);
-      };
-      auto soft = [&](int i) __attribute__((always_inline)) {
-        if (i == 0) mask(sn, x, state);
-        if (i == 1) {
-          bool more = false;
-#pragma unroll
-          for (int t = 0; t < RQ; ++t) more |= tops(sn[t]) > m[t] + kDefer<BF>;
-          if (__any(more) && lane == 0) *flag = x;
-        }
-        if (i == 2) probs(sn, pn);
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) read(i);
@@ -412,6 +437,8 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
         }
         if (i < MQ) {
           use_k(sn, op[i], i);
+          if (!beside(i)) return false;
+          if (i == MQ - 1) sum = sn[0] + sn[1];
         } else {
           const int ks = (i - MQ) / ND, d = (i - MQ) % ND;
           u32x4 va = op[i];
@@ -420,25 +447,47 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
                        from_e4m3<BF, false>(op[i][1]), from_e4m3<BF, true>(op[i][1])};
 #pragma unroll
           for (int t = 0; t < RT; ++t) o[d][t] = mfma32<BF>(va, pb[ks][t], o[d][t]);
-          if (MQ) soft(i - MQ);
+          soft(i - MQ);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (MQ && !MV) {
+      if (MQ && MV) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) soft(i);
+        for (int i = MV; i < kSoft; ++i) soft(i);
       }
+      return true;
+    };
+    // P of tile x from its scores and the rows' maxima of before, in three steps; if
+    // one has grown too much that is told, and follow() does it again
+    auto soft = [&](f32x4& sv, int x, bool tell, int i) __attribute__((always_inline)) {
+      if (i == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sv[e] *= sc;
+      }
+      if (i == 1) {
+        const bool more = top_of(sv) > m + kDefer<BF>;
+        if (tell & __any(more) && lane == 0) s_tell[x & 7][0] = x;
+      }
+      if (i == 2) probs(sv, x);
+    };
+    // the last two of them again for a tile that is not whole
+    auto soft_masked = [&](f32x4& sv, int x, int state) __attribute__((always_inline)) {
+      mask(sv, x, state);
+      soft(sv, x, true, 1);
+      soft(sv, x, true, 2);
     };
 
-    // Values that are not finite, of a tile that not every row sees, are taken out
-    // and brought back after the loop, for the rows that see them.
+    // Values that are not finite are taken out of a tile that not every row sees.
+    // Those that do see one have a score that is not finite either: NaN or
+    // infinity, and so have the row's sum and all of its result, or -infinity,
+    // and the key does not enter.
     auto bad16 = [](uint32_t x) {
       constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
       return (x & e) == e;
     };
     auto clean = [&](char* vt) {
-      for (int i = here(lane); i < 8 * UPR; i += 64) {
-        u32x4* at = (u32x4*)(vt + 8 * w * RB + 16 * i);
+      for (int i = lane; i < RPW * UPR; i += 64) {
+        u32x4* at = (u32x4*)(vt + RPW * w * RB + 16 * i);
         const u32x4 y = *at;
         u32x4 z = y;
 #pragma unroll
@@ -452,140 +501,105 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
             if (bad16(y[e] >> 16)) z[e] &= 0x0000FFFFu;
           }
         }
-        if (((y[0] ^ z[0]) | (y[1] ^ z[1])) | ((y[2] ^ z[2]) | (y[3] ^ z[3]))) {
-          *at = z;
-          s_bad = 1;
-        }
+        if (((y[0] ^ z[0]) | (y[1] ^ z[1])) | ((y[2] ^ z[2]) | (y[3] ^ z[3]))) *at = z;
       }
-      __syncthreads();
+      lds_barrier();
     };
 
-    f32x4 sa[RQ];
+    f32x4 sa = {0, 0, 0, 0};                     // scores of tile x
     int x = b0;
-    // Tile x: its P stands in px, computed with the maxima of before unless
-    // flagged. Scores and P (pn) of tile x + 1, the product of tile x, and the
-    // loads of tile x + 3 into the room of tile x - 1.
-    auto settle = [&](char* vt, char* px, const int* flag) __attribute__((always_inline)) {
-      const bool again = *(volatile const int*)flag == x;
-      const bool gone = *(volatile const int*)&s_gone[x & 3] == x;
-      if (__builtin_amdgcn_readfirstlane(again)) follow(sa, px);
-#pragma unroll
-      for (int t = 0; t < RQ; ++t) l[t] += pend[t];
-      if (__builtin_amdgcn_readfirstlane(gone || !whole(x))) clean(vt);
-    };
-    auto step = [&](char* __restrict vt, char* __restrict kt, char* __restrict to,
-                    char* __restrict px, char* __restrict pn, const int* fx, int* fn) __attribute__((always_inline)) {
-      if (x + 2 < x_end) arrived(std::integral_constant<int, 1>{});
-      else arrived(std::integral_constant<int, 0>{});
-      __syncthreads();
-      const int st = state1;
-      state1 = state2;
-      settle(vt, px, fx);
-      if (x + 3 < x_end) state2 = issue(x + 3, to);
-      products(std::true_type{}, std::true_type{}, sa, x + 1, st, kt, vt, px, pn, fn);
-      ++x;
-    };
-    auto last = [&](char* vt, char* px, const int* fx) __attribute__((always_inline)) {
-      __syncthreads();
-      settle(vt, px, fx);
-      products(std::false_type{}, std::true_type{}, sa, x, 0, nullptr, vt, px, nullptr, nullptr);
-    };
     if (b0 < x_end) {
-      const int st = issue(b0, s_t0);
-      if (b0 + 1 < x_end) state1 = issue(b0 + 1, s_t1);
-      if (b0 + 2 < x_end) state2 = issue(b0 + 2, s_t2);
-      __syncthreads();                           // the parents; s_gone
-      if (masked)
-        s_tree.build(tok0, min(s.m, tok1 + 1), s.C, a.window, a.first, a.err);
-      arrived(std::integral_constant<int, 0>{});
-      __syncthreads();
-      products(std::true_type{}, std::false_type{}, sa, b0, st, s_t0, nullptr, nullptr, s_p0,
-               &s_flag[0]);
-      char *vt = s_t0, *px = s_p0;
-      const int* fx = &s_flag[0];
-      while (x + 1 < x_end) {
-        step(s_t0, s_t1, s_t3, s_p0, s_p1, &s_flag[0], &s_flag[1]);
-        vt = s_t1, px = s_p1, fx = &s_flag[1];
-        if (x + 1 >= x_end) break;
-        step(s_t1, s_t2, s_t0, s_p1, s_p0, &s_flag[1], &s_flag[0]);
-        vt = s_t2, px = s_p0, fx = &s_flag[0];
-        if (x + 1 >= x_end) break;
-        step(s_t2, s_t3, s_t1, s_p0, s_p1, &s_flag[0], &s_flag[1]);
-        vt = s_t3, px = s_p1, fx = &s_flag[1];
-        if (x + 1 >= x_end) break;
-        step(s_t3, s_t0, s_t2, s_p1, s_p0, &s_flag[1], &s_flag[0]);
-        vt = s_t0, px = s_p0, fx = &s_flag[0];
-      }
-      last(vt, px, fx);
-    }
-
-    // The values taken out: the scores and P of their tiles once more, and their
-    // products with the probabilities that are not zero one by one.
-    __syncthreads();
-    if (s_bad) {
-      auto to_f32 = [](uint32_t x) {
-        return BF ? bf16_bits_to_f32(x) : (float)__builtin_bit_cast(_Float16, (uint16_t)x);
+      int st = issue(b0);
+      issue_q();
+      state1 = issue(b0 + 1);
+      arrived(std::integral_constant<int, 1>{});
+      lds_barrier();                             // the first tile, the queries, parents, s_tell
+      take_q();
+      if (masked) s_tree.build(tok0, min(s.m, tok1 + 1), s.C, a.window, a.first, a.err);
+      lds_barrier();                             // all queries taken
+      state2 = issue(b0 + 2);
+      state3 = place(b0 + 3);
+      bool plain = whole(x) && st >= 0;
+      products(std::true_type{}, std::false_type{}, sa, x, [](int) { return true; }, [](int) {});
+#pragma unroll
+      for (int i = 0; i < kSoft; ++i) soft(sa, x, plain, i);
+      if (!plain) soft_masked(sa, x, st);
+      // Tile x: its P stands in LDS, computed with the maxima of before unless told
+      // otherwise. A step computes the scores and P of tile x + 1 and the product
+      // of tile x, and starts the loads of tile x + 3 into the room of tile x - 1
+      // (behind the last tile, loads of nothing, so that the count stays the same).
+      // (A loop of its own, left where something rare is to be done about tile x
+      // first: with that in it, O would be copied from registers to registers in
+      // each step.)
+      auto told_of = [&](int x) {
+        return *(const volatile __attribute__((address_space(3))) i32x2*)
+            (const __attribute__((address_space(3))) int*)s_tell[x & 7];
       };
-      at0 = b0;
-      offs = lookup(b0 + lane);
-      for (int xx = b0; xx < x_end; ++xx) {
-        if (whole(xx)) continue;                 // (of one without a page: nothing is seen)
-        const int st = issue(xx, s_t0);
-        arrived(std::integral_constant<int, 0>{});
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < RQ; ++t) {
-          sa[t] = f32x4{0, 0, 0, 0};
-          read_q(t, [&](int c, const u32x4& y) {          // (not kept beside O here)
-            sa[t] = mfma16<BF>(step_k(read_k(s_t0, c / KS), c % KS), y, sa[t]);
-            __builtin_amdgcn_sched_barrier(0);
-          });
-        }
-        mask(sa, xx, st);
-        probs(sa, s_p0);
-        __syncthreads();
-#pragma unroll 1
-        for (int k = 0; k < 32; ++k) {
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const int r = here(32 * t + l31);
-            const float p = to_f32(
-                *(const uint16_t*)(s_p0 + r * 64 + 16 * ((k >> 3) ^ p_swz(r)) + 2 * (k & 7)));
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              const int h = here(4 * half), some = p != 0.0f ? -1 : 0;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int at = (32 * (w * ND + d) + 8 * (i >> 2) + h + (i & 3)) * ES;
-                const char* v = s_t0 + k * RB + (16 * ((at >> 4) ^ swz(k)) + (at & 15));
-                uint32_t y;
-                if constexpr (F8) y = from_e4m3<BF, false>(*(const uint8_t*)v) & 0xFFFF;
-                else y = *(const uint16_t*)v;
-                constexpr int e = BF ? 0x7F80 : 0x7C00;
-                const int fine = ((int)(y & e) - e) >> 31;           // all ones if finite
-                o[d][t][i] += p * __uint_as_float(__float_as_uint(to_f32(y)) & ~fine & some);
-              }
-              __builtin_amdgcn_sched_barrier(0);
-            }
+      int ready = b0 - 1;                        // the tile that it has been done for
+      while (true) {
+        while (true) {
+          if (ready != x) {
+            arrived(std::integral_constant<int, 1>{});
+            lds_barrier();
           }
+          if (x + 1 >= x_end || (ready != x && !whole(x))) break;
+          const i32x2 tell = told_of(x);
+          f32x4 sn = {0, 0, 0, 0};
+          int next = 0;
+          plain = whole(x + 1) && state1 >= 0;
+          // what has been told is looked at behind operand kTold of the first product,
+          // the loads are spread over those that follow
+          constexpr int kTold = MK / 3, PER = (LOADS + MK - kTold - 2) / (MK - kTold - 1);
+          const bool went = products(
+              std::true_type{}, std::true_type{}, sn, x + 1,
+              [&](int i) __attribute__((always_inline)) {
+                if (i == kTold) {
+                  if (ready != x && __builtin_amdgcn_readfirstlane((tell[0] == x) | (tell[1] == x)))
+                    return false;
+                  l += pend;
+                }
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                  if (i > kTold && (i - kTold - 1) * PER + k < LOADS)
+                    load(x + 3, (i - kTold - 1) * PER + k);
+                return true;
+              },
+              [&](int i) __attribute__((always_inline)) {
+                soft(sn, x + 1, plain, i);
+                if (i == 2) next = place(x + 4);
+              });
+          if (!went) break;
+          ++x;
+          if (!plain) soft_masked(sn, x, state1);
+          state1 = state2;
+          state2 = state3;
+          state3 = next;
+          sa = sn;
         }
-        __syncthreads();
+        if (ready != x) {
+          const i32x2 tell = told_of(x);
+          if (__builtin_amdgcn_readfirstlane(tell[0]) == x) follow(sa, x);
+          if (__builtin_amdgcn_readfirstlane(tell[1]) == x || !whole(x)) clean(s_t[(x - b0) & 3]);
+          ready = x;
+        }
+        if (x + 1 >= x_end) break;
       }
+      l += pend;
+      products(std::false_type{}, std::true_type{}, sa, x + 1, [](int) { return true; },
+               [](int) {});
+      arrived(std::integral_constant<int, 0>{});
     }
 
     // sums of the rows
-#pragma unroll
-    for (int t = 0; t < RQ; ++t) {
-      const float y = xor32_reduce(xor16_reduce(l[t], OpSum{}), OpSum{});
-      if (g4 == 0) s_l[kq][rq * (R / 2) + 16 * t + lc] = y;
-    }
+    l = xor32_reduce(xor16_reduce(l, OpSum{}), OpSum{});
+    if (g4 == 0) s_l[kq][rq * QR + lc] = l;
     __syncthreads();
     const bool all = b0 == 0 && b1 == s.nb;
     if (all) {
       // turned round through LDS, 64-byte runs of a wave's rows
       constexpr int WB = ND * 64;                // bytes of a row that a wave has
-      char* const mine = w == 0 ? s_t0 : w == 1 ? s_t1 : w == 2 ? s_t2 : s_t3;
-      static_assert(R * WB <= TB, "a wave's rows fit a tile");
+      char* const mine = s_t[0] + w * R * WB;
+      static_assert(NW * R * WB <= 4 * TB, "the rows fit the tiles");
       constexpr int WU = WB / 16;                // units of it
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
@@ -619,7 +633,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
       }
     } else {
       // this workgroup's part: the tile that it goes on with, or leaves open
-      float* const part = a.part + (long)(2 * wg + (b0 == 0)) * lat_part_floats(DC, R);
+      float* const part = a.part + (long)(2 * wg + (b0 == 0)) * lat_part_floats(DC);
       const int ln = here(lane);
 #pragma unroll
       for (int d = 0; d < ND; ++d)
@@ -634,11 +648,14 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
         part[R + tid] = s_l[0][tid] + s_l[1][tid];
       }
       if (b0 == 0 && tid == 0) {
-        // the workgroup of the tile's last unit: the largest v with v U / W <= unit
-        const long end = s_pref[seq] + (long)(tile + 1) * s.nb - 1;
+        // the workgroup of the tile's last unit: the largest v that starts before its end
+        const long end = s_pref[seq] + (long)(tile + 1) * s.nb;
+        int v = min((int)W - 1, (int)((double)end * (double)W / (double)U));
+        while (start_of(v) >= end) --v;
+        while (v + 1 < (int)W && start_of(v + 1) < end) ++v;
         meta[0] = seq;
         meta[1] = tile;
-        meta[2] = (int)(((end + 1) * W - 1) / U - wg) + 1;
+        meta[2] = v - wg + 1;
       }
     }
     u += b1 - b0;
@@ -648,18 +665,18 @@ __global__ __launch_bounds__(256, 1) void attn_latent_kernel(AttnArgs a) {
 // Joins the parts of the tile that workgroup blockIdx.x of the kernel above left
 // open, in their order: four runs of 64 lanes' four values (blockIdx.y), four
 // waves with every fourth part each.
-template <bool BF, bool F8, int DC, int R>
+template <bool BF, bool F8, int DC>
 __global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
-  constexpr int RT = R / 32;
+  constexpr int R = kLatRows, RT = R / 32;
   __shared__ f32x4 s_o[3][4][64];
   __shared__ float s_ml[3][2][32];
   const int wg = blockIdx.x;
   const int cnt = a.meta[4 * wg + 2];
   if (cnt == 0) return;
-  const LatSeq s = lat_seq<R>(a, a.meta[4 * wg]);
+  const LatSeq s = lat_seq(a, a.meta[4 * wg]);
   const int lane = lane_id(), w = threadIdx.x >> 6, l31 = lane & 31, half = lane >> 5;
   const int run = blockIdx.y, t = run % RT, dt = run / RT;   // rows 32 t.., values 32 dt..
-  const long pf = lat_part_floats(DC, R);
+  const long pf = lat_part_floats(DC);
   // part k: of the workgroup that opened the tile, then those that went on
   auto part = [&](int k) { return a.part + (long)(2 * (wg + k) + (k == 0)) * pf; };
   float mx = kNegInf, l = 0.0f;
@@ -745,19 +762,19 @@ __global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
     a.lse[(long)s.q0 * H + g] = (mn + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <bool BF, bool F8, int DC, int R>
+template <bool BF, bool F8, int DC>
 hipError_t run_latent(const AttnArgs& a, int grid, hipStream_t s) {
-  attn_latent_kernel<BF, F8, DC, R><<<grid, 256, 0, s>>>(a);
-  latent_join_kernel<BF, F8, DC, R><<<dim3(grid, DC / 32 * (R / 32)), 256, 0, s>>>(a);
+  attn_latent_kernel<BF, F8, DC><<<grid, 64 * kLatWaves, 0, s>>>(a);
+  latent_join_kernel<BF, F8, DC><<<dim3(grid, DC / 32 * (kLatRows / 32)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int DC, int R>
+template <int DC>
 hipError_t run_latent_d(const AttnArgs& a, int fmt, int grid, hipStream_t s) {
   const bool f8 = a.c.fmt == KV_E4M3;
   if (fmt == KV_BF16)
-    return f8 ? run_latent<true, true, DC, R>(a, grid, s) : run_latent<true, false, DC, R>(a, grid, s);
-  return f8 ? run_latent<false, true, DC, R>(a, grid, s) : run_latent<false, false, DC, R>(a, grid, s);
+    return f8 ? run_latent<true, true, DC>(a, grid, s) : run_latent<true, false, DC>(a, grid, s);
+  return f8 ? run_latent<false, true, DC>(a, grid, s) : run_latent<false, false, DC>(a, grid, s);
 }
 
 }  // namespace

@@ -113,15 +113,16 @@ hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 constexpr int kTreeMax = 256;           // tokens of one tree
 hipError_t launch_attn_tree(const AttnArgs& a, int fmt, hipStream_t s);
 
-// Latent cache: c.D the latent vector's length, one head. A workgroup takes R =
-// 32 or 64 rows (token, query head) at a time; the keys of all tiles of rows,
+// Latent cache: c.D the latent vector's length, one head. A workgroup takes tiles
+// of kLatRows rows, a row being a (token, query head) pair; the keys of all tiles,
 // laid end to end, are dealt out evenly to at most kLatGrid workgroups.
-constexpr int kLatGrid = 256;           // one a CU
+constexpr int kLatRows = 64;
+constexpr int kLatWaves = 8;            // of a workgroup
+constexpr int kLatGrid = 256;           // workgroups, one a CU
 constexpr int kLatSeqs = 256;           // sequences per launch
 constexpr int kLatMinUnits = 2;         // of 32 keys, that a workgroup is there for
-constexpr int lat_rows(long n, long T, int hq) { return T * hq <= 32 * n ? 32 : 64; }
-constexpr long lat_part_floats(int D, int R) { return (long)R * (D + 2); }
-size_t latent_ws_bytes(long n, long T, int hq, int D);
+constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
+size_t latent_ws_bytes(int D);
 hipError_t launch_attn_latent(const AttnArgs& a, int fmt, hipStream_t s);
 
 // Workgroups of 256 threads in one launch: a grid has fewer than 2^32 threads.

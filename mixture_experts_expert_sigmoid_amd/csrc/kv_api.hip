@@ -447,7 +447,7 @@ size_t moe_attn_latent_workspace_size(const moe_latent_cache* cache, long n, lon
   if (!cache || (cache->latent_dim != 256 && cache->latent_dim != 512) || n < 0 ||
       n >= (1L << 20) || n_heads < 1 || n_heads > 1024 || T < 0 || T > 0x7FFFFFFFL / n_heads)
     return 0;
-  return moe::latent_ws_bytes(n, T, n_heads, cache->latent_dim);
+  return moe::latent_ws_bytes(cache->latent_dim);
 }
 
 int moe_attn_latent(const moe_latent_cache* cache, const moe_kv_table* table, const int* slots,
@@ -470,7 +470,7 @@ int moe_attn_latent(const moe_latent_cache* cache, const moe_kv_table* table, co
   st = attn_rows(at, cache->latent_dim + cache->rope_dim, cache->latent_dim, T, &a);
   if (st) return st;
   if (T == 0) return MOE_OK;
-  const size_t need = moe::latent_ws_bytes(n, T, at->n_heads, cache->latent_dim);
+  const size_t need = moe::latent_ws_bytes(cache->latent_dim);
   if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return MOE_ERR_WORKSPACE;
   a.c = dev_latent(cache);
   a.t = dev_table(table);
