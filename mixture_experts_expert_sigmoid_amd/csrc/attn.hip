@@ -137,7 +137,7 @@ hipError_t launch_attn_latent(const AttnArgs& all, int fmt, hipStream_t s) {
     // no more workgroups than the table's longest contexts can keep busy
     const long tiles = a.cu ? a.T * a.hq / kLatRows + a.n
                             : a.n * (((long)a.hq + kLatRows - 1) / kLatRows);
-    const long units = tiles * ((long)a.t.max_pages * a.t.ps / 32 + 1);
+    const long units = tiles * ((long)a.t.max_pages * a.t.ps / 32 + 1 + kLatStart);
     const long want = (units + kLatMinUnits - 1) / kLatMinUnits;
     const int grid = (int)(want < kLatGrid ? want : kLatGrid);
     const hipError_t e = D == 256 ? launch_latent_256(a, fmt, grid, s)

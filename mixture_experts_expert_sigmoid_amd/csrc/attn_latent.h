@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     long v = 0;
     if (tid < a.n) {
       const LatSeq s = lat_seq(a, tid);
-      v = (long)s.tiles * s.nb;
+      v = (long)s.tiles * (s.nb + kLatStart);
     }
     for (int d = 1; d < 64; d <<= 1) {
       const long o = __shfl_up(v, d);
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
                      ? (int)(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8)
                      : (int)blockIdx.x;
   int* const meta = a.meta + 4 * wg;
-  if (tid == 0) meta[2] = 0;
+  if (tid == 0) meta[3] = 0;
   if (wg >= W) return;
   // workgroup v starts at unit v U / W, whole and rest by themselves
   const uint32_t w32 = (uint32_t)W;
@@ -188,10 +188,14 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     seq = __builtin_amdgcn_readfirstlane(seq);   // (alike in all lanes: told so)
     const LatSeq s = lat_seq(a, seq);
     const long rel = u - s_pref[seq];
+    const int units = s.nb + kLatStart;          // of a tile; the first ones stand for its start
     const int tile = __builtin_amdgcn_readfirstlane(
-        rel >> 32 ? (int)(rel / s.nb) : (int)((uint32_t)rel / (uint32_t)s.nb));
-    const int b0 = __builtin_amdgcn_readfirstlane((int)(rel - (long)tile * s.nb));
-    const int b1 = (int)min((long)s.nb, b0 + (u_end - u));
+        rel >> 32 ? (int)(rel / units) : (int)((uint32_t)rel / (uint32_t)units));
+    const int v0 = __builtin_amdgcn_readfirstlane((int)(rel - (long)tile * units));
+    const int v1 = (int)min((long)units, v0 + (u_end - u));
+    u += v1 - v0;
+    const int b0 = max(0, v0 - kLatStart), b1 = v1 - kLatStart;
+    if (b1 <= b0) continue;
     const int rows = s.m * H, r0 = tile * R;
     const int tok0 = r0 / H, tok1 = (min(rows, r0 + R) - 1) / H;
     const bool tree = a.parent != nullptr;
@@ -649,123 +653,144 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       }
       if (b0 == 0 && tid == 0) {
         // the workgroup of the tile's last unit: the largest v that starts before its end
-        const long end = s_pref[seq] + (long)(tile + 1) * s.nb;
+        const long end = s_pref[seq] + (long)(tile + 1) * units;
         int v = min((int)W - 1, (int)((double)end * (double)W / (double)U));
         while (start_of(v) >= end) --v;
         while (v + 1 < (int)W && start_of(v + 1) < end) ++v;
-        meta[0] = seq;
-        meta[1] = tile;
-        meta[2] = v - wg + 1;
+        meta[0] = s.q0;
+        meta[1] = rows;
+        meta[2] = r0;
+        meta[3] = v - wg + 1;
       }
     }
-    u += b1 - b0;
   }
 }
 
 // Joins the parts of the tile that workgroup blockIdx.x of the kernel above left
-// open, in their order: four runs of 64 lanes' four values (blockIdx.y), four
-// waves with every fourth part each.
+// open, in their order. A run, 32 values of 32 rows, is a wave's, 16 values a lane;
+// a workgroup has four of them (blockIdx.y). Up to kLatFew parts: a wave each;
+// more: one run after another, every fourth part to each wave.
+constexpr int kLatFew = 16;
 template <bool BF, bool F8, int DC>
 __global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
   constexpr int R = kLatRows, RT = R / 32;
   __shared__ f32x4 s_o[3][4][64];
   __shared__ float s_ml[3][2][32];
   const int wg = blockIdx.x;
-  const int cnt = a.meta[4 * wg + 2];
+  const i32x4 meta = *(const i32x4*)(a.meta + 4 * wg);     // q0, rows, first row, parts
+  const int cnt = meta[3];
   if (cnt == 0) return;
-  const LatSeq s = lat_seq(a, a.meta[4 * wg]);
   const int lane = lane_id(), w = threadIdx.x >> 6, l31 = lane & 31, half = lane >> 5;
-  const int run = blockIdx.y, t = run % RT, dt = run / RT;   // rows 32 t.., values 32 dt..
   const long pf = lat_part_floats(DC);
   // part k: of the workgroup that opened the tile, then those that went on
   auto part = [&](int k) { return a.part + (long)(2 * (wg + k) + (k == 0)) * pf; };
-  float mx = kNegInf, l = 0.0f;
-  f32x4 acc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f32x4{0, 0, 0, 0};
-  for (int k0 = w; k0 < cnt; k0 += 16) {
-    f32x4 y[4][4];
-    float pm[4], pl[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + 4 * j;
-      const float* p = part(k < cnt ? k : k0);
-      pm[j] = k < cnt ? p[32 * t + l31] : kNegInf;
-      pl[j] = p[R + 32 * t + l31];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y[j][i] = *(const f32x4*)(p + 2 * R + ((run * 4 + i) * 64 + lane) * 4);
-    }
-    float mn = mx;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mn = fmaxf(mn, pm[j]);
-    const float mu = mn == kNegInf ? 0.0f : mn;
-    const float f0 = exp2_fast(mx - mu);
-    l *= f0;
+  struct State {
+    float m, l;
+    f32x4 o[4];
+  };
+  const f32x4 zero = {0, 0, 0, 0};
+  auto scale = [](State& s, float f) {
+    s.l *= f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] *= f0;
+      for (int e = 0; e < 4; ++e) s.o[i][e] *= f;
+  };
+  // adds parts k0, k0 + stride, ... of a run, four at a time
+  auto add = [&](State& s, int run, int k0, int stride) {
+    const int t = run % RT;
+    for (; k0 < cnt; k0 += 4 * stride) {
+      f32x4 y[4][4];
+      float pm[4], pl[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (k0 + 4 * j >= cnt) continue;
-      const float f = exp2_fast(pm[j] - mu);
-      l += f * pl[j];
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * stride;
+        const float* p = part(k < cnt ? k : k0);
+        pm[j] = k < cnt ? p[32 * t + l31] : kNegInf;
+        pl[j] = p[R + 32 * t + l31];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
+          y[j][i] = *(const f32x4*)(p + 2 * R + ((run * 4 + i) * 64 + lane) * 4);
+      }
+      float mn = s.m;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] += f * y[j][i][e];
+      for (int j = 0; j < 4; ++j) mn = fmaxf(mn, pm[j]);
+      const float mu = mn == kNegInf ? 0.0f : mn;
+      scale(s, exp2_fast(s.m - mu));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k0 + j * stride >= cnt) continue;
+        const float f = exp2_fast(pm[j] - mu);
+        s.l += f * pl[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s.o[i][e] += f * y[j][i][e];
+      }
+      s.m = mn;
     }
-    mx = mn;
-  }
-  if (w) {
+  };
+  auto write = [&](const State& s, int run) {
+    const int H = a.hq, g = meta[2] + 32 * (run % RT) + l31, dt = run / RT;
+    if (g >= meta[1]) return;
+    const int tk = g / H;
+    const float inv = (F8 ? a.c.ks[0] : 1.0f) / s.l;
+    char* dst = a.out + (long)(meta[0] + tk) * a.o_row + (g - tk * H) * a.o_head + 64 * dt +
+                8 * half;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_o[w - 1][i][lane] = acc[i];
-    if (half == 0) {
-      s_ml[w - 1][0][l31] = mx;
-      s_ml[w - 1][1][l31] = l;
+    for (int i = 0; i < 4; ++i)
+      *(u32x2*)(dst + 16 * i) = u32x2{
+          pack16<BF>(of_sum(s.o[i][0], inv, s.l), of_sum(s.o[i][1], inv, s.l)),
+          pack16<BF>(of_sum(s.o[i][2], inv, s.l), of_sum(s.o[i][3], inv, s.l))};
+    if (a.lse && dt == 0 && half == 0)
+      a.lse[(long)meta[0] * H + g] = (s.m + __builtin_amdgcn_logf(s.l)) * kLn2;
+  };
+  if (cnt <= kLatFew) {
+    State s{kNegInf, 0.0f, {zero, zero, zero, zero}};
+    add(s, 4 * blockIdx.y + w, 0, 1);
+    write(s, 4 * blockIdx.y + w);
+    return;
+  }
+  for (int run = 4 * blockIdx.y; run < 4 * (int)blockIdx.y + 4; ++run) {
+    State s{kNegInf, 0.0f, {zero, zero, zero, zero}};
+    add(s, run, w, 4);
+    if (w) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_o[w - 1][i][lane] = s.o[i];
+      if (half == 0) {
+        s_ml[w - 1][0][l31] = s.m;
+        s_ml[w - 1][1][l31] = s.l;
+      }
     }
-  }
-  __syncthreads();
-  if (w) return;
-  float mn = mx;
+    __syncthreads();
+    if (w == 0) {
+      float mn = s.m;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) mn = fmaxf(mn, s_ml[k][0][l31]);
-  const float mu = mn == kNegInf ? 0.0f : mn;
-  const float f0 = exp2_fast(mx - mu);
-  l *= f0;
+      for (int k = 0; k < 3; ++k) mn = fmaxf(mn, s_ml[k][0][l31]);
+      const float mu = mn == kNegInf ? 0.0f : mn;
+      scale(s, exp2_fast(s.m - mu));
+      s.m = mn;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < 3; ++k) {
+        const float f = exp2_fast(s_ml[k][0][l31] - mu);
+        s.l += f * s_ml[k][1][l31];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] *= f0;
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 y = s_o[k][i][lane];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const float f = exp2_fast(s_ml[k][0][l31] - mu);
-    l += f * s_ml[k][1][l31];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 y = s_o[k][i][lane];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] += f * y[e];
+          for (int e = 0; e < 4; ++e) s.o[i][e] += f * y[e];
+        }
+      }
+      write(s, run);
     }
+    __syncthreads();
   }
-  const int H = a.hq, g = a.meta[4 * wg + 1] * R + 32 * t + l31;
-  if (g >= s.m * H) return;
-  const int tk = g / H;
-  const float inv = (F8 ? a.c.ks[0] : 1.0f) / l;
-  char* dst = a.out + (long)(s.q0 + tk) * a.o_row + (g - tk * H) * a.o_head + 64 * dt + 8 * half;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *(u32x2*)(dst + 16 * i) = u32x2{pack16<BF>(of_sum(acc[i][0], inv, l), of_sum(acc[i][1], inv, l)),
-                                    pack16<BF>(of_sum(acc[i][2], inv, l), of_sum(acc[i][3], inv, l))};
-  if (a.lse && dt == 0 && half == 0)
-    a.lse[(long)s.q0 * H + g] = (mn + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <bool BF, bool F8, int DC>
 hipError_t run_latent(const AttnArgs& a, int grid, hipStream_t s) {
   attn_latent_kernel<BF, F8, DC><<<grid, 64 * kLatWaves, 0, s>>>(a);
-  latent_join_kernel<BF, F8, DC><<<dim3(grid, DC / 32 * (kLatRows / 32)), 256, 0, s>>>(a);
+  latent_join_kernel<BF, F8, DC><<<dim3(grid, DC / 32 * (kLatRows / 32) / 4), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
