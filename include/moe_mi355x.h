@@ -683,6 +683,34 @@ int moe_attn_latent(const moe_latent_cache *cache, const moe_kv_table *table,
 size_t moe_attn_latent_workspace_size(const moe_latent_cache *cache, long n,
                                       long T, int n_heads);
 
+/* Expanded attention of prompts: head h's keys are [k[j][h], k_rope[j]] and its
+ * values v[j][h], as a product of Wk_h and Wv_h with the latent vectors left
+ * them, in rows instead of pages. */
+typedef struct {
+  const void *k;       /* [S][n_heads][128], 16-byte aligned */
+  long k_stride_row, k_stride_head;    /* elements, multiples of 8; strides of
+                          rows under 2^25 */
+  const void *k_rope;  /* [S][64], shared by the heads */
+  long rope_stride_row;
+  const void *v;       /* [S][n_heads][128] */
+  long v_stride_row, v_stride_head;
+} moe_latent_rows;
+
+/* attn: q [T][n_heads][192] (128 values for k, then 64 for k_rope), out
+ * [T][n_heads][128], n_heads 1..1024, window and n_first as for
+ * moe_attn_prefill; rows all of type fmt. Rows cu_q[i] .. cu_q[i + 1] - 1 of q
+ * are the newest tokens of the sequence whose keys and values are rows cu_k[i]
+ * .. cu_k[i + 1] - 1 (device int32 [n + 1] each, ascending, cu_k from 0 to S <=
+ * 2^28): a prompt, or, with more keys than rows, the next chunk of one. Rows of
+ * q before their sequence's first key give 0 and -infinity; rows outside the
+ * list are not written. Workspace: moe_attn_latent_prompt_workspace_size(n, T,
+ * n_heads) bytes. Errors: NULL, SHAPE, FORMAT, PARAM, WORKSPACE, HIP. */
+int moe_attn_latent_prompt(const moe_latent_rows *kv, long n, const int *cu_k,
+                           long S, const int *cu_q, long T,
+                           const moe_attn *attn, void *ws, size_t ws_bytes,
+                           void *stream);
+size_t moe_attn_latent_prompt_workspace_size(long n, long T, int n_heads);
+
 /* --------------------------------------------------------------- misc -- */
 /* Synchronises `stream`, then copies *err_word (device) to *host_bits. */
 int moe_read_device_error(const int *err_word, int *host_bits, void *stream);

@@ -86,6 +86,12 @@ class MoeLatentCache(ctypes.Structure):
                 ("stride_tok", c_long), ("c", c_void_p), ("scale", c_void_p)]
 
 
+class MoeLatentRows(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("k_stride_row", c_long), ("k_stride_head", c_long),
+                ("k_rope", c_void_p), ("rope_stride_row", c_long), ("v", c_void_p),
+                ("v_stride_row", c_long), ("v_stride_head", c_long)]
+
+
 class MoeKvTable(ctypes.Structure):
     _fields_ = [("n_slots", c_int), ("max_pages", c_int), ("ld", c_long),
                 ("n_pages", c_int), ("page_size", c_int), ("table", c_void_p),
@@ -177,6 +183,10 @@ _SIGS = {
     "moe_attn_latent": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvTable), c_void_p, c_long,
                                 c_void_p, c_long, c_void_p, POINTER(MoeAttn), c_void_p, c_void_p,
                                 c_size_t, c_void_p]),
+    "moe_attn_latent_prompt": (c_int, [POINTER(MoeLatentRows), c_long, c_void_p, c_long,
+                                       c_void_p, c_long, POINTER(MoeAttn), c_void_p, c_size_t,
+                                       c_void_p]),
+    "moe_attn_latent_prompt_workspace_size": (c_size_t, [c_long, c_long, c_int]),
     "moe_attn_latent_workspace_size": (c_size_t, [POINTER(MoeLatentCache), c_long, c_long,
                                                   c_int]),
     "moe_latent_pages": (c_int, [POINTER(MoeLatentCache), POINTER(MoeKvCache)]),
@@ -737,6 +747,31 @@ def moe_attn_latent(cache: MoeLatentCache, table: MoeKvTable, q, cu_q, out, scal
     _check(lib().moe_attn_latent(cache, table, _i32(slots, n, where), n, _i32(cu_q, 1, where), T,
                                  _i32(parent, T, where), a, _err(err_word, where),
                                  *_work(ws, where), _stream(stream)), where)
+
+
+def moe_attn_latent_prompt_workspace_size(n: int, T: int, n_heads: int) -> int:
+    return lib().moe_attn_latent_prompt_workspace_size(n, T, n_heads)
+
+
+def moe_attn_latent_prompt(q, k, k_rope, v, cu_q, cu_k, out, scale, ws, *, window=0, n_first=0,
+                           lse=None, stream=None):
+    """Expanded attention of the newest tokens of n = len(cu_q) - 1 sequences: q
+    [T][heads][192], k and v [S][heads][128], k_rope [S][64], out [T][heads][128],
+    lse [T][heads]; cu_k int32 [n + 1] as cu_q."""
+    where = "moe_attn_latent_prompt"
+    shape, rows = q.shape, k.shape
+    a = _attn(where, shape, 192, 128, q, out, scale, window, n_first, lse)
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or k_rope.dtype is not q.dtype:
+        raise MoeError(-2, where, "q, k, k_rope and v differ in type")
+    if len(rows) != 3 or rows[1] != shape[1]:
+        raise MoeError(-2, where, f"k {tuple(rows)} has other heads than q {tuple(shape)}")
+    S, n = rows[0], cu_q.numel() - 1
+    ks, vs = _rows(k, where, rows, 128), _rows(v, where, rows, 128)
+    kv = MoeLatentRows(k.data_ptr(), ks[0], ks[1], k_rope.data_ptr(),
+                       _flat(k_rope, where, S, 64), v.data_ptr(), vs[0], vs[1])
+    _check(lib().moe_attn_latent_prompt(kv, n, _i32(cu_k, n + 1, where), S,
+                                        _i32(cu_q, 1, where), shape[0], a, *_work(ws, where),
+                                        _stream(stream)), where)
 
 
 class _Workspace:

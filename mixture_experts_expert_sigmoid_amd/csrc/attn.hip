@@ -12,6 +12,7 @@ hipError_t launch_prefill_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_prefill_256(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_latent_256(const AttnArgs& a, int fmt, int grid, hipStream_t s);
 hipError_t launch_latent_512(const AttnArgs& a, int fmt, int grid, hipStream_t s);
+hipError_t launch_dense_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_tree_64(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_tree_128(const AttnArgs& a, int fmt, hipStream_t s);
 hipError_t launch_tree_256(const AttnArgs& a, int fmt, hipStream_t s);
@@ -106,6 +107,10 @@ hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
   return a.c.D == 64    ? launch_tree_64(a, fmt, s)
          : a.c.D == 128 ? launch_tree_128(a, fmt, s)
                         : launch_tree_256(a, fmt, s);
+}
+
+hipError_t launch_attn_dense(const AttnArgs& all, int fmt, hipStream_t s) {
+  return launch_dense_128(split_prefill(all), fmt, s);
 }
 
 size_t latent_ws_bytes(int D) {

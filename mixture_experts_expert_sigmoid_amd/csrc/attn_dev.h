@@ -74,13 +74,17 @@ __device__ __forceinline__ uint32_t lds_of(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 // Those at offsets from `bytes` on read nothing and write zeros.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"      // (m0 has no value to be preserved)
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t bytes, int at, int off,
                                             uint32_t to) {
+  auto alike = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); };
   const uint64_t b = (uint64_t)base;
-  const u32x4 rsrc = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, bytes, 0x00020000u};
+  const u32x4 rsrc = {alike((uint32_t)b), alike((uint32_t)(b >> 32) & 0xFFFFu), alike(bytes),
+                      0x00020000u};
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(rsrc), "s"(off)
+               : "s"(alike(to)), "v"(at), "s"(rsrc), "s"(alike(off))
                : "memory", "m0");
 }
 
@@ -91,6 +95,7 @@ __device__ __forceinline__ void load_lanes_to_lds(const char* from, uint32_t to)
                : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
                : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -46,9 +46,11 @@
 namespace moe {
 namespace {
 
-// what the newest tokens of a sequence see of each other: those before them, or
-// their ancestors in a tree
-enum { kCausal, kTree };
+// What the newest tokens of a sequence see of each other: those before them, or
+// their ancestors in a tree. kDense: those before them, and keys and values in
+// rows instead of pages, a head of them for each query head; behind a key's D
+// values come kLatRope that all heads share.
+enum { kCausal, kTree, kDense };
 
 // keys of a tile, rows of a workgroup's tile
 template <int D>
@@ -60,6 +62,7 @@ struct PreShape {
 // what a workgroup works on
 struct PreTile {
   int seq, slot, L, m, q0;     // sequence; its slot, length, new tokens, first row of q
+  long k0;                     // first row of keys (kDense)
   int tile, rows;              // tile of PreShape::ROWS rows, rows of the sequence
   int p_min, p_max;            // positions of its first and last row
   int lo_min, lo_max;          // first key of the window at those
@@ -97,8 +100,15 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   // (below 0 where rows of q come before the first sequence's)
   if (t.tile < 0 || t.tile * ROWS >= t.rows) return false;
   // (uniform, told so: loads behind the error word's atomic are not taken for it)
-  t.slot = __builtin_amdgcn_readfirstlane(kv_slot(a.slots, t.seq, a.t.n_slots, a.err));
-  t.L = __builtin_amdgcn_readfirstlane(kv_len(a.t, t.slot));
+  if constexpr (MODE == kDense) {
+    auto row = [&](int i) { return max(0L, min((long)a.cu_k[i], a.S)); };
+    t.slot = 0;
+    t.k0 = row(t.seq);
+    t.L = (int)max(0L, row(t.seq + 1) - t.k0);
+  } else {
+    t.slot = __builtin_amdgcn_readfirstlane(kv_slot(a.slots, t.seq, a.t.n_slots, a.err));
+    t.L = __builtin_amdgcn_readfirstlane(kv_len(a.t, t.slot));
+  }
   const int r1 = min(t.rows, (t.tile + 1) * ROWS) - 1;
   if constexpr (MODE == kTree) {
     // any row may see any drafted token; all see those before (p_min), from the
@@ -135,23 +145,34 @@ __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
   return max(1, min(min(a.n_split, nb >> 2), (int)sqrtf((float)nb * a.split_gain)));
 }
 
+// what a workgroup's waves tell each other
+struct PreNotes {
+  int gone;                                      // last tile with a group that has no page
+  int miss[2][4];                                // the same for each wave's group, by buffer
+  int bad;                                       // values of V not finite were taken out
+};
+
 template <bool BF, bool F8, int D, int MODE>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_prefill_kernel(AttnArgs a) {
   constexpr int BN = PreShape<D>::BN, ROWS = PreShape<D>::ROWS;
   constexpr int NA = BN / 32;                    // 32-key score tiles
-  constexpr int NC = D / 16;                     // steps of the first product
+  constexpr bool PAGED = MODE != kDense;
+  constexpr int DR = PAGED ? 0 : kLatRope;       // shared values of a key
+  constexpr int NC = (D + DR) / 16;              // steps of the first product
   constexpr int ND = D / 32;                     // 32-row tiles of O^T
   constexpr int UPR = D / 8;                     // 16-byte units of a row in LDS
   constexpr int WR = BN / 4;                     // rows of a tile that a wave brings
   constexpr int GPR = F8 ? D / 16 : UPR;         // 16-byte units of a row in memory
   constexpr int NL = WR * GPR / 64;              // loads per lane and array
   constexpr int TB = BN * D * 2;                 // bytes of a tile in LDS
+  constexpr int KB = TB + BN * DR * 2;           // with the keys' shared values
   static_assert(NL >= 1, "tile");
 
-  __shared__ __align__(16) char s_k0[TB], s_k1[TB], s_v0[TB], s_v1[TB];
-  __shared__ int s_gone;                         // last tile with a group that has no page
-  __shared__ int s_miss[2][4];                   // the same for each wave's group, by buffer
-  __shared__ int s_bad;                          // values of V not finite were taken out
+  __shared__ __align__(16) char s_k0[KB], s_k1[KB], s_v0[TB], s_v1[TB];
+  // (dense tiles of two workgroups fill a CU's LDS; of the notes they need bad
+  // alone, and find room for it in the end)
+  __shared__ PreNotes s_note;
+  bool bad = false;
   __shared__ TreeRows<MODE == kTree ? ROWS : 0> s_tree;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -169,10 +190,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
   const int x1 = (int)((long)(blockIdx.y + 1) * t.nb / parts);
-  if (tid < 8) s_miss[tid >> 2][tid & 3] = -1;
-  if (tid == 0) {
-    s_gone = -1;
-    s_bad = 0;
+  if constexpr (PAGED) {
+    if (tid < 8) s_note.miss[tid >> 2][tid & 3] = -1;
+    if (tid == 0) {
+      s_note.gone = -1;
+      s_note.bad = 0;
+    }
   }
 
 
@@ -236,13 +259,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   float m = kNegInf, l = 0.0f;
 
   const int* row = a.t.table + (long)max(0, t.slot) * a.t.ld;
-  const char* kb = a.c.k + kvh * a.c.sh;
-  const char* vb = a.c.v + kvh * a.c.sh;
+  const char* kb = a.c.k + kvh * a.c.sh + (PAGED ? 0L : t.k0 * a.c.st);
+  const char* vb = a.c.v + (PAGED ? kvh * a.c.sh : kvh * a.v_head + t.k0 * a.v_row);
+  const char* rb = PAGED ? nullptr : a.kr + t.k0 * a.kr_row;
   const int grp = w * WR / 16;                   // 16-key group that this wave brings from
 
-  // Byte offset in the cache of the wave's group of the next 64 tiles, a tile
-  // a lane; kMissing: no page, kUnseen: nothing of it is visible. One lookup a
-  // tile is then two lane reads.
+  // Byte offset in the cache (dense: the key) of the wave's group of the next 64
+  // tiles, a tile a lane; kMissing: no page, kUnseen: nothing of it is visible. One
+  // lookup a tile is then two lane reads.
   constexpr long kMissing = -(1L << 32), kUnseen = -(2L << 32);
   struct Group {
     long off;                                    // 0 without a page
@@ -252,6 +276,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   auto lookup = [&](int x) {
     const int key = group_key(GT * x + grp);
     if (x >= x1 || key > t.p_max || !(key + 16 > t.lo_min || key < a.first)) return kUnseen;
+    if constexpr (!PAGED) return (long)key;
     const int i = kv_entry(a.t, key), e = row[i];
     return e >= 0 && e < a.t.n_pages ? e * a.c.sp + (key - i * a.t.ps) * a.c.st : kMissing;
   };
@@ -278,6 +303,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   int k_at = l31 * (2 * D) + 16 * (half ^ k_swz(l31));
   const int v_row = 4 * half + ((lane & 15) >> 2), v_d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   int v_at = v_row * (2 * D) + (16 * ((v_d >> 3) ^ v_swz(v_row)) + 2 * (v_d & 7));
+  // unit 2 c + half of the shared values is at r_at ^ 32 c
+  const int r_at = TB + l31 * 128 + 16 * (half ^ (l31 >> 1 & 7));
   const uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
   // either value of a pair infinite or NaN: the exponent's carry
   auto carry = [&](uint32_t x) { return (x & 0x7FFF7FFFu) + (BF ? 0x00800080u : 0x04000400u); };
@@ -290,7 +317,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   auto clean = [&](u32x4 v, int j, bool ok) {      // of key j
     if (!ok || j > t.p_max || !(j >= t.lo_min || j < a.first)) return u32x4{0, 0, 0, 0};
     if ((carry(v[0]) | carry(v[1]) | carry(v[2]) | carry(v[3])) & 0x80008000u) {
-      s_bad = 1;
+      if constexpr (PAGED) s_note.bad = 1; else bad = true;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = clean16(v[e]);
     }
@@ -303,34 +330,51 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // arrival. A lane's offset stays below 2^31 (16 stride_tok < 2^30).
   constexpr int RPL = 64 / GPR;
   const int l_row = ((w * WR) & 15) + lane / GPR;
-  const uint32_t l_at = (uint32_t)l_row * (uint32_t)a.c.st;
   // the lane's unit in load 0; the swizzles are exclusive ors of row bits
   const uint32_t k_unit = 16 * (lane % GPR ^ (F8 ? 0 : k_swz(l_row)));
   const uint32_t v_unit = 16 * (lane % GPR ^ (F8 ? 0 : v_swz(l_row)));
   u32x4 rk[F8 ? NL : 1], rv[F8 ? NL : 1];
-  auto issue = [&](const char* p, uint32_t unit, auto swz, char* to, u32x4* raw) {
+  // from rows that lie st bytes apart, of which those from `bytes` on are not there
+  auto issue = [&](const char* p, uint32_t bytes, long st, uint32_t unit, auto swz, char* to,
+                   u32x4* raw) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i, p += RPL * a.c.st) {
-      uint32_t f = l_at + (unit ^ (F8 ? 0 : 16 * swz(i * RPL)));
+    for (int i = 0; i < NL; ++i) {
+      uint32_t f = (uint32_t)l_row * (uint32_t)st + (unit ^ (F8 ? 0 : 16 * swz(i * RPL)));
       asm volatile("" : "+v"(f));                // added by the load, not ahead of it
       if constexpr (F8)
-        raw[i] = *(const u32x4*)(p + f);
+        raw[i] = *(const u32x4*)(p + i * RPL * st + f);
       else
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(p + f),
-            (__attribute__((address_space(3))) void*)(to + (w * WR * UPR + i * 64) * 16), 16, 0,
-            0);
+        load_to_lds(p, bytes, (int)f, i * RPL * (int)st,
+                    lds_of(to) + (w * WR * UPR + i * 64) * 16);
     }
+  };
+  // bytes that a group's rows of st bytes have: those of keys before the end
+  auto bytes_of = [&](const Group& gr, long st) {
+    if (gr.state < 0) return 0u;
+    return PAGED ? 0x7FFFFFFFu : (uint32_t)(min(16, t.L - (int)gr.off) * st);
   };
   auto issue_k = [&](int x, const Group& gr, char* to, int* miss) {
-    if (gr.state == (int)(kMissing >> 32) && lane == 0) {
-      atomicOr(a.err, kErrPage);
-      s_gone = x;
-      miss[w] = x;
+    if constexpr (PAGED) {
+      if (gr.state == (int)(kMissing >> 32) && lane == 0) {
+        atomicOr(a.err, kErrPage);
+        s_note.gone = x;
+        miss[w] = x;
+      }
+      issue(kb + gr.off, bytes_of(gr, a.c.st), a.c.st, k_unit, k_swz, to, rk);
+    } else {
+      issue(kb + gr.off * a.c.st, bytes_of(gr, a.c.st), a.c.st, k_unit, k_swz, to, rk);
+      const char* p = rb + gr.off * a.kr_row;
+      const uint32_t f = lane / 8 * (uint32_t)a.kr_row;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)                // eight rows of the wave's 16 each
+        load_to_lds(p, bytes_of(gr, a.kr_row), (int)(f + 16 * (lane % 8 ^ (lane / 16) ^ 4 * i)),
+                    8 * i * (int)a.kr_row, lds_of(to) + TB + (w * WR + 8 * i) * 128);
     }
-    issue(kb + gr.off, k_unit, k_swz, to, rk);
   };
-  auto issue_v = [&](const Group& gr, char* to) { issue(vb + gr.off, v_unit, v_swz, to, rv); };
+  auto issue_v = [&](const Group& gr, char* to) {
+    const long st = PAGED ? a.c.st : a.v_row;
+    issue(vb + (PAGED ? gr.off : gr.off * st), bytes_of(gr, st), st, v_unit, v_swz, to, rv);
+  };
   auto expand = [&](const u32x4& raw, u32x4 (&y)[2]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -382,6 +426,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
 
   // Operand c, aa of the first product: 8 values of D of 32 keys
   auto read_k = [&](const char* from, int c, int aa) {
+    if (c >= D / 16)
+      return *(const u32x4*)(from + 32 * aa * 128 + (r_at ^ (32 * (c - D / 16))));
     return *(const u32x4*)(from + 32 * aa * (2 * D) + (k_at ^ (32 * c)));
   };
   // Operand of the second product: keys 4 half + 0..3 of the gth 16-key step,
@@ -561,7 +607,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     finish_k(kn);
     if (x > x0) finish_v(x, g0, vx);
     __syncthreads();
-    const int gone_tile = s_gone;
+    const int gone_tile = PAGED ? s_note.gone : -1;
     g0 = g1;
     if (x + 2 < x1) {
       g1 = group_of(x + 2);
@@ -582,8 +628,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   };
   if (x0 < x1) {
     g0 = group_of(x0);
-    __syncthreads();                             // s_gone and s_miss are set
-    issue_k(x0, g0, s_k0, s_miss[0]);
+    __syncthreads();                             // s_note is set
+    issue_k(x0, g0, s_k0, s_note.miss[0]);
     issue_v(g0, s_v0);
     if constexpr (MODE == kTree)
       if (masked)
@@ -594,16 +640,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
     finish_k(s_k0);
     finish_v(x0, g0, s_v0);
     __syncthreads();
-    const int gone_tile = s_gone;
-    if (x0 + 1 < x1) issue_k(x0 + 1, g1, s_k1, s_miss[1]);
+    const int gone_tile = PAGED ? s_note.gone : -1;
+    if (x0 + 1 < x1) issue_k(x0 + 1, g1, s_k1, s_note.miss[1]);
     scores(sa, s_k0);
-    settle(sa, x0, gone_tile, s_miss[0]);
+    settle(sa, x0, gone_tile, s_note.miss[0]);
     while (x + 2 < x1) {
-      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_miss[0], s_miss[1]);
-      step(sb, sa, s_k1, s_k0, s_v1, s_v0, s_miss[1], s_miss[0]);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_note.miss[0], s_note.miss[1]);
+      step(sb, sa, s_k1, s_k0, s_v1, s_v0, s_note.miss[1], s_note.miss[0]);
     }
     if (x + 1 < x1) {
-      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_miss[0], s_miss[1]);
+      step(sa, sb, s_k0, s_k1, s_v0, s_v1, s_note.miss[0], s_note.miss[1]);
       last(sb, s_v1);
     } else {
       last(sa, s_v0);
@@ -613,29 +659,43 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   // values of V that are not finite and were staged as zeros: their products,
   // for the rows that see their key
   __syncthreads();
-  if (s_bad) {
+  if constexpr (!PAGED) {
+    if (lane == 0) ((int*)s_k0)[w] = 0;
+    if (bad) ((int*)s_k0)[w] = 1;
+    __syncthreads();
+    bad = ((int*)s_k0)[0] | ((int*)s_k0)[1] | ((int*)s_k0)[2] | ((int*)s_k0)[3];
+    __syncthreads();
+  } else {
+    bad = s_note.bad;
+  }
+  if (bad) {
     const int pos = pos_of(), lo = a.window ? pos - a.window + 1 : 0;
     for (int xx = x0; xx < x1; ++xx) {
       if (whole(xx)) continue;
       for (int i = 0; i < BN; ++i) {
         const int j = group_key(GT * xx + i / 16) + i % 16;
         if (j > t.p_max || !(j >= t.lo_min || j < a.first)) continue;
-        const int e = kv_entry(a.t, j), p = row[e];
-        if (p < 0 || p >= a.t.n_pages) continue;
-        const long off = p * a.c.sp + (long)(j - e * a.t.ps) * a.c.st;
+        long off = 0;
+        if constexpr (PAGED) {
+          const int e = kv_entry(a.t, j), p = row[e];
+          if (p < 0 || p >= a.t.n_pages) continue;
+          off = p * a.c.sp + (long)(j - e * a.t.ps) * a.c.st;
+        }
         auto value = [&](const char* base, int dd) {
           uint32_t x16;
           if constexpr (F8)
-            x16 = from_e4m3<BF, false>(*(const uint8_t*)(base + off + dd)) & 0xFFFF;
+            x16 = from_e4m3<BF, false>(*(const uint8_t*)(base + dd)) & 0xFFFF;
           else
-            x16 = *(const uint16_t*)(base + off + 2 * dd);
+            x16 = *(const uint16_t*)(base + 2 * dd);
           return BF ? bf16_bits_to_f32(x16)
                     : (float)__builtin_bit_cast(_Float16, (uint16_t)x16);
         };
+        const char* vj = vb + (PAGED ? off : j * a.v_row);
+        const char* kj = kb + (PAGED ? off : j * a.c.st);
         auto finite = [](float f) { return fabsf(f) < __builtin_huge_valf(); };
         bool any = false;
 #pragma unroll 1
-        for (int dd = lane; dd < D; dd += 64) any |= !finite(value(vb, dd));
+        for (int dd = lane; dd < D; dd += 64) any |= !finite(value(vj, dd));
         if (!__any(any)) continue;
         float dot = 0.0f;
 #pragma unroll
@@ -643,7 +703,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t q16 = (q[c][i >> 1] >> (16 * (i & 1))) & 0xFFFF;
-            dot += value(kb, 16 * c + 8 * half + i) *
+            const int dd = 16 * c + 8 * half + i;
+            dot += (c < D / 16 ? value(kj, dd) : value(rb + j * a.kr_row, dd - D)) *
                    (BF ? bf16_bits_to_f32(q16)
                        : (float)__builtin_bit_cast(_Float16, (uint16_t)q16));
           }
@@ -658,7 +719,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
         for (int d = 0; d < ND; ++d)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float f = value(vb, 32 * d + 8 * (i >> 2) + 4 * half + (i & 3));
+            const float f = value(vj, 32 * d + 8 * (i >> 2) + 4 * half + (i & 3));
             if (sees && !finite(f)) o[d][i] += pv * f;
             if (i == 15) __builtin_amdgcn_sched_barrier(0);
           }

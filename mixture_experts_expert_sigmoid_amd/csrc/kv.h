@@ -53,6 +53,13 @@ struct AttnArgs {
   int n_tiles;           // of a key-value head
   int block0;            // first of all workgroups that this launch runs
   const int* parent;     // of each row, trees only
+  // dense keys (c.k, c.st, c.sh) and values (c.v): rows cu_k[i].. of S, and the
+  // values that a key's heads share; strides in bytes
+  const int* cu_k;
+  long S;
+  long v_row, v_head;
+  const char* kr;
+  long kr_row;
   // decode: every pair is one team's
   int whole;
   // partial results of split rows
@@ -112,6 +119,9 @@ hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 // kernels, with ancestors in place of the tokens before.
 constexpr int kTreeMax = 256;           // tokens of one tree
 hipError_t launch_attn_tree(const AttnArgs& a, int fmt, hipStream_t s);
+// So do prompts whose keys and values are dense rows.
+constexpr int kDenseDim = 128;          // values of a head, and of a key's own
+hipError_t launch_attn_dense(const AttnArgs& a, int fmt, hipStream_t s);
 
 // Latent cache: c.D the latent vector's length, one head. A workgroup takes tiles
 // of kLatRows rows, a row being a (token, query head) pair; the keys of all tiles,

@@ -442,6 +442,62 @@ int moe_latent_append(const moe_latent_cache* cache, const moe_kv_table* table, 
   return done(moe::launch_latent_append(a, fmt, (hipStream_t)stream), "moe_latent_append");
 }
 
+size_t moe_attn_latent_prompt_workspace_size(long n, long T, int n_heads) {
+  if (n < 0 || n >= (1L << 20) || n_heads < 1 || n_heads > 1024 || T < 0 ||
+      T > 0x7FFFFFFFL / n_heads)
+    return 0;
+  return moe::prefill_ws_bytes(n, T, n_heads, n_heads, moe::kDenseDim);
+}
+
+int moe_attn_latent_prompt(const moe_latent_rows* kv, long n, const int* cu_k, long S,
+                           const int* cu_q, long T, const moe_attn* at, void* ws,
+                           size_t ws_bytes, void* stream) {
+  constexpr int D = moe::kDenseDim, DR = moe::kLatRope;
+  if (!kv || !at) return MOE_ERR_NULL;
+  if (at->fmt != MOE_KV_BF16 && at->fmt != MOE_KV_F16) return MOE_ERR_FORMAT;
+  if (n < 0 || n >= (1L << 20) || T < 0 || S < 0 || S > kMaxTokens || at->n_heads < 1 ||
+      at->n_heads > 1024 || T > 0x7FFFFFFFL / at->n_heads || (n == 0 && T > 0))
+    return MOE_ERR_SHAPE;
+  moe::AttnArgs a{};
+  const int st = attn_rows(at, D + DR, D, T, &a);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  if (!cu_q || !cu_k || (S > 0 && (!kv->k || !kv->k_rope || !kv->v))) return MOE_ERR_NULL;
+  if (!row_strides_ok(kv->k_stride_row, kv->k_stride_head, D) ||
+      !row_strides_ok(kv->v_stride_row, kv->v_stride_head, D) ||
+      !row_strides_ok(kv->rope_stride_row, DR, DR))
+    return MOE_ERR_SHAPE;
+  for (long s : {kv->k_stride_row, kv->v_stride_row, kv->rope_stride_row})
+    if (s >= (1L << 30) / 32) return MOE_ERR_SHAPE;
+  if ((((uintptr_t)kv->k) | ((uintptr_t)kv->k_rope) | ((uintptr_t)kv->v)) & 15)
+    return MOE_ERR_PARAM;
+  const size_t need = moe::prefill_ws_bytes(n, T, at->n_heads, at->n_heads, D);
+  if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return MOE_ERR_WORKSPACE;
+  a.c.k = (char*)kv->k;
+  a.c.v = (char*)kv->v;
+  a.c.st = kv->k_stride_row * 2;
+  a.c.sh = kv->k_stride_head * 2;
+  a.v_row = kv->v_stride_row * 2;
+  a.v_head = kv->v_stride_head * 2;
+  a.kr = (const char*)kv->k_rope;
+  a.kr_row = kv->rope_stride_row * 2;
+  a.c.fmt = at->fmt;
+  a.c.hkv = at->n_heads;
+  a.c.D = D;
+  a.g = 1;
+  // (no table; contexts are at most the rows there are)
+  a.t.ps = 16;
+  a.t.max_pages = (int)((S + 15) / 16);
+  attn_window(at, S, &a);
+  a.n = (int)n;
+  a.cu = cu_q;
+  a.cu_k = cu_k;
+  a.S = S;
+  a.T = T;
+  a.part = (float*)ws;
+  return done(moe::launch_attn_dense(a, at->fmt, (hipStream_t)stream), "moe_attn_latent_prompt");
+}
+
 size_t moe_attn_latent_workspace_size(const moe_latent_cache* cache, long n, long T,
                                       int n_heads) {
   if (!cache || (cache->latent_dim != 256 && cache->latent_dim != 512) || n < 0 ||
