@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
   constexpr int RPL = 64 / UPR, NLD = RPW / RPL;          // rows of a load; loads
   constexpr int LOADS = NLD + 1;
   constexpr int NK = (DC + kLatRope) / 32;                // steps of the first product
-  constexpr int QR = 2 * R / NW;                          // a wave's rows in it
+  constexpr int QR = 2 * R / NW;                          // a wave's rows of scores
   constexpr int RT = R / 32;                              // 32-row tiles in the second
   constexpr int ND = DC / 32 / NW;                        // a wave's 32-row tiles of O^T
   constexpr int QB = R * (DC + kLatRope) * 2;             // the queries
@@ -93,18 +93,29 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 
   __shared__ __align__(16) char s_t[4][TB];               // tile x in (x - first) % 4
   __shared__ __align__(16) char s_q[F8 ? QB : 16];        // the queries, or in the last two tiles
-  __shared__ __align__(16) char s_p[2][R * 64];           // P of tile x in x % 2
+  __shared__ __align__(16) char s_p[R * 64];              // P of the tile before the one whose
+                                                          // scores are computed
+  // halves of scores for the wave next to each; between steps, and in the end,
+  // what the rows' waves tell each other
+  __shared__ __align__(16) union {
+    char half[NW][1024];
+    struct { float f[R], top[2][R], l[2][R]; } row;
+  } s_x;
   static_assert(F8 || 2 * TB == QB, "two tiles hold the queries");
   __shared__ long s_pref[kLatSeqs + 1];
   __shared__ TreeRows<R> s_tree;
-  __shared__ float s_m[R], s_f[R], s_lm[2][R], s_l[2][R];
+  __shared__ float s_m[R];
   __shared__ long s_scan[NW];
   // by x % 8: tile x if its P is to be done again; if a group of it has no page
   __shared__ __align__(8) int s_tell[8][2];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kq = w / (NW / 2), rq = w % (NW / 2);         // its 16 keys, its 16 rows
+  // Its 16 keys (kq) and 16 rows (rq) of scores. The wave next to it has the
+  // same keys and the next rows; one of them (dq) multiplies the first half of
+  // the depth for both, the other the second, so that an operand of K is read
+  // from LDS for 32 rows.
+  const int kq = w / (NW / 2), rq = w % (NW / 2), dq = w & 1;
   const int lc = lane & 15, g4 = lane >> 4, half = lane >> 5, l31 = lane & 31;
   const int H = a.hq;
 
@@ -161,10 +172,22 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
   // Operands' places in a tile, of which one turn of the swizzle takes 256 bytes:
   // a register for each place within those, the rest by constant distances
   const int k_row = 16 * kq + lc, v_row = 8 * half + (F8 ? lc >> 1 : lc >> 2);
-  int k_at[4], v_at[ND][2];
+  constexpr int KS = F8 ? 2 : 1, MK = NK / KS;            // reads of K that the depth takes
+  constexpr int MR = kLatRope / 32 / KS, ML = MK - MR;    // of rotary values, of latent ones
+  constexpr int MW = (MK + 1) / 2;                        // of a wave (the second half: MK - MW)
+  int k_at[4], kr_at[MR], v_at[ND][2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) k_at[j] = k_row * RB + 16 * ((4 * j + g4) ^ swz(k_row));
-  int kr_at = 32 * RB + k_row * RRB + 16 * (g4 ^ swz_r(k_row));
+  for (int j = 0; j < 4; ++j) {
+    const int g = dq * MW + j;
+    k_at[j] = k_row * RB + 256 * (g >> 2) + 16 * ((4 * (g & 3) + g4) ^ swz(k_row));
+  }
+  // the second half's last reads; the first half's of the same number
+#pragma unroll
+  for (int n = 0; n < MR; ++n) {
+    constexpr int first = MK - MW - MR;
+    kr_at[n] = dq ? 32 * RB + k_row * RRB + 16 * ((4 * n + g4) ^ swz_r(k_row))
+                  : k_at[(first + n) & 3] + 256 * ((first + n) >> 2);
+  }
 #pragma unroll
   for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -298,36 +321,49 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       load_lanes_to_lds(from(r, QU + (lane % 8 ^ (r >> 1 & 7))),
                         lds_of(qa) + R * DC * 2 + w * QW * 128);
     };
-    u32x4 q[NK];
+    u32x4 q[2][MW * KS];                         // of 32 rows, half of the depth
     auto take_q = [&] {
-      const int ln = here(lane), lc = ln & 15, g4 = ln >> 4, r = rq * QR + lc;
+      const int ln = here(lane), lc = ln & 15, g4 = ln >> 4;
 #pragma unroll
-      for (int c = 0; c < NK; ++c) {
-        // values from 32 c + 8 g4 on; e4m3: as a unit of 16 keeps them for two steps
-        const int un = F8 ? 8 * (c >> 1) + 2 * g4 + (c & 1) : 4 * c + g4;
-        q[c] = *(const u32x4*)(qa + (32 * c < DC
-                                         ? r * DC * 2 + 16 * (un ^ q_swz(r))
-                                         : R * DC * 2 + r * 128 + 16 * ((un & 7) ^ (r >> 1 & 7))));
-      }
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < MW * KS; ++i) {
+          // values from 32 c + 8 g4 on; e4m3: as a unit of 16 keeps them for two steps
+          const int r = (rq & 2) * QR + t * QR + lc, c = min(dq * MW * KS + i, NK - 1);
+          const int un = F8 ? 8 * (c >> 1) + 2 * g4 + (c & 1) : 4 * c + g4;
+          q[t][i] = *(const u32x4*)(qa + (32 * c < DC
+                                              ? r * DC * 2 + 16 * (un ^ q_swz(r))
+                                              : R * DC * 2 + r * 128 +
+                                                    16 * ((un & 7) ^ (r >> 1 & 7))));
+        }
     };
 
-    // Operands of S^T = K Q^T: this wave's 16 keys. Read i is step i, or for e4m3
-    // steps 2 i and 2 i + 1.
-    constexpr int KS = F8 ? 2 : 1, MK = NK / KS, ML = DC / 32 / KS;
+    // Operands of S^T = K Q^T: this wave's 16 keys. Read i is step i of its half, or
+    // for e4m3 steps 2 i and 2 i + 1.
     auto read_k = [&](const char* kt, int i) __attribute__((always_inline)) {
-      return *(const u32x4*)(i < ML ? kt + k_at[i & 3] + 256 * (i >> 2)
-                             : i == ML ? kt + kr_at : kt + (kr_at ^ 64));
+      constexpr int first = MK - MW - MR;
+      return *(const u32x4*)(kt + (i >= first && i < first + MR ? kr_at[i - first]
+                                                                : k_at[i & 3] + 256 * (i >> 2)));
     };
     auto use_k = [&](f32x4 (&sv)[2], const u32x4& raw, int i) __attribute__((always_inline)) {
+      if (MK % 2 && i == MW - 1 && dq) return;   // the second half is shorter
 #pragma unroll
       for (int e = 0; e < KS; ++e) {
         u32x4 ka = raw;
         if constexpr (F8)
           ka = u32x4{from_e4m3<BF, false>(raw[2 * e]), from_e4m3<BF, true>(raw[2 * e]),
                      from_e4m3<BF, false>(raw[2 * e + 1]), from_e4m3<BF, true>(raw[2 * e + 1])};
-        const int c = KS * i + e;                // two sums, of the even and the odd steps
-        sv[c & 1] = mfma16<BF>(ka, q[c], c < 2 ? f32x4{0, 0, 0, 0} : sv[c & 1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          sv[t] = mfma16<BF>(ka, q[t][KS * i + e], i + e == 0 ? f32x4{0, 0, 0, 0} : sv[t]);
       }
+    };
+    // this wave's scores from both halves, with a barrier between give and take
+    auto give = [&](const f32x4 (&sv)[2]) {
+      *(f32x4*)(s_x.half[w ^ 1] + 16 * lane) = dq ? sv[0] : sv[1];
+    };
+    auto take = [&](const f32x4 (&sv)[2]) {
+      return (dq ? sv[1] : sv[0]) + *(const f32x4*)(s_x.half[w] + 16 * lane);
     };
     // masks the scores of a tile that is not whole
     auto mask = [&](f32x4& sv, int x, int state) __attribute__((always_inline)) {
@@ -360,28 +396,28 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = exp2_fast(sv[i] + neg);
       pend = (p[0] + p[1]) + (p[2] + p[3]);
-      *(u32x2*)(s_p[x & 1] + p_to) = u32x2{pack16<BF>(p[0], p[1]), pack16<BF>(p[2], p[3])};
+      *(u32x2*)(s_p + p_to) = u32x2{pack16<BF>(p[0], p[1]), pack16<BF>(p[2], p[3])};
     };
     // lets m, l and O follow the maximum, after a barrier behind soft(); ends in
     // a barrier
     auto follow = [&](const f32x4& sv, int x) __attribute__((always_inline)) {
       const int r = rq * QR + lc;
       const float top = top_of(sv);
-      if (g4 == 0) s_lm[kq][r] = top;
+      if (g4 == 0) s_x.row.top[kq][r] = top;
       lds_barrier();
       if (tid < R) {
-        const float old = s_m[tid], now = fmaxf(old, fmaxf(s_lm[0][tid], s_lm[1][tid]));
+        const float old = s_m[tid], now = fmaxf(old, fmaxf(s_x.row.top[0][tid], s_x.row.top[1][tid]));
         float df = old - (now == kNegInf ? 0.0f : now);
         if constexpr (!BF) df += pre_lift<BF>(now) - pre_lift<BF>(old);
-        s_f[tid] = exp2_fast(df);
+        s_x.row.f[tid] = exp2_fast(df);
         s_m[tid] = now;
       }
       lds_barrier();
       m = s_m[r];
-      l *= s_f[r];
+      l *= s_x.row.f[r];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const float f = s_f[32 * t + l31];
+        const float f = s_x.row.f[32 * t + l31];
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -414,20 +450,21 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     // S^T of tile x if QK, the product of the tile before with its P if PV. One
     // operand after another, each with the read of the one that is due kAhead
     // later and a share of the rest: beside(i) behind the first product's operand
-    // i, the steps of soft() behind those of the second. The order is kept as
-    // written. False if beside() was: nothing but scores has changed.
+    // i, the steps of soft() behind those of the second, with the barrier that P's
+    // room and the scores' halves ask for. The order is kept as written. False if
+    // beside() was: nothing has changed, and there was no barrier.
     constexpr int kAhead = 4, kSoft = 3;
     auto products = [&](auto qk, auto pv, f32x4& sum, int x, auto beside, auto soft)
         __attribute__((always_inline)) {
-      constexpr int MQ = decltype(qk)::value ? MK : 0, MV = decltype(pv)::value ? 2 * ND : 0;
-      const char *kt = s_t[(x - b0) & 3], *vt = s_t[(x - b0 - 1) & 3], *pt = s_p[(x - 1) & 1];
+      constexpr int MQ = decltype(qk)::value ? MW : 0, MV = decltype(pv)::value ? 2 * ND : 0;
+      const char *kt = s_t[(x - b0) & 3], *vt = s_t[(x - b0 - 1) & 3];
       u32x4 op[MQ + MV], pb[2][RT];
       f32x4 sn[2];
       auto read = [&](int i) __attribute__((always_inline)) {
         op[i] = i < MQ ? read_k(kt, i) : read_v(vt, (i - MQ) / ND, (i - MQ) % ND);
       };
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) read(i);
+      for (int i = 0; i < kAhead && i < MQ + MV; ++i) read(i);
 #pragma unroll
       for (int i = 0; i < MQ + MV; ++i) {
         __builtin_amdgcn_sched_barrier(0);
@@ -437,12 +474,12 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
           for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-              pb[ks][t] = *(const u32x4*)(pt + ((p_from + 32 * 64 * t) ^ (32 * ks)));
+              pb[ks][t] = *(const u32x4*)(s_p + ((p_from + 32 * 64 * t) ^ (32 * ks)));
         }
         if (i < MQ) {
           use_k(sn, op[i], i);
           if (!beside(i)) return false;
-          if (i == MQ - 1) sum = sn[0] + sn[1];
+          if (i == MQ - 1) give(sn);
         } else {
           const int ks = (i - MQ) / ND, d = (i - MQ) % ND;
           u32x4 va = op[i];
@@ -451,13 +488,21 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
                        from_e4m3<BF, false>(op[i][1]), from_e4m3<BF, true>(op[i][1])};
 #pragma unroll
           for (int t = 0; t < RT; ++t) o[d][t] = mfma32<BF>(va, pb[ks][t], o[d][t]);
-          soft(i - MQ);
+          if (MQ && i == MQ) {
+            lds_barrier();
+            sum = take(sn);
+          }
+          if (MQ && i > MQ) soft(i - MQ - 1);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (MQ && MV) {
+      if (MQ && !MV) {
+        lds_barrier();
+        sum = take(sn);
+      }
+      if (MQ) {
 #pragma unroll
-        for (int i = MV; i < kSoft; ++i) soft(i);
+        for (int i = MV ? MV - 1 : 0; i < kSoft; ++i) soft(i);
       }
       return true;
     };
@@ -524,9 +569,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       state2 = issue(b0 + 2);
       state3 = place(b0 + 3);
       bool plain = whole(x) && st >= 0;
-      products(std::true_type{}, std::false_type{}, sa, x, [](int) { return true; }, [](int) {});
-#pragma unroll
-      for (int i = 0; i < kSoft; ++i) soft(sa, x, plain, i);
+      products(std::true_type{}, std::false_type{}, sa, x, [](int) { return true; },
+               [&](int i) { soft(sa, x, plain, i); });
       if (!plain) soft_masked(sa, x, st);
       // Tile x: its P stands in LDS, computed with the maxima of before unless told
       // otherwise. A step computes the scores and P of tile x + 1 and the product
@@ -553,7 +597,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
           plain = whole(x + 1) && state1 >= 0;
           // what has been told is looked at behind operand kTold of the first product,
           // the loads are spread over those that follow
-          constexpr int kTold = MK / 3, PER = (LOADS + MK - kTold - 2) / (MK - kTold - 1);
+          constexpr int kTold = MW / 3, PER = (LOADS + MW - kTold - 2) / (MW - kTold - 1);
           const bool went = products(
               std::true_type{}, std::true_type{}, sn, x + 1,
               [&](int i) __attribute__((always_inline)) {
@@ -596,7 +640,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 
     // sums of the rows
     l = xor32_reduce(xor16_reduce(l, OpSum{}), OpSum{});
-    if (g4 == 0) s_l[kq][rq * QR + lc] = l;
+    if (g4 == 0) s_x.row.l[kq][rq * QR + lc] = l;
     __syncthreads();
     const bool all = b0 == 0 && b1 == s.nb;
     if (all) {
@@ -608,7 +652,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const int r = here(32 * t + l31), half = here(lane) >> 5;
-        const float lr = s_l[0][r] + s_l[1][r];
+        const float lr = s_x.row.l[0][r] + s_x.row.l[1][r];
         const float inv = (F8 ? a.c.ks[0] : 1.0f) / lr;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -631,7 +675,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
         }
       }
       if (a.lse && tid < R && r0 + tid < rows) {
-        const float lr = s_l[0][tid] + s_l[1][tid];
+        const float lr = s_x.row.l[0][tid] + s_x.row.l[1][tid];
         a.lse[(long)s.q0 * H + r0 + tid] =
             (s_m[tid] + (__builtin_amdgcn_logf(lr) - pre_lift<BF>(s_m[tid]))) * kLn2;
       }
@@ -649,7 +693,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
                 f32x4{o[d][t][i], o[d][t][i + 1], o[d][t][i + 2], o[d][t][i + 3]};
       if (tid < R) {
         part[tid] = s_m[tid] - pre_lift<BF>(s_m[tid]);
-        part[R + tid] = s_l[0][tid] + s_l[1][tid];
+        part[R + tid] = s_x.row.l[0][tid] + s_x.row.l[1][tid];
       }
       if (b0 == 0 && tid == 0) {
         // the workgroup of the tile's last unit: the largest v that starts before its end

@@ -15,13 +15,18 @@ namespace {
 template <int N>
 struct TreeRows {
   static constexpr int W = kTreeMax / 32;
-  int par[kTreeMax];
-  uint32_t row[N][W + 1];                        // bits, then the token's depth
+  static_assert(kTreeMax <= 256, "a depth fits a byte");
+  short par[kTreeMax];                           // kTreeMax: none that there can be
+  uint8_t deep[N];
+  uint32_t row[N][W];
 
   // The parents of the sequence's m <= kTreeMax tokens, by the whole
   // workgroup; a barrier before build().
   __device__ void fetch(const int* parent, int m) {
-    for (int i = threadIdx.x; i < min(m, kTreeMax); i += blockDim.x) par[i] = parent[i];
+    for (int i = threadIdx.x; i < min(m, kTreeMax); i += blockDim.x) {
+      const int p = parent[i];
+      par[i] = (short)(p < -1 || p > kTreeMax ? kTreeMax : p);
+    }
   }
   // Rows of tokens t0 .. t1 - 1 behind C tokens of context, a thread each; a
   // barrier before their use.
@@ -39,7 +44,7 @@ struct TreeRows {
     };
     int depth = -1;
     for (int a = t; a >= 0; a = up(a)) ++depth;
-    r[W] = depth;
+    deep[threadIdx.x] = (uint8_t)depth;
     int d = depth;
     for (int a = t; a >= 0; a = up(a), --d)
       if (!window || depth - d < window || C + d < first) r[a >> 5] |= 1u << (a & 31);
@@ -51,7 +56,7 @@ struct TreeRows {
     const uint64_t lo = word(k) | word(k + 1) << 32, hi = word(k + 2);
     return lo >> sh | (sh ? hi << (64 - sh) : 0);
   }
-  __device__ int depth(int i) const { return (int)row[i][W]; }
+  __device__ int depth(int i) const { return deep[i]; }
 };
 template <>
 struct TreeRows<0> {};

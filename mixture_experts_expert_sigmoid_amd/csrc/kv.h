@@ -129,7 +129,7 @@ hipError_t launch_attn_dense(const AttnArgs& a, int fmt, hipStream_t s);
 constexpr int kLatRows = 64;
 constexpr int kLatWaves = 8;            // of a workgroup
 constexpr int kLatGrid = 256;           // workgroups, one a CU
-constexpr int kLatSeqs = 256;           // sequences per launch
+constexpr int kLatSeqs = 128;           // sequences per launch
 constexpr int kLatStart = 4;            // units of 32 keys that a tile's start counts for
 constexpr int kLatMinUnits = 2;         // that a workgroup is there for
 constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
