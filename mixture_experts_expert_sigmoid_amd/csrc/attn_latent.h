@@ -45,6 +45,12 @@ __device__ __forceinline__ LatSeq lat_seq(const AttnArgs& a, int i) {
   return s;
 }
 
+// x / hq for x < hq + kLatRows by the reciprocal h_inv = ceil(2^22 / hq): its excess
+// over 2^22 / hq is below 1, so that of x h_inv below x <= 1087, less than 2^22 / hq
+__device__ __forceinline__ int lat_token(const AttnArgs& a, int x) {
+  return (int)((uint32_t)x * a.h_inv >> 22);
+}
+
 // workgroups that share U units (32 keys of a tile of rows)
 __device__ __forceinline__ long lat_teams(long U, long grid) {
   const long w = (U + kLatMinUnits - 1) / kLatMinUnits;
@@ -152,12 +158,10 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
   auto start_of = [&](int v) { return v * each + v * rest / w32; };
   long u = start_of(wg);
   const long u_end = start_of(wg + 1);
-  int seq = 0;
-  for (int hi = a.n - 1; seq < hi;) {
-    const int mid = (seq + hi + 1) >> 1;
-    if (s_pref[mid] <= u) seq = mid; else hi = mid - 1;
-  }
-  seq = __builtin_amdgcn_readfirstlane(seq);
+  // the sequence of unit u
+  if (tid < a.n && s_pref[tid] <= u && s_pref[tid + 1] > u) s_scan[0] = tid;
+  __syncthreads();
+  int seq = __builtin_amdgcn_readfirstlane((int)s_scan[0]);
 
   const float sc = F8 ? a.scale * a.c.ks[0] : a.scale;
 
@@ -220,7 +224,9 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     const int b0 = max(0, v0 - kLatStart), b1 = v1 - kLatStart;
     if (b1 <= b0) continue;
     const int rows = s.m * H, r0 = tile * R;
-    const int tok0 = r0 / H, tok1 = (min(rows, r0 + R) - 1) / H;
+    const int have = min(R, rows - r0);          // rows of the tile
+    const int tok0 = r0 / H, head0 = r0 - tok0 * H;          // of the first
+    const int tok1 = tok0 + lat_token(a, head0 + have - 1);
     const bool tree = a.parent != nullptr;
     const int p_min = tree ? max(0, s.C) - 1 : s.C + tok0;
     const int p_max = tree ? s.L - 1 : s.C + tok1;
@@ -239,8 +245,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     if (tid < 16) s_tell[tid >> 1][tid & 1] = -1;
 
     // this lane's row in the first product
-    const int my_row = r0 + rq * QR + lc;
-    const int tok = my_row < rows ? my_row / H : -1;
+    const int my_row = rq * QR + lc;
+    const int tok = my_row < have ? tok0 + lat_token(a, head0 + my_row) : -1;
     f32x16 o[ND][RT];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -308,8 +314,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       const int lane = here(tid & 63);
       constexpr int QU = DC / 8, QL = 64 / QU, QW = R / NW;        // units, rows of a load, of a wave
       auto from = [&](int r, int un) {
-        const int g = min(r0 + r, rows - 1), tk = g / H;
-        return a.q + (long)(s.q0 + tk) * a.q_row + (g - tk * H) * a.q_head + 16 * un;
+        const int g = head0 + min(r, have - 1), tk = lat_token(a, g);
+        return a.q + (long)(s.q0 + tok0 + tk) * a.q_row + (g - tk * H) * a.q_head + 16 * un;
       };
 #pragma unroll
       for (int i = 0; i < QW / QL; ++i) {
@@ -666,15 +672,15 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       }
 #pragma unroll
       for (int i = 0; i < R * WU / 64; ++i) {
-        const int ln = here(lane), r = i * (64 / WU) + ln / WU, un = ln % WU, g = r0 + r;
+        const int ln = here(lane), r = i * (64 / WU) + ln / WU, un = ln % WU;
         const u32x4 y = *(const u32x4*)(mine + r * WB + 16 * (un ^ (r & (WU - 1))));
-        if (g < rows) {
-          const int tk = g / H;
-          *(u32x4*)(a.out + (long)(s.q0 + tk) * a.o_row + (g - tk * H) * a.o_head + w * WB +
-                    16 * un) = y;
+        if (r < have) {
+          const int g = head0 + r, tk = lat_token(a, g);
+          *(u32x4*)(a.out + (long)(s.q0 + tok0 + tk) * a.o_row + (g - tk * H) * a.o_head +
+                    w * WB + 16 * un) = y;
         }
       }
-      if (a.lse && tid < R && r0 + tid < rows) {
+      if (a.lse && tid < have) {
         const float lr = s_x.row.l[0][tid] + s_x.row.l[1][tid];
         a.lse[(long)s.q0 * H + r0 + tid] =
             (s_m[tid] + (__builtin_amdgcn_logf(lr) - pre_lift<BF>(s_m[tid]))) * kLn2;

@@ -53,6 +53,7 @@ struct AttnArgs {
   int n_tiles;           // of a key-value head
   int block0;            // first of all workgroups that this launch runs
   const int* parent;     // of each row, trees only
+  uint32_t h_inv;        // latent: see lat_token
   // dense keys (c.k, c.st, c.sh) and values (c.v): rows cu_k[i].. of S, and the
   // values that a key's heads share; strides in bytes
   const int* cu_k;
@@ -130,7 +131,7 @@ constexpr int kLatRows = 64;
 constexpr int kLatWaves = 8;            // of a workgroup
 constexpr int kLatGrid = 256;           // workgroups, one a CU
 constexpr int kLatSeqs = 128;           // sequences per launch
-constexpr int kLatStart = 4;            // units of 32 keys that a tile's start counts for
+constexpr int kLatStart = 7;            // units of 32 keys that a tile's start counts for
 constexpr int kLatMinUnits = 2;         // that a workgroup is there for
 constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
 size_t latent_ws_bytes(int D);
