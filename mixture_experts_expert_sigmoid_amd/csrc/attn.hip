@@ -77,8 +77,23 @@ size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
   return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
 }
 
+// Trees: parts for as many workgroups as run at a time, whatever the tiles. With
+// 384 / 512 / 768 / 1536 of them, us: two trees of 41 and 61 tokens, 64 heads, over
+// 50..60 k e4m3 keys 304 / 260 / 298 / 292; 48 of 9..33 over 201..4001 keys 115 /
+// 117 / 120 / 120.
+int tree_splits(long n, long T, int hq, int hkv) {
+  const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
+  const long s = (kTreeParts + tiles - 1) / tiles;
+  return (int)(s < kPreMaxParts ? s : kPreMaxParts);
+}
+
+size_t tree_ws_bytes(long n, long T, int hq, int hkv, int D) {
+  const int s = tree_splits(n, T, hq, hkv);
+  return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
+}
+
 namespace {
-AttnArgs split_prefill(const AttnArgs& all) {
+AttnArgs split_prefill(const AttnArgs& all, long most) {
   AttnArgs a = all;
   // no more parts than the most keys that a tile can see pay for, so that calls
   // over short tables, or of many rows, need no join
@@ -87,7 +102,6 @@ AttnArgs split_prefill(const AttnArgs& all) {
   const long nb = (span < cap ? span : cap) / (a.c.D == 256 ? 32 : 64);
   a.split_gain = kSplitGain / ((float)(a.T ? a.T : 1) * a.hq);
   const double pay = __builtin_sqrt((double)nb * a.split_gain);
-  long most = prefill_splits(a.n, a.T, a.hq, a.hq / a.g);
   if (most > nb / 4) most = nb / 4;
   if (most > pay) most = (long)pay;
   a.n_split = most < 1 ? 1 : (int)most;
@@ -96,21 +110,22 @@ AttnArgs split_prefill(const AttnArgs& all) {
 }  // namespace
 
 hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all);
+  const AttnArgs a = split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq / all.g));
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);
 }
 
 hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all);
+  const AttnArgs a = split_prefill(all, tree_splits(all.n, all.T, all.hq, all.hq / all.g));
   return a.c.D == 64    ? launch_tree_64(a, fmt, s)
          : a.c.D == 128 ? launch_tree_128(a, fmt, s)
                         : launch_tree_256(a, fmt, s);
 }
 
 hipError_t launch_attn_dense(const AttnArgs& all, int fmt, hipStream_t s) {
-  return launch_dense_128(split_prefill(all), fmt, s);
+  return launch_dense_128(split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq)), fmt,
+                          s);
 }
 
 size_t latent_ws_bytes(int D) {

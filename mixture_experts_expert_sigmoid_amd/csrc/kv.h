@@ -119,6 +119,8 @@ hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
 // Drafted tokens that form a tree behind the context run through the prompt
 // kernels, with ancestors in place of the tokens before.
 constexpr int kTreeMax = 256;           // tokens of one tree
+constexpr int kTreeParts = 512;         // workgroups that a call's parts are for
+size_t tree_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_tree(const AttnArgs& a, int fmt, hipStream_t s);
 // So do prompts whose keys and values are dense rows.
 constexpr int kDenseDim = 128;          // values of a head, and of a key's own

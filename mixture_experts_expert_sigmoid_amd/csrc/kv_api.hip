@@ -269,7 +269,10 @@ int moe_attn_prefill(const moe_kv_cache* cache, const moe_kv_table* table, const
 }
 
 size_t moe_attn_tree_workspace_size(const moe_kv_cache* cache, long n, long T, int n_heads) {
-  return moe_attn_prefill_workspace_size(cache, n, T, n_heads);
+  if (!ws_shape_ok(cache, n_heads) || n < 0 || n >= (1L << 20) || T < 0 ||
+      T > 0x7FFFFFFFL / n_heads)
+    return 0;
+  return moe::tree_ws_bytes(n, T, n_heads, cache->n_heads, cache->head_dim);
 }
 
 int moe_attn_tree(const moe_kv_cache* cache, const moe_kv_table* table, const int* slots, long n,
@@ -282,7 +285,7 @@ int moe_attn_tree(const moe_kv_cache* cache, const moe_kv_table* table, const in
   if (n == 0 && T > 0) return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;
   if (!cu_q || !parent) return MOE_ERR_NULL;
-  const size_t need = moe::prefill_ws_bytes(n, T, a.hq, a.c.hkv, a.c.D);
+  const size_t need = moe::tree_ws_bytes(n, T, a.hq, a.c.hkv, a.c.D);
   if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return MOE_ERR_WORKSPACE;
   a.cu = cu_q;
   a.T = T;
