@@ -421,7 +421,7 @@ hipError_t copy_all(const CopyLayers* cl, int n_cl, const int* from, const int* 
 // copy's first workgroup for it, and without from the launch after the copies:
 // that one gives pages back, after which refs no longer tell who was to be left.
 struct Path {
-  int slot, L, C, k;     // tokens now, those before the tree, accepted ones
+  int slot, L, C, m, k;  // tokens now, those before the tree, drafted, accepted
   const int* at;
   bool marked;           // found right by another workgroup
 };
@@ -439,13 +439,15 @@ __device__ bool path_of(const KeepArgs& a, long i, bool tell, Path& p) {
   __syncthreads();
   const int len = s_len, cap = a.t.max_pages * a.t.ps;
   const int now = (int)((uint32_t)len & ~kKeptBit);
+  p.m = m;
   p.k = c1 - c0;
   p.at = a.path + c0;
   p.marked = len < 0 && now <= cap;
   if (p.marked) {
     p.C = now - p.k;
     p.L = p.C + m;
-    return true;
+    // right as checked before it was marked, unless another entry names the slot
+    return c0 >= 0 && p.k >= 0 && c1 <= a.n_path && p.C >= 0 && p.k <= m && m <= cap - p.C;
   }
   p.L = max(0, min(len, cap));
   p.C = p.L - m;
@@ -503,7 +505,7 @@ __global__ __launch_bounds__(256) void keep_copy_kernel(CopyLayers cl, KeepArgs 
     if ((int)threadIdx.x < cnt) {
       const int j = j0 + threadIdx.x, x = p.at[j];
       long from = -1, to = -1;
-      if (x != j) {
+      if (x > j && x < p.m) {
         from = place(p.C + x);
         to = place(p.C + j);
         if ((from | to) < 0) {
@@ -529,9 +531,7 @@ __global__ __launch_bounds__(256) void keep_kernel(KeepArgs a) {
   int* row = a.t.table + p.slot * a.t.ld;
   const int end = (int)div_up(p.L, a.t.ps);
   for (int j = (int)div_up(p.C + p.k, a.t.ps) + threadIdx.x; j < end; j += 256) {
-    const int e = row[j];
-    if (e == -1) continue;
-    row[j] = -1;
+    const int e = atomicExch(&row[j], -1);
     if (e >= 0 && e < a.t.n_pages) atomicSub(&a.t.refs[e], 1);
   }
   if (threadIdx.x == 0) a.t.len[p.slot] = p.C + p.k;

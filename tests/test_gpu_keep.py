@@ -130,6 +130,34 @@ def test_refusals_leave_the_slot():
     turn([0], [12], [[2, 9, 11]], page)
 
 
+def test_a_slot_named_twice():
+    """Not allowed, and what becomes of that slot is open; but nothing is read or
+    written outside its own tokens, other slots are as if it had not been there,
+    and no page is given back twice."""
+    c = _cache(6, 8, 48, 16, layers=2, hkv=2, D=64)
+    sim = Sim(6, 8, 48, 16)
+    host = [x.cpu() for x in (c.k, c.v)]
+    raw = [x.view(torch.uint8) for x in host]
+    new = [60, 60, 60, 60, 60]
+    c.grow(_i([0, 1, 2, 3, 4]), _i(new))
+    sim.grow([0, 1, 2, 3, 4], new)
+    paths = [[1, 5], [0, 30, 31, 58], [2, 4, 40], list(range(0, 60, 3)), [9]]
+    _call(c, [0, 2, 2, 2, 4], [40, 60, 45, 60, 20], paths)
+    keep(sim, raw, [0, 4], [40, 20], [paths[0], paths[4]])
+    assert M.moe_read_device_error(c.err_word) & ~M.MOE_DEVERR_TREE == 0
+    other = [0, 1, 3, 4]
+    table, refs = c.table.cpu(), c.refs.cpu()
+    assert c.lens[other].tolist() == [sim.len[s] for s in other]
+    for s in other:
+        assert table[s].tolist() == list(sim.t[s])
+    mine = {int(e) for e in table[2] if e >= 0} | {e for e in sim.t[2] if e >= 0}
+    assert 0 <= int(c.lens[2]) <= 60 and set(refs.tolist()) <= {0, 1}
+    for x, y in zip((c.k, c.v), host):
+        for p in range(48):
+            if p not in mine:
+                assert torch.equal(x[:, p].view(torch.uint8).cpu(), y[:, p].view(torch.uint8)), p
+
+
 def test_list_entries_outside_the_path():
     """cu beyond the path, falling or negative: those entries are left."""
     c = _cache(4, 4, 20, 16, layers=1)
