@@ -8,7 +8,12 @@ continues one sequence twice, single-token steps with pages that the window has
 passed returned to the pool, a sequence that ends, and a compaction with more
 steps after it.
 
-    python examples/paged_decoder.py [--kv e4m3] [--check]
+With --drafts, as many turns follow in which a tree of drafted tokens behind each
+sequence is tried in one step (moe_attn_tree), and the branch that the decoder
+would have taken itself is kept (moe_cache_keep). The drafts come from the
+decoder without its layers.
+
+    python examples/paged_decoder.py [--kv e4m3] [--drafts N] [--check]
 
 --check recomputes every attention call densely in 64 bits from the keys and
 values as they were handed to the cache.
@@ -67,13 +72,29 @@ class Dense:
             old = self.kv.get((layer, s))
             self.kv[layer, s] = kv if old is None else [torch.cat(p) for p in zip(old, kv)]
 
-    def check(self, layer, slots, cu, q, out):
+    def keep(self, slots, rows, paths):
+        for (layer, s), kv in self.kv.items():
+            if s in slots:
+                m, path = rows[slots.index(s)], paths[slots.index(s)]
+                at = [kv[0].shape[0] - m + a for a in path]
+                self.kv[layer, s] = [torch.cat([x[:x.shape[0] - m], x[at]]) for x in kv]
+
+    def check(self, layer, slots, cu, q, out, parents=None):
         for i, s in enumerate(slots):
             k, v = self.kv[layer, s]
             L, m = k.shape[0], cu[i + 1] - cu[i]
             j = torch.arange(L, device="cuda")
             p = torch.arange(L - m, L, device="cuda")[:, None]
             see = (j <= p) & ((p - j < WINDOW) | (j < FIRST))
+            if parents:                          # the context and the token's ancestors
+                C, depth = L - m, []
+                for r, a in enumerate(parents[i]):
+                    depth.append(depth[a] + 1 if a >= 0 else 0)
+                    see[r] = (j < C) & ((C + depth[r] - j < WINDOW) | (j < FIRST))
+                    e = r
+                    while e >= 0:
+                        see[r, C + e] = depth[r] - depth[e] < WINDOW or C + depth[e] < FIRST
+                        e = parents[i][e]
             for h in range(HQ):
                 kh, vh = k[:, h // (HQ // HKV)].contiguous(), v[:, h // (HQ // HKV)].contiguous()
                 x = (q[cu[i]:cu[i + 1], h].double()[:, None, :] * kh).sum(-1) * D ** -0.5
@@ -101,9 +122,10 @@ class Decoder:
     def _i32(self, x):
         return torch.tensor(x, dtype=torch.int32, device="cuda")
 
-    def step(self, slots, tokens):
+    def step(self, slots, tokens, parents=None):
         """tokens: a list of new tokens for each slot. Returns the logits after
-        the last of each."""
+        the last of each; with parents, which make a tree of each slot's tokens,
+        the logits after every one."""
         rows = [len(t) for t in tokens]
         cu = [0]
         for m in rows:
@@ -114,20 +136,45 @@ class Decoder:
         for i, layer in enumerate(self.layers):
             q, k, v = (_norm(x) @ layer.qkv.t()).view(-1, HQ + 2 * HKV, D).split([HQ, HKV, HKV], 1)
             self.cache.append(i, sl, start, cu_d, k, v)
-            if max(rows) == 1:
+            if parents:
+                y = self.cache.tree(i, sl, q, cu_d, self._i32(sum(parents, [])), D ** -0.5,
+                                    window=WINDOW, n_first=FIRST)
+            elif max(rows) == 1:
                 y = self.cache.decode(i, sl, q, D ** -0.5, window=WINDOW, n_first=FIRST)
             else:
                 y = self.cache.prefill(i, sl, q, cu_d, D ** -0.5, window=WINDOW, n_first=FIRST)
             if self.dense:
                 self.dense.add(i, slots, cu, k, v)
-                self.dense.check(i, slots, cu, q, y)
+                self.dense.check(i, slots, cu, q, y, parents)
             x = x + y.reshape(-1, HQ * D) @ layer.o.t()
             z = _norm(x)
             out = layer.experts.forward(z, (z @ layer.gate.t()).float())
             self.err |= out["err_word"]
             x = x + out["out"].bfloat16()
-        last = torch.tensor(cu[1:], device="cuda") - 1
+        last = slice(None) if parents else torch.tensor(cu[1:], device="cuda") - 1
         return (_norm(x[last]) @ self.head.t()).float()
+
+    def draft(self, token, wide, depth):
+        """A tree behind `token`: `wide` successors of it, then the best one of
+        each, by the embedding alone. Returns its tokens and their parents."""
+        tokens, parents, last = [token], [-1], [0]
+        for _ in range(depth):
+            x = self.embed[torch.tensor([tokens[i] for i in last], device="cuda")]
+            best = (_norm(x) @ self.head.t()).topk(wide if len(last) == 1 else 1).indices.tolist()
+            new = [(t, p) for p, ts in zip(last, best) for t in ts]
+            last = list(range(len(tokens), len(tokens) + len(new)))
+            tokens += [t for t, _ in new]
+            parents += [p for _, p in new]
+        return tokens, parents
+
+    def keep(self, slots, rows, paths):
+        cu = [0]
+        for p in paths:
+            cu.append(cu[-1] + len(p))
+        self.cache.keep(self._i32(slots), self._i32(rows), self._i32(cu),
+                        self._i32(sum(paths, [])))
+        if self.dense:
+            self.dense.keep(slots, rows, paths)
 
     def trim(self, slots):
         self.cache.trim(self._i32(slots), WINDOW, FIRST)
@@ -192,12 +239,43 @@ def session(kv="bf16", check=False, steps=40):
     return dec, text, used
 
 
+def drafted(dec, text, slots, turns, wide=3, depth=4):
+    """Continues the texts by turns of drafted trees. Returns the tokens kept."""
+    kept = 0
+    for _ in range(turns):
+        trees = [dec.draft(text[s][-1], wide, depth) for s in slots]
+        tokens, parents = [t for t, _ in trees], [p for _, p in trees]
+        best, paths, at = dec.step(slots, tokens, parents).argmax(-1).tolist(), [], 0
+        for s, t, p in zip(slots, tokens, parents):
+            path = [0]
+            while True:                          # the child that was the best token
+                text[s].append(best[at + path[-1]])
+                child = [i for i in range(len(t)) if p[i] == path[-1] and t[i] == text[s][-1]]
+                if not child:
+                    break
+                path.append(child[0])
+            paths.append(path)
+            at += len(t)
+            kept += len(path)
+        dec.keep(slots, [len(t) for t in tokens], paths)
+        dec.trim(slots)
+    errors = M.moe_read_device_error(dec.cache.err_word) | M.moe_read_device_error(dec.err)
+    if errors:
+        raise RuntimeError(f"error word {errors:#x}")
+    return kept
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--kv", choices=["bf16", "e4m3"], default="bf16")
+    ap.add_argument("--drafts", type=int, default=0)
     ap.add_argument("--check", action="store_true")
     args = ap.parse_args()
     decoder, text, used = session(args.kv, args.check)
+    if args.drafts:
+        slots = [1, 2, 4]
+        n = drafted(decoder, text, slots, args.drafts)
+        print(f"drafts: {n / (args.drafts * len(slots)):.2f} tokens kept a turn")
     for s, t in text.items():
         print(f"slot {s}: {len(t)} tokens, {t[:12]} ...")
     print("pages in use:", used)

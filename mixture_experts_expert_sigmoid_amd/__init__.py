@@ -791,33 +791,27 @@ class _Workspace:
         return self.buffers[-1]
 
 
-class KvCache:
-    """A paged cache of several layers with its tables: device tensors, their
-    descriptors and a workspace. Slots are handed in as int32 device tensors.
-    Everything is enqueued on `stream` (the current one if None); calls on
-    different streams have to be ordered by the caller, as they share the
-    tables and the workspace. Graphs captured through the object hold its
+class _PagedCache:
+    """The tables, the workspace and the upkeep of a paged cache of several
+    layers: device tensors and their descriptors. Slots are handed in as int32
+    device tensors. Everything is enqueued on `stream` (the current one if None);
+    calls on different streams have to be ordered by the caller, as they share
+    the tables and the workspace. Graphs captured through the object hold its
     addresses, so it has to outlive them; later calls, larger ones too, leave
     what they use in place. Problems found on the device are ORed into
     err_word."""
 
-    def __init__(self, *, n_layers, n_pages, page_size, n_heads, head_dim, n_slots, max_pages,
-                 dtype=torch.bfloat16, k_scale=None, v_scale=None, device="cuda"):
-        shape = (n_layers, n_pages, n_heads, page_size, head_dim)
-        self.k = torch.empty(shape, dtype=dtype, device=device)
-        self.v = torch.empty(shape, dtype=dtype, device=device)
-        i32 = dict(dtype=torch.int32, device=device)
+    def __init__(self, arrays, n_pages, page_size, n_slots, max_pages):
+        """arrays: the tensors of the cached values and their scales."""
+        i32 = dict(dtype=torch.int32, device=arrays[0].device)
         self.table = torch.full((n_slots, max_pages), -1, **i32)
         self.lens = torch.zeros(n_slots, **i32)
         self.refs = torch.zeros(n_pages, **i32)
         self.err_word = torch.zeros(1, **i32)
-        # scales: [n_layers][n_heads], for float8_e4m3fn
-        self.layers = [kv_cache(self.k[i], self.v[i], None if k_scale is None else k_scale[i],
-                                None if v_scale is None else v_scale[i])
-                       for i in range(n_layers)]
         self.desc = kv_table(self.table, self.lens, page_size, n_pages, self.refs)
-        self._scales = [t for t in (k_scale, v_scale) if t is not None]
-        self._ws = _Workspace(self.k.device)
+        self._arrays = arrays
+        self._pages = []                         # every layer's pages, for the upkeep
+        self._ws = _Workspace(arrays[0].device)
         self._streams = {}                       # those that work was enqueued on
 
     def _on(self, stream):
@@ -826,14 +820,17 @@ class KvCache:
         raw = _stream(stream)
         if raw not in self._streams:
             self._streams[raw] = s = torch.cuda.current_stream() if stream is None else stream
-            for t in (self.k, self.v, self.table, self.lens, self.refs, self.err_word,
-                      *self._scales, *self._ws.buffers):
+            for t in (*self._arrays, self.table, self.lens, self.refs, self.err_word,
+                      *self._ws.buffers):
                 t.record_stream(s)
 
-    def _new(self, like, stream):
-        """An empty tensor like `like`, contiguous, of the stream it is used on."""
+    def _new(self, like, stream, D=None):
+        """An empty tensor like `like`, contiguous, of the stream it is used on;
+        with rows of D."""
         with torch.cuda.stream(stream):
-            return torch.empty_like(like, memory_format=torch.contiguous_format)
+            if D is None:
+                return torch.empty_like(like, memory_format=torch.contiguous_format)
+            return like.new_empty((*like.shape[:-1], D))
 
     def workspace(self, need, stream=None):
         """At least `need` bytes for work on `stream`."""
@@ -853,6 +850,47 @@ class KvCache:
         ws = self.workspace(moe_cache_workspace_size(self.desc, n_new.numel()), stream)
         moe_cache_grow(self.desc, slots, n_new, start, self.err_word, ws, stream)
         return start
+
+    def free(self, slots, stream=None):
+        self._on(stream)
+        moe_cache_free(self.desc, slots, self.err_word, stream)
+
+    def trim(self, slots, window, n_first=0, stream=None):
+        self._on(stream)
+        moe_cache_trim(self.desc, slots, window, n_first, self.err_word, stream)
+
+    def fork(self, src, dst, stream=None):
+        ws = self.workspace(moe_cache_workspace_size(self.desc, src.numel()), stream)
+        moe_cache_fork(self._pages, self.desc, src, dst, self.err_word, ws, stream)
+
+    def compact(self, n_used=None, stream=None):
+        ws = self.workspace(moe_cache_workspace_size(self.desc, 0), stream)
+        moe_cache_compact(self._pages, self.desc, n_used, self.err_word, ws, stream)
+
+    def keep(self, slots, n_draft, cu, path, stream=None):
+        """The accepted path of each slot's tree of drafted tokens: entries cu[i] ..
+        cu[i + 1] - 1 of path, among its n_draft[i] newest tokens. They become the
+        newest ones, and the pages of the rest are given back."""
+        self._on(stream)
+        moe_cache_keep(self._pages, self.desc, n_draft, cu, path, self.err_word, slots=slots,
+                       stream=stream)
+
+
+class KvCache(_PagedCache):
+    """A paged cache of keys and values of several layers with its tables."""
+
+    def __init__(self, *, n_layers, n_pages, page_size, n_heads, head_dim, n_slots, max_pages,
+                 dtype=torch.bfloat16, k_scale=None, v_scale=None, device="cuda"):
+        shape = (n_layers, n_pages, n_heads, page_size, head_dim)
+        self.k = torch.empty(shape, dtype=dtype, device=device)
+        self.v = torch.empty(shape, dtype=dtype, device=device)
+        super().__init__([t for t in (self.k, self.v, k_scale, v_scale) if t is not None],
+                         n_pages, page_size, n_slots, max_pages)
+        # scales: [n_layers][n_heads], for float8_e4m3fn
+        self.layers = [kv_cache(self.k[i], self.v[i], None if k_scale is None else k_scale[i],
+                                None if v_scale is None else v_scale[i])
+                       for i in range(n_layers)]
+        self._pages = self.layers
 
     def append(self, layer, slots, start, cu, k, v, stream=None):
         self._on(stream)
@@ -878,22 +916,6 @@ class KvCache:
                          n_first=n_first, slots=slots, lse=lse, stream=stream)
         return out
 
-    def free(self, slots, stream=None):
-        self._on(stream)
-        moe_cache_free(self.desc, slots, self.err_word, stream)
-
-    def trim(self, slots, window, n_first=0, stream=None):
-        self._on(stream)
-        moe_cache_trim(self.desc, slots, window, n_first, self.err_word, stream)
-
-    def fork(self, src, dst, stream=None):
-        ws = self.workspace(moe_cache_workspace_size(self.desc, src.numel()), stream)
-        moe_cache_fork(self.layers, self.desc, src, dst, self.err_word, ws, stream)
-
-    def compact(self, n_used=None, stream=None):
-        ws = self.workspace(moe_cache_workspace_size(self.desc, 0), stream)
-        moe_cache_compact(self.layers, self.desc, n_used, self.err_word, ws, stream)
-
     def tree(self, layer, slots, q, cu_q, parent, scale, out=None, window=0, n_first=0, lse=None,
              stream=None):
         """The newest tokens as drafted trees: parent int32 [T]."""
@@ -905,11 +927,49 @@ class KvCache:
                       window=window, n_first=n_first, slots=slots, lse=lse, stream=stream)
         return out
 
-    def keep(self, slots, n_draft, cu, path, stream=None):
-        """The accepted paths of the trees; the rest of them is given back."""
+
+class LatentCache(_PagedCache):
+    """A paged cache of the latent vectors and rotary keys of several layers with
+    its tables."""
+
+    def __init__(self, *, n_layers, n_pages, page_size, n_slots, max_pages, latent_dim=512,
+                 rope_dim=64, dtype=torch.bfloat16, scale=None, device="cuda"):
+        self.c = torch.empty((n_layers, n_pages, page_size, latent_dim + rope_dim), dtype=dtype,
+                             device=device)
+        super().__init__([self.c] if scale is None else [self.c, scale], n_pages, page_size,
+                         n_slots, max_pages)
+        # scale: [n_layers], for float8_e4m3fn
+        self.layers = [latent_cache(self.c[i], latent_dim,
+                                    None if scale is None else scale[i:i + 1])
+                       for i in range(n_layers)]
+        self._pages = [moe_latent_pages(c) for c in self.layers]
+
+    def append(self, layer, slots, start, cu, c, rope, stream=None):
         self._on(stream)
-        moe_cache_keep(self.layers, self.desc, n_draft, cu, path, self.err_word, slots=slots,
-                       stream=stream)
+        moe_latent_append(self.layers[layer], self.desc, start, cu, c, rope, self.err_word,
+                          slots=slots, stream=stream)
+
+    def attend(self, layer, slots, q, cu_q, scale, parent=None, out=None, window=0, n_first=0,
+               lse=None, stream=None):
+        """Absorbed attention: one token of each slot (cu_q None), the newest tokens,
+        or drafted trees (with their parents)."""
+        c = self.layers[layer]
+        out = self._new(q, stream, c.latent_dim) if out is None else out
+        n = q.shape[0] if cu_q is None else cu_q.numel() - 1
+        ws = self.workspace(moe_attn_latent_workspace_size(c, n, q.shape[0], q.shape[1]), stream)
+        moe_attn_latent(c, self.desc, q, cu_q, out, scale, self.err_word, ws, parent=parent,
+                        window=window, n_first=n_first, slots=slots, lse=lse, stream=stream)
+        return out
+
+    def prompt(self, q, k, k_rope, v, cu_q, cu_k, scale, out=None, window=0, n_first=0, lse=None,
+               stream=None):
+        """Expanded attention of prompts, over the rows the caller has expanded."""
+        out = self._new(q, stream, v.shape[-1]) if out is None else out
+        ws = self.workspace(moe_attn_latent_prompt_workspace_size(cu_q.numel() - 1, q.shape[0],
+                                                                  q.shape[1]), stream)
+        moe_attn_latent_prompt(q, k, k_rope, v, cu_q, cu_k, out, scale, ws, window=window,
+                               n_first=n_first, lse=lse, stream=stream)
+        return out
 
 
 # ------------------------------------------------------------ layer object
