@@ -112,8 +112,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
   __shared__ TreeRows<R> s_tree;
   __shared__ float s_m[R];
   __shared__ long s_scan[NW];
-  // by x % 8: tile x if its P is to be done again; if a group of it has no page
-  __shared__ __align__(8) int s_tell[8][2];
+  __shared__ int s_tell[8];                               // by x % 8: tile x if its P is to be
+                                                          // done again
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     __syncthreads();                             // of the piece before
     if (masked) s_tree.fetch(a.parent + s.q0, s.m);
     if (tid < R) s_m[tid] = kNegInf;
-    if (tid < 16) s_tell[tid >> 1][tid & 1] = -1;
+    if (tid < 8) s_tell[tid] = -1;
 
     // this lane's row in the first product
     const int my_row = rq * QR + lc;
@@ -282,11 +282,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       const int hi32 = __builtin_amdgcn_readlane((int)(offs >> 32), x - at0);
       const long off = (long)(((uint64_t)(uint32_t)max(hi32, 0) << 32) | lo32);
       src = a.c.k + (hi32 < 0 ? 0L : off) + l_from * a.c.st;
-      bytes = hi32 < 0 ? 0 : 0x7FFFFFFF;         // (nothing is read without a place)
-      if (hi32 == (int)(kMissing >> 32) && lane == 0) {
-        atomicOr(a.err, kErrPage);
-        s_tell[x & 7][1] = x;
-      }
+      bytes = hi32 < 0 ? 0 : 0x7FFFFFFF;         // (without a place: nothing, and zeros in LDS)
+      if (hi32 == (int)(kMissing >> 32) && lane == 0) atomicOr(a.err, kErrPage);
       return hi32;
     };
     auto load = [&](int x, int i) __attribute__((always_inline)) {
@@ -521,7 +518,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       }
       if (i == 1) {
         const bool more = top_of(sv) > m + kDefer<BF>;
-        if (tell & __any(more) && lane == 0) s_tell[x & 7][0] = x;
+        if (tell & __any(more) && lane == 0) s_tell[x & 7] = x;
       }
       if (i == 2) probs(sv, x);
     };
@@ -586,8 +583,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
       // first: with that in it, O would be copied from registers to registers in
       // each step.)
       auto told_of = [&](int x) {
-        return *(const volatile __attribute__((address_space(3))) i32x2*)
-            (const __attribute__((address_space(3))) int*)s_tell[x & 7];
+        return *(const volatile __attribute__((address_space(3))) int*)
+            (const __attribute__((address_space(3))) int*)&s_tell[x & 7];
       };
       int ready = b0 - 1;                        // the tile that it has been done for
       while (true) {
@@ -597,7 +594,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
             lds_barrier();
           }
           if (x + 1 >= x_end || (ready != x && !whole(x))) break;
-          const i32x2 tell = told_of(x);
+          const int tell = told_of(x);
           f32x4 sn = {0, 0, 0, 0};
           int next = 0;
           plain = whole(x + 1) && state1 >= 0;
@@ -608,7 +605,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
               std::true_type{}, std::true_type{}, sn, x + 1,
               [&](int i) __attribute__((always_inline)) {
                 if (i == kTold) {
-                  if (ready != x && __builtin_amdgcn_readfirstlane((tell[0] == x) | (tell[1] == x)))
+                  if (ready != x && __builtin_amdgcn_readfirstlane(tell) == x)
                     return false;
                   l += pend;
                 }
@@ -631,9 +628,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
           sa = sn;
         }
         if (ready != x) {
-          const i32x2 tell = told_of(x);
-          if (__builtin_amdgcn_readfirstlane(tell[0]) == x) follow(sa, x);
-          if (__builtin_amdgcn_readfirstlane(tell[1]) == x || !whole(x)) clean(s_t[(x - b0) & 3]);
+          if (__builtin_amdgcn_readfirstlane(told_of(x)) == x) follow(sa, x);
+          if (!whole(x)) clean(s_t[(x - b0) & 3]);
           ready = x;
         }
         if (x + 1 >= x_end) break;

@@ -188,3 +188,26 @@ def test_rows_outside_the_lists_and_graph():
         part.cu, part.host = np.array([0, lens[0], sum(lens)]), rows.host
         want = want_of(part, m, q[20:20 + sum(m)], 0, 0, 0.07)
         check(replayed[20:20 + sum(m)].double().cpu().numpy(), want[0], want[2], "out")
+
+
+def test_no_keys_and_no_rows():
+    """Calls without a key, and sequences without keys or rows among others."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = dict(dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(16, M.moe_attn_latent_prompt_workspace_size(4, 80, 3)),
+                     dtype=torch.uint8, device="cuda")
+    q, out = torch.randn(3, 3, 192, **b), torch.full((3, 3, 128), 7.0, **b)
+    lse = torch.full((3, 3), 7.0, device="cuda")
+    none = torch.empty(0, 3, 128, **b)
+    M.moe_attn_latent_prompt(q, none, torch.empty(0, 64, **b), none,
+                             torch.tensor([0, 1, 3], **i32), torch.tensor([0, 0, 0], **i32), out,
+                             0.07, ws, lse=lse)
+    assert (out == 0).all() and (lse == -np.inf).all()
+    rng = np.random.default_rng(8)
+    rows = Rows(rng, "bf16", 3, [5, 0, 70, 9])
+    q = _q(rng, 75, 3, D + R, "bf16")
+    out, lse = run(rows, [5, 3, 67, 0], q, 0, 0, 0.07)
+    want = want_of(rows, [5, 3, 67, 0], q, 0, 0, 0.07)
+    check(out, want[0], want[2], "out")
+    check(lse, want[1], want[3], "lse")
+    assert (out[5:8] == 0).all() and (lse[5:8] == -np.inf).all()
