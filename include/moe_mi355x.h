@@ -603,9 +603,10 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * MOE_DEVERR_CACHE_PAGE. No dst occurs twice or is also a src.
  *
  * layers: host array of n_layers (1..1024) caches alike in all but their
- * pointers and scales; a cache whose v is its k has one array. Limits: 0 <= n < 2^20, for fork 0 <= n <= 65535, for
- * copy_pages 0 <= n < 2^31. Workspace: moe_cache_workspace_size(table, n)
- * bytes, 16-byte aligned, serve grow, fork and compact for up to n slots. */
+ * pointers and scales; a cache whose v is its k has one array. Limits: 0 <= n <
+ * 2^20, for fork 0 <= n <= 65535, for copy_pages 0 <= n < 2^31, for keep 0 <=
+ * n_path < 2^31. Workspace: moe_cache_workspace_size(table, n) bytes, 16-byte
+ * aligned, serve grow, fork and compact for up to n slots; keep takes none. */
 int moe_cache_grow(const moe_kv_table *table, const int *slots,
                    const int *n_new, long n, int *start, int *err_word,
                    void *ws, size_t ws_bytes, void *stream);
@@ -673,7 +674,9 @@ int moe_latent_append(const moe_latent_cache *cache, const moe_kv_table *table,
  * one row each, T = n) are the newest tokens of slots[i] (NULL: i): what they
  * see of each other goes by parent as in moe_attn_tree, or, without (NULL), by
  * their order as in moe_attn_prefill. The keys of all rows are dealt out evenly
- * over the GPU and the parts joined in a fixed order. Limits: 0 <= n < 2^20,
+ * over the GPU and the parts joined in a fixed order. A key that is not finite
+ * makes the rows that see it NaN, unless it gives them a score of -infinity and
+ * with it no part in the sum. Limits: 0 <= n < 2^20,
  * T < 2^31 / n_heads. Workspace: moe_attn_latent_workspace_size(cache, n, T,
  * n_heads) bytes. Errors as for moe_attn_decode. */
 int moe_attn_latent(const moe_latent_cache *cache, const moe_kv_table *table,

@@ -1,5 +1,42 @@
 // Attention over a paged cache of latent vectors: keys are a token's latent
 // vector and rotary key, values its latent vector, all query heads share them.
+//
+// Mathematics. As for prompts (one pass with the running maximum and sum, S^T =
+// K Q^T, P = 2^(S - m), O^T = V^T P^T, fp32 but for the 16-bit operands, m
+// followed only when it has grown by 2^kDefer), with one key head of 576 or 320
+// values and g = all query heads: a tile of 64 rows, (token, head) pairs
+// token-major, uses each latent vector 64 times in both products, and a vector
+// is read from memory once, as key and as value. Codes of e4m3 caches are
+// multiplied as they are; the scale goes into the softmax's and the result's.
+//
+// Layout. O of 64 rows is 128 KB, a quarter of a CU's registers, so a CU holds one
+// workgroup of eight waves: in the second product each has 64 of the 512 values
+// for all rows, in the first 16 keys and 16 rows, of which it multiplies half the
+// depth for 32 rows (an operand of K, read from LDS, then serves twice) and
+// trades the other rows' half with the wave next to it. Q lives in registers, K
+// in four LDS buffers of 32 keys, written by DMA three tiles ahead and waited for
+// by count, never emptied; V is the same bytes read transposed
+// (ds_read_b64_tr_b16, _b8 for codes). The scores and P of tile x + 1 are
+// computed among the products of tile x, in written order; two barriers a tile.
+// What is rare (masks, a maximum that grew, values that are not finite) stands
+// outside the loop: within, it made the compiler copy O in each step.
+//
+// Work. The keys of all tiles, end to end, are dealt out evenly to at most 256
+// workgroups, whatever the lengths; a tile's start (places, queries, an empty
+// pipeline: 5 us) counts as kLatStart units of 32 keys. Parts of a tile are
+// joined in order by a second launch. The counts are computed by every workgroup
+// from the lengths, up to kLatSeqs sequences a launch.
+//
+// Bound. A step (32 keys, 64 rows, 4.5 MFLOP) takes 1.25 us, 0.91 PFLOP/s over 256
+// CUs: 37 % of its cycles issue matrix instructions and as many move LDS, and eight
+// waves in step overlap them no better. Reading further ahead, K across the
+// barrier, other places for the loads: no change. Beside the steps there are 2 us
+// of prologue, 5 a piece of start and the parts, 131 KB each, written and read.
+// Measured: a token of 64 sequences of 201..4001 keys, 128 heads (177 MB, 38
+// GFLOP) 80 us, 66 of it this kernel and 13 the join; trees over e4m3 (142 GFLOP)
+// 181 us, 0.78 PFLOP/s; one token of 16 heads over 777 keys 18.8 us, latency. The
+// first form (four waves, O in the accumulators' half of the registers, waits by
+// the compiler) took 173 us and 294.
 #pragma once
 #include <type_traits>
 
@@ -715,7 +752,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 // Joins the parts of the tile that workgroup blockIdx.x of the kernel above left
 // open, in their order. A run, 32 values of 32 rows, is a wave's, 16 values a lane;
 // a workgroup has four of them (blockIdx.y). Up to kLatFew parts: a wave each;
-// more: one run after another, every fourth part to each wave.
+// more: one run after another, every fourth part to each wave. Bound by the parts'
+// bytes for batches (50 MB in 13 us), by latency else (5 us).
 constexpr int kLatFew = 16;
 template <bool BF, bool F8, int DC>
 __global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
