@@ -728,8 +728,9 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *(f32x4*)(part + 2 * R + ((((w * ND + d) * RT + t) * 4 + (i >> 2)) * 64 + ln) * 4) =
-                f32x4{o[d][t][i], o[d][t][i + 1], o[d][t][i + 2], o[d][t][i + 3]};
+            if (32 * t + (ln & 31) < have)
+              *(f32x4*)(part + 2 * R + ((((w * ND + d) * RT + t) * 4 + (i >> 2)) * 64 + ln) * 4) =
+                  f32x4{o[d][t][i], o[d][t][i + 1], o[d][t][i + 2], o[d][t][i + 3]};
       if (tid < R) {
         part[tid] = s_m[tid] - pre_lift<BF>(s_m[tid]);
         part[R + tid] = s_x.row.l[0][tid] + s_x.row.l[1][tid];
@@ -750,45 +751,51 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 }
 
 // Joins the parts of the tile that workgroup blockIdx.x of the kernel above left
-// open, in their order. A run, 32 values of 32 rows, is a wave's, 16 values a lane;
-// a workgroup has four of them (blockIdx.y). Up to kLatFew parts: a wave each;
-// more: one run after another, every fourth part to each wave. Bound by the parts'
-// bytes for batches (50 MB in 13 us), by latency else (5 us).
-constexpr int kLatFew = 16;
-template <bool BF, bool F8, int DC>
-__global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
-  constexpr int R = kLatRows, RT = R / 32;
-  __shared__ f32x4 s_o[3][4][64];
-  __shared__ float s_ml[3][2][32];
+// open, in their order. A run is 32 values of 32 rows, 16 values a lane. A wave has
+// one to itself, or, SPREAD, for few tiles of many parts, a workgroup has, every
+// kLatJoin-th part to each wave. Bound by the parts' bytes for batches (50 MB in 13
+// us), by latency else.
+constexpr int kLatJoin = 8;
+template <bool BF, bool F8, int DC, bool SPREAD>
+__global__ __launch_bounds__(SPREAD ? 64 * kLatJoin : 256) void latent_join_kernel(AttnArgs a) {
+  constexpr int R = kLatRows, RT = R / 32, NW = SPREAD ? kLatJoin : 1;
+  __shared__ f32x4 s_o[NW][4][64];
+  __shared__ float s_ml[NW][2][32];
   const int wg = blockIdx.x;
   const i32x4 meta = *(const i32x4*)(a.meta + 4 * wg);     // q0, rows, first row, parts
   const int cnt = meta[3];
-  if (cnt == 0) return;
   const int lane = lane_id(), w = threadIdx.x >> 6, l31 = lane & 31, half = lane >> 5;
+  const int run = SPREAD ? (int)blockIdx.y : 4 * (int)blockIdx.y + w;
+  const int t = run % RT, g = meta[2] + 32 * t + l31;      // of the sequence's rows
+  if (cnt == 0 || meta[2] + 32 * t >= meta[1]) return;
+  const bool there = g < meta[1];
   const long pf = lat_part_floats(DC);
   // part k: of the workgroup that opened the tile, then those that went on
   auto part = [&](int k) { return a.part + (long)(2 * (wg + k) + (k == 0)) * pf; };
-  struct State {
-    float m, l;
-    f32x4 o[4];
-  };
-  const f32x4 zero = {0, 0, 0, 0};
-  auto scale = [](State& s, float f) {
-    s.l *= f;
+  float m = kNegInf, l = 0.0f;
+  f32x4 o[4] = {};
+  auto scale = [&](float f) {
+    l *= f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s.o[i][e] *= f;
+      for (int e = 0; e < 4; ++e) o[i][e] *= f;
   };
-  // adds parts k0, k0 + stride, ... of a run, four at a time
-  auto add = [&](State& s, int run, int k0, int stride) {
-    const int t = run % RT;
-    for (; k0 < cnt; k0 += 4 * stride) {
-      f32x4 y[4][4];
-      float pm[4], pl[4];
+  auto add = [&](float f, float pl, const f32x4 (&y)[4]) {
+    l += f * pl;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] += f * y[i][e];
+  };
+  const int step = SPREAD ? NW : 1;
+  for (int k0 = SPREAD ? w : 0; k0 < cnt; k0 += 4 * step) {
+    f32x4 y[4][4];
+    float pm[4], pl[4];
+    if (there) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = k0 + j * stride;
+        const int k = k0 + j * step;
         const float* p = part(k < cnt ? k : k0);
         pm[j] = k < cnt ? p[32 * t + l31] : kNegInf;
         pl[j] = p[R + 32 * t + l31];
@@ -796,85 +803,57 @@ __global__ __launch_bounds__(256) void latent_join_kernel(AttnArgs a) {
         for (int i = 0; i < 4; ++i)
           y[j][i] = *(const f32x4*)(p + 2 * R + ((run * 4 + i) * 64 + lane) * 4);
       }
-      float mn = s.m;
+      float mn = m;
 #pragma unroll
       for (int j = 0; j < 4; ++j) mn = fmaxf(mn, pm[j]);
       const float mu = mn == kNegInf ? 0.0f : mn;
-      scale(s, exp2_fast(s.m - mu));
+      scale(exp2_fast(m - mu));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 + j * stride >= cnt) continue;
-        const float f = exp2_fast(pm[j] - mu);
-        s.l += f * pl[j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s.o[i][e] += f * y[j][i][e];
-      }
-      s.m = mn;
+      for (int j = 0; j < 4; ++j)
+        if (k0 + j * step < cnt) add(exp2_fast(pm[j] - mu), pl[j], y[j]);
+      m = mn;
     }
-  };
-  auto write = [&](const State& s, int run) {
-    const int H = a.hq, g = meta[2] + 32 * (run % RT) + l31, dt = run / RT;
-    if (g >= meta[1]) return;
-    const int tk = g / H;
-    const float inv = (F8 ? a.c.ks[0] : 1.0f) / s.l;
-    char* dst = a.out + (long)(meta[0] + tk) * a.o_row + (g - tk * H) * a.o_head + 64 * dt +
-                8 * half;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *(u32x2*)(dst + 16 * i) = u32x2{
-          pack16<BF>(of_sum(s.o[i][0], inv, s.l), of_sum(s.o[i][1], inv, s.l)),
-          pack16<BF>(of_sum(s.o[i][2], inv, s.l), of_sum(s.o[i][3], inv, s.l))};
-    if (a.lse && dt == 0 && half == 0)
-      a.lse[(long)meta[0] * H + g] = (s.m + __builtin_amdgcn_logf(s.l)) * kLn2;
-  };
-  if (cnt <= kLatFew) {
-    State s{kNegInf, 0.0f, {zero, zero, zero, zero}};
-    add(s, 4 * blockIdx.y + w, 0, 1);
-    write(s, 4 * blockIdx.y + w);
-    return;
   }
-  for (int run = 4 * blockIdx.y; run < 4 * (int)blockIdx.y + 4; ++run) {
-    State s{kNegInf, 0.0f, {zero, zero, zero, zero}};
-    add(s, run, w, 4);
-    if (w) {
+  if constexpr (SPREAD) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s_o[w - 1][i][lane] = s.o[i];
-      if (half == 0) {
-        s_ml[w - 1][0][l31] = s.m;
-        s_ml[w - 1][1][l31] = s.l;
-      }
+    for (int i = 0; i < 4; ++i) s_o[w][i][lane] = o[i];
+    if (half == 0) {
+      s_ml[w][0][l31] = m;
+      s_ml[w][1][l31] = l;
     }
     __syncthreads();
-    if (w == 0) {
-      float mn = s.m;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) mn = fmaxf(mn, s_ml[k][0][l31]);
-      const float mu = mn == kNegInf ? 0.0f : mn;
-      scale(s, exp2_fast(s.m - mu));
-      s.m = mn;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float f = exp2_fast(s_ml[k][0][l31] - mu);
-        s.l += f * s_ml[k][1][l31];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 y = s_o[k][i][lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s.o[i][e] += f * y[e];
-        }
-      }
-      write(s, run);
+    if (w) return;
+    const int n = min(cnt, NW);
+    float mn = m;
+    for (int k = 1; k < n; ++k) mn = fmaxf(mn, s_ml[k][0][l31]);
+    const float mu = mn == kNegInf ? 0.0f : mn;
+    scale(exp2_fast(m - mu));
+    m = mn;
+    for (int k = 1; k < n; ++k) {
+      const f32x4 y[4] = {s_o[k][0][lane], s_o[k][1][lane], s_o[k][2][lane], s_o[k][3][lane]};
+      add(exp2_fast(s_ml[k][0][l31] - mu), s_ml[k][1][l31], y);
     }
-    __syncthreads();
   }
+  if (!there) return;
+  const int H = a.hq, tk = g / H, dt = run / RT;
+  const float inv = (F8 ? a.c.ks[0] : 1.0f) / l;
+  char* dst = a.out + (long)(meta[0] + tk) * a.o_row + (g - tk * H) * a.o_head + 64 * dt + 8 * half;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *(u32x2*)(dst + 16 * i) = u32x2{pack16<BF>(of_sum(o[i][0], inv, l), of_sum(o[i][1], inv, l)),
+                                    pack16<BF>(of_sum(o[i][2], inv, l), of_sum(o[i][3], inv, l))};
+  if (a.lse && dt == 0 && half == 0)
+    a.lse[(long)meta[0] * H + g] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <bool BF, bool F8, int DC>
 hipError_t run_latent(const AttnArgs& a, int grid, hipStream_t s) {
   attn_latent_kernel<BF, F8, DC><<<grid, 64 * kLatWaves, 0, s>>>(a);
-  latent_join_kernel<BF, F8, DC><<<dim3(grid, DC / 32 * (kLatRows / 32) / 4), 256, 0, s>>>(a);
+  constexpr unsigned runs = DC / 32 * (kLatRows / 32);
+  if (a.spread)
+    latent_join_kernel<BF, F8, DC, true><<<dim3(grid, runs), 64 * kLatJoin, 0, s>>>(a);
+  else
+    latent_join_kernel<BF, F8, DC, false><<<dim3(grid, runs / 4), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
