@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     auto whole = [&](int x) { return x >= whole0 && x < whole1; };
     const bool masked = tree && (b0 < whole0 || x_end > whole1);
 
-    __syncthreads();                             // of the piece before
+    lds_barrier();                               // of the piece before, whose stores may go on
     if (masked) s_tree.fetch(a.parent + s.q0, s.m);
     if (tid < R) s_m[tid] = kNegInf;
     if (tid < 8) s_tell[tid] = -1;
@@ -680,7 +680,7 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     // sums of the rows
     l = xor32_reduce(xor16_reduce(l, OpSum{}), OpSum{});
     if (g4 == 0) s_x.row.l[kq][rq * QR + lc] = l;
-    __syncthreads();
+    lds_barrier();
     const bool all = b0 == 0 && b1 == s.nb;
     if (all) {
       // turned round through LDS, 64-byte runs of a wave's rows

@@ -135,8 +135,8 @@ constexpr int kLatWaves = 8;            // of a workgroup
 constexpr int kLatGrid = 256;           // workgroups, one a CU
 constexpr int kLatSeqs = 128;           // sequences per launch
 constexpr int kLatStart = 7;            // units of 32 keys that a tile's start counts for
-constexpr int kLatFew = 8;              // parts of a tile that a wave by itself joins
-constexpr int kLatMinUnits = 2;         // that a workgroup is there for
+constexpr int kLatFew = 16;             // parts of a tile that a wave by itself joins
+constexpr int kLatMinUnits = 4;         // that a workgroup is there for
 constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
 size_t latent_ws_bytes(int D);
 hipError_t launch_attn_latent(const AttnArgs& a, int fmt, hipStream_t s);
