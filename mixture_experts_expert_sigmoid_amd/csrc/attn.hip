@@ -80,21 +80,26 @@ size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
 // Trees: parts for as many workgroups as run at a time, whatever the tiles. With
 // 384 / 512 / 768 / 1536 of them, us: two trees of 41 and 61 tokens, 64 heads, over
 // 50..60 k e4m3 keys 304 / 260 / 298 / 292; 48 of 9..33 over 201..4001 keys 115 /
-// 117 / 120 / 120.
-int tree_splits(long n, long T, int hq, int hkv) {
+// 117 / 120 / 120. With head_dim 256, whose workgroups have a CU each, no more than
+// fit: a few beyond 256 are a second round (8 trees of 2..23 tokens, 64 heads over 4,
+// 1400 keys: 47 us, with 320 workgroups 60). A part of a tree has two tiles of keys at
+// least, of a prompt four: one tree over 777 keys 14.9 us against 16.6, three of 1..8
+// tokens within a window of 907 31.8 against 29.9.
+int tree_splits(long n, long T, int hq, int hkv, int D) {
   const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
-  const long s = (kTreeParts + tiles - 1) / tiles;
-  return (int)(s < kPreMaxParts ? s : kPreMaxParts);
+  const long s = D == 256 ? kTreeParts / 2 / tiles : (kTreeParts + tiles - 1) / tiles;
+  return (int)(s < 1 ? 1 : s < kPreMaxParts ? s : kPreMaxParts);
 }
 
 size_t tree_ws_bytes(long n, long T, int hq, int hkv, int D) {
-  const int s = tree_splits(n, T, hq, hkv);
+  const int s = tree_splits(n, T, hq, hkv, D);
   return s > 1 ? (size_t)s * T * hq * (D + 2) * 4 : 0;
 }
 
 namespace {
-AttnArgs split_prefill(const AttnArgs& all, long most) {
+AttnArgs split_prefill(const AttnArgs& all, long most, int part_min) {
   AttnArgs a = all;
+  a.part_min = part_min;
   // no more parts than the most keys that a tile can see pay for, so that calls
   // over short tables, or of many rows, need no join
   const long cap = (long)a.t.max_pages * a.t.ps;
@@ -102,7 +107,7 @@ AttnArgs split_prefill(const AttnArgs& all, long most) {
   const long nb = (span < cap ? span : cap) / (a.c.D == 256 ? 32 : 64);
   a.split_gain = kSplitGain / ((float)(a.T ? a.T : 1) * a.hq);
   const double pay = __builtin_sqrt((double)nb * a.split_gain);
-  if (most > nb / 4) most = nb / 4;
+  if (most > nb / part_min) most = nb / part_min;
   if (most > pay) most = (long)pay;
   a.n_split = most < 1 ? 1 : (int)most;
   return a;
@@ -110,21 +115,21 @@ AttnArgs split_prefill(const AttnArgs& all, long most) {
 }  // namespace
 
 hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq / all.g));
+  const AttnArgs a = split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq / all.g), 4);
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);
 }
 
 hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all, tree_splits(all.n, all.T, all.hq, all.hq / all.g));
+  const AttnArgs a = split_prefill(all, tree_splits(all.n, all.T, all.hq, all.hq / all.g, all.c.D), 2);
   return a.c.D == 64    ? launch_tree_64(a, fmt, s)
          : a.c.D == 128 ? launch_tree_128(a, fmt, s)
                         : launch_tree_256(a, fmt, s);
 }
 
 hipError_t launch_attn_dense(const AttnArgs& all, int fmt, hipStream_t s) {
-  return launch_dense_128(split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq)), fmt,
+  return launch_dense_128(split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq), 4), fmt,
                           s);
 }
 

@@ -156,7 +156,7 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
 // read back, so t / c is split_gain, a constant over the rows of the call.
 __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
   if (a.n_split == 1) return 1;
-  return max(1, min(min(a.n_split, nb >> 2), (int)sqrtf((float)nb * a.split_gain)));
+  return max(1, min(min(a.n_split, nb / a.part_min), (int)sqrtf((float)nb * a.split_gain)));
 }
 
 // what a workgroup's waves tell each other
@@ -795,9 +795,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   }
 }
 
-// Joins the parts of split tiles: a workgroup for each 16 rows of a tile, 16
-// lanes a row, the parts in order.
-template <bool BF, bool F8, int D, int MODE>
+// Joins the parts of split tiles, the parts in order: 16 lanes a row, or Q times as
+// many, every Q-th part to each. Four for trees of more than 16 parts, which are few
+// rows, bound by the chain of their loads (three of 64 parts, 10 heads of 256: the
+// call 44 us against 52); with few parts of many rows they cost (trees of 52..121
+// tokens in two parts 167 us against 151).
+template <bool BF, bool F8, int D, int MODE, int Q>
 __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   constexpr int ROWS = PreShape<D>::ROWS, V = D / 16;
   PreTile t;
@@ -808,8 +811,9 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   if (!pre_span<D, MODE>(a, t)) return;
   const int parts = pre_parts(a, t.nb);
   if (parts == 1) return;
-  const int r = t.tile * ROWS + (int)blockIdx.y * 16 + (threadIdx.x >> 4);
+  const int r = t.tile * ROWS + ((int)blockIdx.y * 16 + (int)(threadIdx.x >> 4)) / Q;
   if (r >= t.rows) return;
+  const int q = (int)(threadIdx.x >> 4) % Q;
   const int d0 = (int)(threadIdx.x & 15) * V, tok = r / a.g, head = kvh * a.g + r - tok * a.g;
   const long rows = a.T * a.hq, ri = ((long)t.q0 + tok) * a.hq + head;
   const float* ml = a.part + (long)a.n_split * rows * D + ri * 2;
@@ -839,7 +843,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   for (int i = 0; i < MP; ++i) {
     const int end = min(16, parts - 16 * i);
 #pragma unroll 4
-    for (int j = 0; j < end; ++j) {
+    for (int j = q; j < end; j += Q) {
       const float f = __shfl(pm[i], j, 16);
       const float* p = a.part + ((long)(16 * i + j) * rows + ri) * D + d0;
 #pragma unroll
@@ -849,6 +853,11 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
         for (int k = 0; k < 4; ++k) acc[e + k] += f * y[k];
       }
     }
+  }
+  if constexpr (Q > 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = xor32_reduce(xor16_reduce(acc[e], OpSum{}), OpSum{});
+    if (q) return;
   }
   const float inv = (F8 ? a.c.vs[kvh] : 1.0f) / l;
   char* dst = a.out + ((long)t.q0 + tok) * a.o_row + head * a.o_head + 2 * d0;
@@ -870,8 +879,12 @@ hipError_t run_prefill(const AttnArgs& all, hipStream_t s) {
     const unsigned grid = (unsigned)(blocks - b < kMaxGrid ? blocks - b : kMaxGrid);
     a.block0 = (int)b;
     attn_prefill_kernel<BF, F8, D, MODE><<<dim3(grid, a.n_split), 256, 0, s>>>(a);
-    if (a.n_split > 1)
-      prefill_join_kernel<BF, F8, D, MODE>
+    constexpr int Q = MODE == kTree ? 4 : 1;
+    if (Q > 1 && a.n_split > 16)
+      prefill_join_kernel<BF, F8, D, MODE, Q>
+          <<<dim3(grid, PreShape<D>::ROWS / 16 * Q), 256, 0, s>>>(a);
+    else if (a.n_split > 1)
+      prefill_join_kernel<BF, F8, D, MODE, 1>
           <<<dim3(grid, PreShape<D>::ROWS / 16), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

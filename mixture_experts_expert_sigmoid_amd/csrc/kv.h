@@ -50,6 +50,7 @@ struct AttnArgs {
   long T;
   int n_split;
   float split_gain;      // see pre_parts
+  int part_min;          // tiles of keys that a part has at least
   int n_tiles;           // of a key-value head
   int block0;            // first of all workgroups that this launch runs
   const int* parent;     // of each row, trees only
