@@ -99,7 +99,6 @@ size_t tree_ws_bytes(long n, long T, int hq, int hkv, int D) {
 namespace {
 AttnArgs split_prefill(const AttnArgs& all, long most, int part_min) {
   AttnArgs a = all;
-  a.part_min = part_min;
   // no more parts than the most keys that a tile can see pay for, so that calls
   // over short tables, or of many rows, need no join
   const long cap = (long)a.t.max_pages * a.t.ps;
@@ -115,22 +114,23 @@ AttnArgs split_prefill(const AttnArgs& all, long most, int part_min) {
 }  // namespace
 
 hipError_t launch_attn_prefill(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq / all.g), 4);
+  const AttnArgs a = split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq / all.g), kPartMin);
   return a.c.D == 64    ? launch_prefill_64(a, fmt, s)
          : a.c.D == 128 ? launch_prefill_128(a, fmt, s)
                         : launch_prefill_256(a, fmt, s);
 }
 
 hipError_t launch_attn_tree(const AttnArgs& all, int fmt, hipStream_t s) {
-  const AttnArgs a = split_prefill(all, tree_splits(all.n, all.T, all.hq, all.hq / all.g, all.c.D), 2);
+  const AttnArgs a = split_prefill(all, tree_splits(all.n, all.T, all.hq, all.hq / all.g, all.c.D),
+                                   kTreePartMin);
   return a.c.D == 64    ? launch_tree_64(a, fmt, s)
          : a.c.D == 128 ? launch_tree_128(a, fmt, s)
                         : launch_tree_256(a, fmt, s);
 }
 
 hipError_t launch_attn_dense(const AttnArgs& all, int fmt, hipStream_t s) {
-  return launch_dense_128(split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq), 4), fmt,
-                          s);
+  return launch_dense_128(split_prefill(all, prefill_splits(all.n, all.T, all.hq, all.hq), kPartMin),
+                          fmt, s);
 }
 
 size_t latent_ws_bytes(int D) {

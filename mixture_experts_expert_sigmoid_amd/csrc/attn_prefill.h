@@ -58,8 +58,8 @@ enum { kCausal, kTree, kDense };
 // split further than a prompt's (tree_splits). Bound by HBM for a batch, by the
 // matrix cores and the codes' expansion for long contexts. Measured: 48 trees of
 // 9..33 tokens over 201..4001 keys, 32 heads over 8 of 128, bf16 (436 MB) 116 us,
-// 3.8 TB/s; two of 41 and 61, 64 heads, over 50..60 k e4m3 keys (217 GFLOP) 260-267
-// us, 0.83 PFLOP/s; one of 8 tokens over 777 keys 15.7 us, latency.
+// 3.8 TB/s; two of 41 and 61, 64 heads, over 50..60 k e4m3 keys (217 GFLOP) 260-270
+// us, 0.82 PFLOP/s; one of 8 tokens over 777 keys 14.6 us, latency.
 // Dense rows (kDense): a group's place is its row, and the loads' own bounds end
 // each sequence, so a ragged batch needs no pages; a key's rotary values are a tile
 // of 64 beside it, read for all heads alike. Two workgroups fill a CU's LDS (2 x 80
@@ -150,13 +150,15 @@ __device__ __forceinline__ bool pre_span(const AttnArgs& a, PreTile& t) {
   return true;
 }
 
-// Parts that a tile's keys are split into: at least four key tiles each, and no
-// more than pay. With nb tiles of a time t, nb t / p + p c is least at p =
+// Parts that a tile's keys are split into: at least four key tiles each (trees:
+// two), and no more than pay. With nb tiles of a time t, nb t / p + p c is least at p =
 // sqrt(nb t / c); the cost c of a part is that of its fp32 rows written and
 // read back, so t / c is split_gain, a constant over the rows of the call.
+template <int MODE>
 __device__ __forceinline__ int pre_parts(const AttnArgs& a, int nb) {
   if (a.n_split == 1) return 1;
-  return max(1, min(min(a.n_split, nb / a.part_min), (int)sqrtf((float)nb * a.split_gain)));
+  constexpr int least = MODE == kTree ? kTreePartMin : kPartMin;
+  return max(1, min(min(a.n_split, nb / least), (int)sqrtf((float)nb * a.split_gain)));
 }
 
 // what a workgroup's waves tell each other
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
   if (!pre_span<D, MODE>(a, t)) return;
-  const int parts = pre_parts(a, t.nb);
+  const int parts = pre_parts<MODE>(a, t.nb);
   if ((int)blockIdx.y >= parts) return;
   const int x0 = (int)((long)blockIdx.y * t.nb / parts);
   const int x1 = (int)((long)(blockIdx.y + 1) * t.nb / parts);
@@ -809,7 +811,7 @@ __global__ __launch_bounds__(256) void prefill_join_kernel(AttnArgs a) {
   t.seq = pre_last(a, [&](int i, int cu) { return (int)((long)cu * a.g / ROWS) + i <= tt; });
   t.tile = tt - (int)((long)pre_cu(a, t.seq) * a.g / ROWS) - t.seq;
   if (!pre_span<D, MODE>(a, t)) return;
-  const int parts = pre_parts(a, t.nb);
+  const int parts = pre_parts<MODE>(a, t.nb);
   if (parts == 1) return;
   const int r = t.tile * ROWS + ((int)blockIdx.y * 16 + (int)(threadIdx.x >> 4)) / Q;
   if (r >= t.rows) return;

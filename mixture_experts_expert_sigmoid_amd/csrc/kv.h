@@ -50,7 +50,6 @@ struct AttnArgs {
   long T;
   int n_split;
   float split_gain;      // see pre_parts
-  int part_min;          // tiles of keys that a part has at least
   int n_tiles;           // of a key-value head
   int block0;            // first of all workgroups that this launch runs
   const int* parent;     // of each row, trees only
@@ -114,6 +113,7 @@ constexpr int kPreRows = 128;
 // tiles that n sequences of T tokens can have, per key-value head
 inline long prefill_tiles(long n, long T, int g) { return T * g / kPreRows + n; }
 constexpr int kPreMaxParts = 64;
+constexpr int kPartMin = 4, kTreePartMin = 2;   // tiles of keys that a part has at least
 int prefill_splits(long n, long T, int hq, int hkv);
 size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D);
 hipError_t launch_attn_prefill(const AttnArgs& a, int fmt, hipStream_t s);
