@@ -166,6 +166,9 @@ CASES = {
     "e4m3_128": ("bf16", "e4m3", 512, 128, 64, "heads", 16, [(200, 1), (63, 2)], None, 0, 0),
     "e4m3_f16": ("f16", "e4m3", 256, 20, 16, "dense", 0, [(33, 7), (290, 3)], None, 0, 0),
     "split_long": ("bf16", "bf16", 512, 16, 64, "dense", 0, [(20010, 1)], None, 0, 0),
+    "split_few": ("f16", "f16", 256, 5, 128, "dense", 0, [(12011, 1), (3001, 2)], None, 0, 0),
+    "split_rows": ("bf16", "bf16", 512, 3, 32, "pad", 0, [(15000, 30)], None, 0, 0),
+    "split_codes": ("bf16", "e4m3", 256, 1, 16, "dense", 0, [(9000, 3), (14001, 1)], star, 0, 0),
     "split_heads": ("bf16", "bf16", 512, 128, 64, "dense", 0, [(5000, 1), (77, 1)], None, 0, 0),
     "split_e4m3": ("f16", "e4m3", 512, 40, 128, "dense", 0, [(9001, 3), (36, 1)], None, 0, 0),
     "tree": ("bf16", "bf16", 512, 8, 16, "dense", 0, [(30, 8), (0, 33), (63, 64)], bushy, 0, 0),

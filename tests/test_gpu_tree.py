@@ -124,6 +124,11 @@ CASES = {
     "split_long": ("bf16", "bf16", 128, 4, 1, 64, "head", "dense", [(20011, 24)], bushy, 0, 0),
     "split_two": ("f16", "e4m3", 128, 16, 2, 128, "tok", "dense", [(9001, 37), (11, 60)], bushy,
                   0, 0),
+    "split_many": ("f16", "f16", 256, 5, 1, 128, "head", "dense", [(9011, 2)], bushy, 0, 0),
+    "split_many_d64": ("bf16", "bf16", 64, 3, 3, 16, "tok", "pad", [(9500, 7), (77, 3)], bushy, 0,
+                       0),
+    "split_many_e4m3": ("bf16", "e4m3", 128, 4, 2, 64, "head", "dense", [(15000, 3), (9000, 1)],
+                        star, 0, 0),
     "mqa_64": ("bf16", "bf16", 128, 64, 1, 16, "head", "dense", [(95, 11), (400, 3)], bushy, 0, 0),
     "window": ("bf16", "bf16", 128, 8, 2, 16, "head", "dense",
                [(1, 20), (100, 30), (1000, 64), (515, 7)], bushy, 64, 4),
