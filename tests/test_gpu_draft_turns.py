@@ -333,6 +333,63 @@ def test_captured_turns():
         assert M.moe_read_device_error(eager[0].err_word) == 0
 
 
+def test_two_streams():
+    """Calls in flight on two streams at once, each with a workspace of its own, and
+    two graphs that share one, replayed in turn: the results of calls by themselves."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n, m, L = 3, 9, 2000
+    a = M.KvCache(n_layers=1, n_pages=400, page_size=16, n_heads=2, head_dim=128, n_slots=n,
+                  max_pages=130)
+    b = M.LatentCache(n_layers=1, n_pages=400, page_size=16, n_slots=n, max_pages=130)
+    for x in (a.k, a.v, b.c):
+        x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+    sl, cu, parent = _i(range(n)), _i(cu_of([m] * n)), _i([-1, 0, 0, 1, 2, 2, 4, 5, 5] * n)
+    for c in (a, b):
+        c.grow(sl, _i([L] * n))
+    q = torch.randn(n * m, 8, 128, generator=gen, device="cuda").bfloat16()
+    ql = torch.randn(n * m, 16, 576, generator=gen, device="cuda").bfloat16()
+    ws = [torch.empty(1 << 27, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    outs = [torch.empty_like(q) for _ in range(2)] + [
+        torch.empty(n * m, 16, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+    def call(i, w):
+        if i < 2:
+            M.moe_attn_tree(a.layers[0], a.desc, q, cu, parent, outs[i], 0.09, a.err_word, w)
+        else:
+            M.moe_attn_latent(b.layers[0], b.desc, ql, cu, outs[i], 0.07, b.err_word, w,
+                              parent=parent)
+
+    for i in range(4):
+        call(i, ws[i])
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                call(i, ws[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    graphs = []
+    for i in (0, 2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i, ws[0])
+        graphs.append(g)
+    for _ in range(3):
+        outs[0].zero_()
+        outs[2].zero_()
+        ws[0].fill_(0xFF)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[2], want[2])
+    assert M.moe_read_device_error(a.err_word) == 0 and M.moe_read_device_error(b.err_word) == 0
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_example(kv):
     path = os.path.join(os.path.dirname(__file__), "..", "examples", "paged_decoder.py")

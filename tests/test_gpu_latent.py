@@ -161,6 +161,8 @@ CASES = {
     "one_head": ("bf16", "bf16", 256, 1, 16, "dense", 0, [(64, 1), (95, 70)], None, 0, 0),
     "prompt": ("bf16", "bf16", 512, 6, 32, "dense", 0, [(0, 77), (0, 1), (0, 33)], None, 0, 0),
     "chunk": ("f16", "f16", 512, 12, 16, "pad", 0, [(200, 19), (63, 40)], None, 0, 0),
+    "heads_1000": ("bf16", "bf16", 256, 1000, 16, "dense", 0, [(40, 2), (3, 1)], None, 0, 0),
+    "heads_1024": ("f16", "f16", 512, 1024, 16, "heads", 0, [(70, 1)], None, 0, 0),
     "odd_heads": ("bf16", "bf16", 512, 33, 16, "dense", 24, [(50, 2), (300, 3)], None, 0, 0),
     "e4m3": ("bf16", "e4m3", 512, 16, 64, "dense", 0, [(200, 1), (62, 1), (512, 1)], None, 0, 0),
     "e4m3_128": ("bf16", "e4m3", 512, 128, 64, "heads", 16, [(200, 1), (63, 2)], None, 0, 0),
