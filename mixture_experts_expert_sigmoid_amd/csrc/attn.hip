@@ -165,7 +165,8 @@ hipError_t launch_attn_latent(const AttnArgs& all, int fmt, hipStream_t s) {
     const long units = tiles * ((long)a.t.max_pages * a.t.ps / 32 + 1 + kLatStart);
     const long want = (units + kLatMinUnits - 1) / kLatMinUnits;
     const int grid = (int)(want < kLatGrid ? want : kLatGrid);
-    a.spread = tiles * kLatFew < grid;
+    a.spread = tiles * kLatFew < grid ? (int)tiles : 0;
+    a.teams = grid;
     a.h_inv = ((1u << 22) + a.hq - 1) / a.hq;
     const hipError_t e = D == 256 ? launch_latent_256(a, fmt, grid, s)
                                   : launch_latent_512(a, fmt, grid, s);

@@ -750,18 +750,17 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
   }
 }
 
-// Joins the parts of the tile that workgroup blockIdx.x of the kernel above left
-// open, in their order. A run is 32 values of 32 rows, 16 values a lane. A wave has
-// one to itself, or, SPREAD, for few tiles of many parts, a workgroup has, every
-// kLatJoin-th part to each wave. Bound by the parts' bytes for batches (50 MB in 13
-// us), by latency else.
+// Joins the parts of the tile that workgroup wg of the kernel above left open, in
+// their order. A run is 32 values of 32 rows, 16 values a lane. A wave has one to
+// itself, or, SPREAD, for few tiles of many parts, a workgroup has, every kLatJoin-th
+// part to each wave. Bound by the parts' bytes for batches (50 MB in 13 us), by
+// latency else.
 constexpr int kLatJoin = 8;
 template <bool BF, bool F8, int DC, bool SPREAD>
-__global__ __launch_bounds__(SPREAD ? 64 * kLatJoin : 256) void latent_join_kernel(AttnArgs a) {
+__device__ __forceinline__ void latent_join(const AttnArgs& a, int wg) {
   constexpr int R = kLatRows, RT = R / 32, NW = SPREAD ? kLatJoin : 1;
   __shared__ f32x4 s_o[NW][4][64];
   __shared__ float s_ml[NW][2][32];
-  const int wg = blockIdx.x;
   const i32x4 meta = *(const i32x4*)(a.meta + 4 * wg);     // q0, rows, first row, parts
   const int cnt = meta[3];
   const int lane = lane_id(), w = threadIdx.x >> 6, l31 = lane & 31, half = lane >> 5;
@@ -846,12 +845,40 @@ __global__ __launch_bounds__(SPREAD ? 64 * kLatJoin : 256) void latent_join_kern
     a.lse[(long)meta[0] * H + g] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// Tiles left open: one for each workgroup of the first launch, or, SPREAD, the few
+// that there are shared out to blockIdx.x. (Of a workgroup for each of 256 that might
+// have left one, times 32 runs, the launch alone took 20 us: one token of 128 heads
+// over 16,812 keys, 45 us of joining then.)
+template <bool BF, bool F8, int DC, bool SPREAD>
+__global__ __launch_bounds__(SPREAD ? 64 * kLatJoin : 256) void latent_join_kernel(AttnArgs a) {
+  if constexpr (!SPREAD) {
+    latent_join<BF, F8, DC, SPREAD>(a, blockIdx.x);
+  } else {
+    constexpr int W = kLatGrid / 64;
+    static_assert(kLatJoin >= W, "a thread for each workgroup of the first launch");
+    __shared__ uint64_t s_open[W];
+    const int tid = threadIdx.x;
+    if (tid < kLatGrid) {
+      const uint64_t open = __ballot(tid < a.teams && a.meta[4 * tid + 3] != 0);
+      if (tid % 64 == 0) s_open[tid / 64] = open;
+    }
+    __syncthreads();
+    int i = 0;
+    for (int k = 0; k < W; ++k)
+      for (uint64_t open = s_open[k]; open; open &= open - 1, ++i)
+        if (i % (int)gridDim.x == (int)blockIdx.x) {
+          latent_join<BF, F8, DC, SPREAD>(a, 64 * k + __builtin_ctzll(open));
+          __syncthreads();                       // its LDS is free again
+        }
+  }
+}
+
 template <bool BF, bool F8, int DC>
 hipError_t run_latent(const AttnArgs& a, int grid, hipStream_t s) {
   attn_latent_kernel<BF, F8, DC><<<grid, 64 * kLatWaves, 0, s>>>(a);
   constexpr unsigned runs = DC / 32 * (kLatRows / 32);
   if (a.spread)
-    latent_join_kernel<BF, F8, DC, true><<<dim3(grid, runs), 64 * kLatJoin, 0, s>>>(a);
+    latent_join_kernel<BF, F8, DC, true><<<dim3(a.spread, runs), 64 * kLatJoin, 0, s>>>(a);
   else
     latent_join_kernel<BF, F8, DC, false><<<dim3(grid, runs / 4), 256, 0, s>>>(a);
   return hipGetLastError();

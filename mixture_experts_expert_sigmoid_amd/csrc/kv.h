@@ -54,7 +54,8 @@ struct AttnArgs {
   int block0;            // first of all workgroups that this launch runs
   const int* parent;     // of each row, trees only
   uint32_t h_inv;        // latent: see lat_token
-  int spread;            // latent: few tiles, many parts of each to be joined
+  int spread;            // latent: tiles, if they are few, with many parts to be joined
+  int teams;             // latent: workgroups of the first launch
   // dense keys (c.k, c.st, c.sh) and values (c.v): rows cu_k[i].. of S, and the
   // values that a key's heads share; strides in bytes
   const int* cu_k;
@@ -137,7 +138,7 @@ constexpr int kLatGrid = 256;           // workgroups, one a CU
 constexpr int kLatSeqs = 128;           // sequences per launch
 constexpr int kLatStart = 7;            // units of 32 keys that a tile's start counts for
 constexpr int kLatFew = 16;             // parts of a tile that a wave by itself joins
-constexpr int kLatMinUnits = 4;         // that a workgroup is there for
+constexpr int kLatMinUnits = 2;         // that a workgroup is there for
 constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
 size_t latent_ws_bytes(int D);
 hipError_t launch_attn_latent(const AttnArgs& a, int fmt, hipStream_t s);
