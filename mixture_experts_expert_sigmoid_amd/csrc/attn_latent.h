@@ -34,7 +34,7 @@
 // of prologue, 5 a piece of start and the parts, 131 KB each, written and read.
 // Measured: a token of 64 sequences of 201..4001 keys, 128 heads (177 MB, 38
 // GFLOP) 80 us, 66 of it this kernel and 13 the join; trees over e4m3 (142 GFLOP)
-// 181 us, 0.78 PFLOP/s; one token of 16 heads over 777 keys 18.8 us, latency. The
+// 181 us, 0.78 PFLOP/s; one token of 16 heads over 777 keys 17.6 us, latency. The
 // first form (four waves, O in the accumulators' half of the registers, waits by
 // the compiler) took 173 us and 294.
 #pragma once
