@@ -64,31 +64,31 @@ __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// Loads of 16 bytes a lane from base + off + at straight into LDS, lane l's to LDS
-// address `to` + 16 l (base, off and to alike in the wave; the offsets below 2^31). In
-// assembly, since the compiler takes loads into one array of LDS for loads into
-// any, and would wait for those in flight wherever LDS is read; they are to be
-// waited for by count (wait_counts), before a barrier if other waves read them. A
-// buffer load: global ones count as flat, and wait_counts would not do.
+// Loads of 16 bytes a lane from base + at straight into LDS, lane l's to LDS address
+// `to` + 16 l (base alike in the wave; at below 2^31); those at offsets from `bytes` on
+// read nothing and write zeros. The whole offset is the lane's: it alone is what the
+// bound is compared with, whatever a scalar offset would do beside it. In assembly,
+// since the compiler takes loads into one array of LDS for loads into any, and would
+// wait for those in flight wherever LDS is read; they are to be waited for by count
+// (wait_counts), before a barrier if other waves read them.
 __device__ __forceinline__ uint32_t lds_of(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
-// Those at offsets from `bytes` on read nothing and write zeros.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"      // (m0 has no value to be preserved)
-__device__ __forceinline__ void load_to_lds(const char* base, uint32_t bytes, int at, int off,
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t bytes, int at,
                                             uint32_t to) {
   auto alike = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); };
   const uint64_t b = (uint64_t)base;
   const u32x4 rsrc = {alike((uint32_t)b), alike((uint32_t)(b >> 32) & 0xFFFFu), alike(bytes),
                       0x00020000u};
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
-               : "s"(alike(to)), "v"(at), "s"(rsrc), "s"(alike(off))
+               : "s"(alike(to)), "v"(at), "s"(rsrc)
                : "memory", "m0");
 }
 
-// The same from an address of each lane's own.
+// The same from an address of each lane's own, without a bound.
 __device__ __forceinline__ void load_lanes_to_lds(const char* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :

@@ -326,10 +326,11 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     auto load = [&](int x, int i) __attribute__((always_inline)) {
       const uint32_t to = lds_of(s_t) + ((x - b0) & 3) * TB;
       if (i < NLD)
-        load_to_lds(src, bytes, here(l_row + (l_unit ^ 16 * swz(i * RPL))), i * RPL * (int)a.c.st,
+        load_to_lds(src, bytes,
+                    here(l_row + (l_unit ^ 16 * swz(i * RPL)) + i * RPL * (int)a.c.st),
                     to + (RPW * w + i * RPL) * RB);
       else if (lane < RPW * URR)
-        load_to_lds(src, bytes, l_rope, 0, to + 32 * RB + RPW * w * RRB);
+        load_to_lds(src, bytes, l_rope, to + 32 * RB + RPW * w * RRB);
     };
     auto issue = [&](int x) __attribute__((always_inline)) {
       const int state = place(x);

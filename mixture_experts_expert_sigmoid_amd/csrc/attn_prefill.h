@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
       if constexpr (F8)
         raw[i] = *(const u32x4*)(p + i * RPL * st + f);
       else
-        load_to_lds(p, bytes, (int)f, i * RPL * (int)st,
+        load_to_lds(p, bytes, (int)(f + i * RPL * (uint32_t)st),
                     lds_of(to) + (w * WR * UPR + i * 64) * 16);
     }
   };
@@ -383,8 +383,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 2 : 3) void attn_pre
       const uint32_t f = lane / 8 * (uint32_t)a.kr_row;
 #pragma unroll
       for (int i = 0; i < 2; ++i)                // eight rows of the wave's 16 each
-        load_to_lds(p, bytes_of(gr, a.kr_row), (int)(f + 16 * (lane % 8 ^ (lane / 16) ^ 4 * i)),
-                    8 * i * (int)a.kr_row, lds_of(to) + TB + (w * WR + 8 * i) * 128);
+        load_to_lds(p, bytes_of(gr, a.kr_row),
+                    (int)(f + 8 * i * (uint32_t)a.kr_row +
+                          16 * (lane % 8 ^ (lane / 16) ^ 4 * i)),
+                    lds_of(to) + TB + (w * WR + 8 * i) * 128);
     }
   };
   auto issue_v = [&](const Group& gr, char* to) {
