@@ -451,8 +451,8 @@ typedef struct {
 #define MOE_DEVERR_CACHE_FULL 0x10 /* grow or fork: not enough free pages or
                                       table entries for a slot, left as it was */
 #define MOE_DEVERR_CACHE_BUSY 0x20 /* fork into a slot that holds tokens, keep
-                                      in a page of several slots: left as it
-                                      was */
+                                      or grow in a page of several slots: left
+                                      as it was */
 #define MOE_DEVERR_TREE 0x40       /* a drafted token whose parent does not come
                                       before it (taken as a child of the
                                       context), a tree of more than
@@ -551,7 +551,8 @@ size_t moe_attn_tree_workspace_size(const moe_kv_cache *cache, long n, long T,
  * 16-byte aligned, strides in elements, multiples of 8. Into a MOE_KV_E4M3
  * cache: code = e4m3fn(round-to-nearest-even(x / scale[head])), the fp32
  * quotient saturated to +-448 (NaN: 0x7F). Positions of different rows must
- * differ. */
+ * differ, and lie in pages that no other slot's table names, as those that
+ * moe_cache_grow gives do. */
 int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
                      const int *slots, const int *start, const int *cu, long n,
                      long T, int fmt, const void *k, long k_stride_row,
@@ -568,7 +569,11 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * where page_size * (entries held) is short. A slot is left as it was, with
  * start[i] = -1 and MOE_DEVERR_CACHE_FULL, if its table row is too short, or
  * if it needs a page and the slots up to it in the list whose rows suffice
- * need more pages in all than are free.
+ * need more pages in all than are free; with MOE_DEVERR_CACHE_BUSY if it ends
+ * inside a page that other entries name too (refs > 1; moe_cache_keep may cut
+ * a slot back to there), where new tokens would be written over theirs. It
+ * needs no pages in that count then. A fork of it goes on in a copy of that
+ * page, and so does the slot itself once no other has the page.
  *
  * moe_cache_free gives the slots' pages back (refs - 1 each, entries -1,
  * len 0), those in entries past the tokens too. (Grow and fork expect none
@@ -595,8 +600,9 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * the context, in every layer; the slot's length follows, and pages left
  * without tokens go back. An entry that is no such path leaves its slot as it
  * was, with MOE_DEVERR_TREE; so does one that would write into a page of
- * another slot too, with MOE_DEVERR_CACHE_BUSY. cu: device int32 [n + 1],
- * within 0..n_path.
+ * another slot too, with MOE_DEVERR_CACHE_BUSY. A path that moves nothing
+ * writes nothing, and may leave the slot's end inside such a page (see
+ * moe_cache_grow). cu: device int32 [n + 1], within 0..n_path.
  *
  * moe_cache_copy_pages copies page src[i] to page dst[i], in every layer;
  * entries < 0 are skipped, entries >= n_pages too, with

@@ -845,7 +845,7 @@ class _PagedCache:
 
     def grow(self, slots, n_new, stream=None):
         """Room for n_new more tokens of each slot; returns their first positions
-        (-1 where there was none)."""
+        (-1 where there was none, or the slot ends inside a page that it shares)."""
         start = self._new(n_new, stream)
         ws = self.workspace(moe_cache_workspace_size(self.desc, n_new.numel()), stream)
         moe_cache_grow(self.desc, slots, n_new, start, self.err_word, ws, stream)

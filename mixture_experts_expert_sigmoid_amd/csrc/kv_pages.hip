@@ -129,8 +129,10 @@ __device__ __forceinline__ int owner_of(const long* incl, int n, long r) {
   return lo;
 }
 
-// one workgroup; bound by latency (a scan of the list, then a step per 8192
-// pages looked at)
+// One workgroup; bound by latency (a scan of the list, then a step per 8192
+// pages looked at). A slot that ends inside a page of another slot too is not let
+// on: its next tokens would be written over the other's (keep leaves such slots,
+// where it cuts back tokens that a fork shares).
 __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* slots,
                                                         const int* n_new, int n, int* start,
                                                         const int* seg_free, int* err) {
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
     const int i = base + threadIdx.x, m = min(n - base, kThreads);
     int slot = -1, L = 0, add = 0;
     long have = 0, need = 0;
-    bool full = false;
+    bool full = false, shared = false;
     if (i < n) {
       slot = kv_slot(slots, i, t.n_slots, err);
       L = kv_len(t, slot);
@@ -152,8 +154,12 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
       if (slot >= 0) {
         have = div_up(L, t.ps);
         const long want = div_up((long)L + add, t.ps);
-        full = want > t.max_pages || (spent && want > have);
-        need = full ? 0 : want - have;
+        if (add > 0 && L % t.ps) {
+          const int e = t.table[slot * t.ld + kv_entry(t, L)];
+          shared = e >= 0 && e < t.n_pages && t.refs[e] > 1;
+        }
+        full = want > t.max_pages || (!shared && spent && want > have);
+        need = full || shared ? 0 : want - have;
       }
     }
     s_slot[threadIdx.x] = slot;
@@ -182,10 +188,10 @@ __global__ __launch_bounds__(kThreads) void grow_kernel(KvTable t, const int* sl
           *e = -1;
         }
       }
-      const bool ok = slot >= 0 && !full;
+      const bool ok = slot >= 0 && !full && !shared;
       start[i] = ok ? L : -1;
       if (ok && add > 0) t.len[slot] = L + add;
-      if (slot >= 0 && full) atomicOr(err, kErrFull);
+      if (slot >= 0 && !ok) atomicOr(err, full ? kErrFull : kErrBusy);
     }
     spent |= found < total;
     __syncthreads();
