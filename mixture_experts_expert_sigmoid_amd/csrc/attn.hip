@@ -67,7 +67,7 @@ constexpr float kSplitGain = 5000;
 // parts per tile so that about 512 workgroups run
 int prefill_splits(long n, long T, int hq, int hkv) {
   const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
-  if (tiles >= 384) return 1;
+  if (tiles < 1 || tiles >= 384) return 1;        // (0: a batch without a sequence)
   const long s = (512 + tiles - 1) / tiles;
   return (int)(s < kPreMaxParts ? s : kPreMaxParts);
 }
@@ -87,6 +87,7 @@ size_t prefill_ws_bytes(long n, long T, int hq, int hkv, int D) {
 // tokens within a window of 907 31.8 against 29.9.
 int tree_splits(long n, long T, int hq, int hkv, int D) {
   const long tiles = prefill_tiles(n, T, hq / hkv) * hkv;
+  if (tiles < 1) return 1;
   const long s = D == 256 ? kTreeParts / 2 / tiles : (kTreeParts + tiles - 1) / tiles;
   return (int)(s < 1 ? 1 : s < kPreMaxParts ? s : kPreMaxParts);
 }
