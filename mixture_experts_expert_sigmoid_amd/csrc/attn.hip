@@ -166,9 +166,9 @@ hipError_t launch_attn_latent(const AttnArgs& all, int fmt, hipStream_t s) {
     const long units = tiles * ((long)a.t.max_pages * a.t.ps / 32 + 1 + kLatStart);
     const long want = (units + kLatMinUnits - 1) / kLatMinUnits;
     const int grid = (int)(want < kLatGrid ? want : kLatGrid);
-    // few tiles, many parts of each: a workgroup a run joins them, else a wave. For 16
-    // parts and more, us: 30 sequences of 16 heads over 1500 keys (8 parts) 39 so, 30 by
-    // waves; 4 of 8 heads over 7..30 k keys (64 parts) 30 and 87.
+    // few tiles, many parts of each: a workgroup a run joins them, else a wave. So / by
+    // waves, us: 30 sequences of 16 heads over 1500 keys (8 parts) 39 / 30; 4 of 8 heads
+    // over 7..30 k keys (64 parts) 30 / 87.
     a.spread = tiles * kLatFew < grid ? (int)tiles : 0;
     a.teams = grid;
     a.h_inv = ((1u << 22) + a.hq - 1) / a.hq;

@@ -5,9 +5,12 @@
 // K Q^T, P = 2^(S - m), O^T = V^T P^T, fp32 but for the 16-bit operands, m
 // followed only when it has grown by 2^kDefer), with one key head of 576 or 320
 // values and g = all query heads: a tile of 64 rows, (token, head) pairs
-// token-major, uses each latent vector 64 times in both products, and a vector
-// is read from memory once, as key and as value. Codes of e4m3 caches are
-// multiplied as they are; the scale goes into the softmax's and the result's.
+// token-major, uses each latent vector 64 times in both products, and reads it once,
+// as key and as value. (With more rows a sequence has more tiles, and each reads the
+// vectors: see Work.) P is rounded to the 16 bits of q, which the matrix instructions
+// take at their rate; results stand up to a third further from the 64-bit values than
+// with P of 32 bits. Codes of e4m3 caches are multiplied as they are; the scale goes
+// into the softmax's and the result's.
 //
 // Layout. O of 64 rows is 128 KB, a quarter of a CU's registers, so a CU holds one
 // workgroup of eight waves: in the second product each has 64 of the 512 values
@@ -25,18 +28,21 @@
 // workgroups, whatever the lengths; a tile's start (places, queries, an empty
 // pipeline: 5 us) counts as kLatStart units of 32 keys. Parts of a tile are
 // joined in order by a second launch. The counts are computed by every workgroup
-// from the lengths, up to kLatSeqs sequences a launch.
+// from the lengths, up to kLatSeqs sequences a launch. The units of a tile come
+// after all of the tile before, so that the tiles of a sequence read the same keys at
+// different times: 128 heads, two tiles a token, miss the L2 for 356 MB of a cache of
+// 177 MB, trees of 64 heads for 571 MB of 60.
 //
 // Bound. A step (32 keys, 64 rows, 4.5 MFLOP) takes 1.25 us, 0.91 PFLOP/s over 256
-// CUs: 37 % of its cycles issue matrix instructions and as many move LDS, and eight
-// waves in step overlap them no better. Reading further ahead, K across the
-// barrier, other places for the loads: no change. Beside the steps there are 2 us
-// of prologue, 5 a piece of start and the parts, 131 KB each, written and read.
-// Measured: a token of 64 sequences of 201..4001 keys, 128 heads (177 MB, 38
-// GFLOP) 80 us, 66 of it this kernel and 13 the join; trees over e4m3 (142 GFLOP)
-// 181 us, 0.78 PFLOP/s; one token of 16 heads over 777 keys 17.6 us, latency. The
-// first form (four waves, O in the accumulators' half of the registers, waits by
-// the compiler) took 173 us and 294.
+// CUs: 37 % of its cycles issue matrix instructions and as many move LDS (28-30 % of
+// them in bank conflicts), and eight waves in step overlap the two no better. Reading further ahead, K across the barrier, other places for the loads:
+// no change. Beside the steps there are 2 us of prologue, 5 a piece of start and
+// the parts, 131 KB each, written and read. Measured: a token of 64 sequences of
+// 201..4001 keys, 128 heads (177 MB, 38 GFLOP) 79-80 us, 66-68 of it this kernel
+// and 13 the join; trees over e4m3 (142 GFLOP) 176-180 us, 0.79-0.80 PFLOP/s; one
+// token of 16 heads over 777 keys 17.7 us, latency. The first form (four waves, O
+// in the accumulators' half of the registers, waits by the compiler) took 173 us
+// and 294.
 #pragma once
 #include <type_traits>
 
@@ -182,7 +188,8 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
     __syncthreads();
   }
   const long U = s_pref[a.n], W = lat_teams(U, gridDim.x);
-  // workgroups next to each other read the same keys: they go to one XCD
+  // workgroups next to each other go on along a tile or have the next one of the same
+  // sequence, which reads the same keys, if later: they go to one XCD (L2 hits of 18-20 %)
   const int wg = W > 128 && gridDim.x % 8 == 0
                      ? (int)(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8)
                      : (int)blockIdx.x;
@@ -205,7 +212,10 @@ __global__ __launch_bounds__(64 * kLatWaves, 2) void attn_latent_kernel(AttnArgs
 
   // Swizzles: the 16-byte units of a row lie turned by its number, so that what is
   // read at a time -- the same unit of 16 rows (K, P), the next four units of four
-  // rows or the next two of eight (V, transposed) -- lies in different banks.
+  // rows or the next two of eight (V, transposed) -- lies in different places of 256
+  // bytes. Not so of 128: rows r and r + 2 of K (codes: r + 4) are that far apart, and
+  // 28-30 % of the active cycles of LDS go to conflicts, where the prompts' kernels,
+  // whose turn is the row's number, have 1-2 %.
   auto swz = [](int r) {
     return F8 ? (r & 7) << 1 | (r >> 3 & 1) : (r & 3) << 2 | (r >> 2 & 3);
   };

@@ -57,14 +57,17 @@ enum { kCausal, kTree, kDense };
 // them are whole, so that the tree costs a mask in the last ones. The keys are
 // split further than a prompt's (tree_splits). Bound by HBM for a batch, by the
 // matrix cores and the codes' expansion for long contexts. Measured: 48 trees of
-// 9..33 tokens over 201..4001 keys, 32 heads over 8 of 128, bf16 (436 MB) 116 us,
-// 3.8 TB/s; two of 41 and 61, 64 heads, over 50..60 k e4m3 keys (217 GFLOP) 260-270
-// us, 0.82 PFLOP/s; one of 8 tokens over 777 keys 14.6 us, latency.
+// 9..33 tokens over 201..4001 keys, 32 heads over 8 of 128, bf16 (436 MB) 108-118 us,
+// 3.7-4.0 TB/s; two of 41 and 61, 64 heads, over 50..60 k e4m3 keys (217 GFLOP) 260-277
+// us, 0.79-0.84 PFLOP/s; one of 8 tokens over 777 keys 14.2-14.7 us, latency.
 // Dense rows (kDense): a group's place is its row, and the loads' own bounds end
 // each sequence, so a ragged batch needs no pages; a key's rotary values are a tile
 // of 64 beside it, read for all heads alike. Two workgroups fill a CU's LDS (2 x 80
-// KB). Bound by the matrix cores: 6001 tokens of 32 heads (369 GFLOP) 382-385 us,
-// 0.96 PFLOP/s; three prompts of 17..130 tokens of 16 heads 11.8 us, latency.
+// KB). Bound by the matrix cores: 6001 tokens of 32 heads (369 GFLOP) 372-397 us from
+// one card to the next, 0.93-0.99 PFLOP/s; three prompts of 17..130 tokens of 16 heads
+// 11.5-11.8 us, latency. Dealt out by tiles, all at once: where they are few and long, a
+// CU with a long one and its part has twice the average (1689 tokens of 16 heads 44 us,
+// ten prompts of 553..1574 of 3 heads 52).
 
 // keys of a tile, rows of a workgroup's tile
 template <int D>

@@ -137,10 +137,13 @@ constexpr int kLatWaves = 8;            // of a workgroup
 constexpr int kLatGrid = 256;           // workgroups, one a CU
 constexpr int kLatSeqs = 128;           // sequences per launch
 constexpr int kLatStart = 7;            // units of 32 keys that a tile's start counts for
-constexpr int kLatFew = 16;             // parts of a tile that a wave by itself joins
-// units that a workgroup is there for; with 1 / 2 / 3 / 4 / 6, us: one token of 16
+// Parts of a tile that a wave by itself joins; measured on either side of it, with 8
+// and 64 of them (launch_attn_latent), not near it.
+constexpr int kLatFew = 16;
+// Units that a workgroup is there for; with 1 / 2 / 3 / 4 / 6, us: one token of 16
 // heads over 777 keys 16.5 / 18.0 / 18.6 / 19.1 / 21.3, of 4 sequences over 2400 e4m3
-// keys 26.0 / 23.0 / 22.4 / 22.8 / 24.4
+// keys 26.0 / 23.0 / 22.4 / 22.8 / 24.4. The best for neither, and within a tenth of it
+// for both.
 constexpr int kLatMinUnits = 2;
 constexpr long lat_part_floats(int D) { return (long)kLatRows * (D + 2); }
 size_t latent_ws_bytes(int D);

@@ -9,8 +9,8 @@
 // kernel. 8 rows a workgroup and 4
 // loads in flight: 16 rows, 4 rows, 8 or 2 loads were all slower (8: 67 us).
 // Rows of a latent cache (a vector and its rotary key, one head, one scale) go the
-// same way: 36,000 of them into an e4m3 cache (63 MB) 17.5 us, 3.6 TB/s, a token of
-// each of 64 sequences 7.2 us a call, 3.7 us of it the kernel.
+// same way: 36,000 of them into an e4m3 cache (63 MB) 17.5-18.4 us, 3.4-3.6 TB/s, a
+// token of each of 64 sequences 6.5-7.2 us a call, 3.6 us of it the kernel.
 #include "common.h"
 #include "kv.h"
 

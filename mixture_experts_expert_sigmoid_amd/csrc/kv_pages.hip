@@ -12,7 +12,7 @@
 //
 // Measured: free, trim, grow and fork for 96 slots of a pool of 4096 pages 24
 // us for the four calls, launches and their latencies (2.7, 3.5, 7.3 and 9.5 us
-// on the GPU); compaction of 1.07 GB of pages, read and written, 216 us, and
+// on the GPU; that grow looks at the last page's count shows in no figure); compaction of 1.07 GB of pages, read and written, 216 us, and
 // copy_pages of 2.15 GB 429 us, 5.0 TB/s, the rate of a large copy.
 #include "kv.h"
 
@@ -418,10 +418,9 @@ hipError_t copy_all(const CopyLayers* cl, int n_cl, const int* from, const int* 
 // -------------------------------------------------------------------- keep
 // The accepted path of a tree of drafted tokens: its j-th token, the a_j-th
 // drafted one, goes to place j behind the C tokens of context. a is ascending,
-// so a_j >= j: no token goes to the place of a later one of the path, and a
-// thread that has read a batch of tokens before it writes them, in the path's
-// order, has read every place before it is written. A thread keeps to its 16
-// bytes of a token, so nothing else is to be ordered.
+// so a_j >= j, and a token's place lies behind those already written: moved one
+// by one in the path's order, each is read before it is overwritten. A thread keeps
+// to its 16 bytes of every token, so nothing is to be ordered between threads.
 //
 // A slot that is to be kept gets its new length with the sign bit set from the
 // copy's first workgroup for it, and without from the launch after the copies:
@@ -483,10 +482,9 @@ __device__ bool path_of(const KeepArgs& a, long i, bool tell, Path& p) {
 constexpr int kKeepTokens = 64;         // of a path, found at a time
 
 // Workgroup (i, y): 256 of the 16-byte columns that all arrays' tokens have, of
-// entry i. A path rises, so an entry's token is behind the places written
-// before it, and in order each is read before it is overwritten. One token
-// after the other: the workgroups of a large batch cover each other's latency,
-// and 2, 4, 8 or 16 loads of a thread in flight took longer, with 256 paths of
+// entry i. One token after the other: the workgroups of a large batch cover each
+// other's latency, and 2, 4, 8 or 16 loads of a thread in flight (each batch read
+// before it is written) took longer, with 256 paths of
 // up to 12 tokens in 8 layers (93 MB) 39, 38, 48 and 51 us against 29 (copies
 // that put the lengths back included), and no less with 1 to 64 paths of up to
 // 60. For a step's few tokens the time is that of finding the places (slot ->
