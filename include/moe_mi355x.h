@@ -569,10 +569,10 @@ int moe_cache_append(const moe_kv_cache *cache, const moe_kv_table *table,
  * where page_size * (entries held) is short. A slot is left as it was, with
  * start[i] = -1 and MOE_DEVERR_CACHE_FULL, if its table row is too short, or
  * if it needs a page and the slots up to it in the list whose rows suffice
- * need more pages in all than are free; with MOE_DEVERR_CACHE_BUSY if it ends
- * inside a page that other entries name too (refs > 1; moe_cache_keep may cut
- * a slot back to there), where new tokens would be written over theirs. It
- * needs no pages in that count then. A fork of it goes on in a copy of that
+ * need more pages in all than are free; with MOE_DEVERR_CACHE_BUSY if it is to
+ * get tokens (n_new[i] > 0) and ends inside a page that other entries name too
+ * (refs > 1; moe_cache_keep may cut a slot back to there), where they would be
+ * written over theirs. It needs no pages in that count then. A fork of it goes on in a copy of that
  * page, and so does the slot itself once no other has the page.
  *
  * moe_cache_free gives the slots' pages back (refs - 1 each, entries -1,
